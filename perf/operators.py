@@ -193,10 +193,10 @@ def _own(s):
         return tq.tq_linear_epilogue_backward(s["dy"], s["z"], act=c["act"])
     t = c["temperature"]
     if op == "distill":
-        loss, lse, lse_rest = tq.tq_topk_distill(s["logits"], s["idx"], s["val"], temperature=t,
-                                                 teacher_lse=s["teacher_lse"])
-        return loss, tq.tq_topk_distill_backward(s["logits"], s["idx"], s["val"], lse, s["dloss"], temperature=t,
-                                                 teacher_lse=s["teacher_lse"], lse_rest=lse_rest)
+        loss, stats, rest_sum = tq.tq_topk_distill(s["logits"], s["idx"], s["val"], temperature=t,
+                                                   teacher_lse=s["teacher_lse"])
+        return loss, tq.tq_topk_distill_backward(s["logits"], s["idx"], s["val"], stats, s["dloss"], temperature=t,
+                                                 teacher_lse=s["teacher_lse"], rest_sum=rest_sum)
     return tq.tq_topk_distill_grad(s["logits"], s["idx"], s["val"], dloss=s["dloss"], temperature=t,
                                    teacher_lse=s["teacher_lse"])
 
