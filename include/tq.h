@@ -17,7 +17,11 @@
  *     dynamic-range quantization by mode and scope,
  *   - integer codes of binary64 inputs computed in binary64,
  *   - the GEMMs that consume the codes: the W8A8 quantized linear, the FP4
- *     weight-only linear and the block-scaled FP8 GEMM.
+ *     weight-only linear and the block-scaled FP8 GEMM,
+ *   - what stands around a quantized layer: layer norm (forward, fused with
+ *     the per-token quantizer, backward), the W8A8 product with bias,
+ *     activation and residual in its epilogue and that epilogue's backward,
+ *     and the distillation loss of a student against its teacher's top logits.
  *
  * Sources (page titles and sections):
  *   [Q]  docs.rs baracuda_kernels::quantize -- module overview (dtype
@@ -91,6 +95,7 @@ typedef enum { TQ_NVFP4 = 0, TQ_MXFP4 = 1 } tq_fp4_kind;
 typedef enum { TQ_RANGE_SYMMETRIC = 0, TQ_RANGE_ASYMMETRIC = 1 } tq_range_mode;
 typedef enum { TQ_GRAN_TENSOR = 0, TQ_GRAN_CHANNEL = 1, TQ_GRAN_TOKEN = 2, TQ_GRAN_GROUP = 3 } tq_granularity;
 typedef enum { TQ_SCOPE_TENSOR = 0, TQ_SCOPE_TOKEN = 1, TQ_SCOPE_CHANNEL = 2 } tq_range_scope;
+typedef enum { TQ_ACT_NONE = 0, TQ_ACT_RELU = 1, TQ_ACT_SILU = 2, TQ_ACT_GELU = 3, TQ_ACT_GELU_TANH = 4 } tq_act;
 
 /* Version of this ABI (bumped on any signature change). */
 int tq_abi_version(void);
@@ -550,6 +555,125 @@ tq_status tq_fp4_concat_rows(const uint8_t* packed1, const uint8_t* block_scale1
 tq_status tq_fp4_predequant_to_fp8(const uint8_t* packed, const uint8_t* block_scale,
                                    float host_global_scale, int64_t rows, int64_t k, int kind,
                                    uint8_t* fp8_out, void* stream);
+
+/* ===================================================================== */
+/* Around a quantized layer: norm, epilogue, distillation                 */
+/* ===================================================================== */
+/*
+ * These calls take every pointer at its type's natural alignment
+ * (TQ_ERR_ALIGN otherwise) and row strides in elements; the widest accesses
+ * need no more.  All statistics and sums are binary32; every output is rounded
+ * once.  Results do not depend on the launch: no sum's order is left to
+ * atomics.  NaN and infinities go through as IEEE arithmetic takes them unless
+ * stated otherwise.
+ */
+
+/* Layer norm over the last dimension of x [rows, cols] (row r starts
+ * x_row_stride elements after row r - 1):
+ *   mu = sum_j x_j / cols,  v = sum_j (x_j - mu)^2 / cols,  r = 1 / sqrt(v + eps)
+ *   y_j = ((x_j - mu) * r) * weight_j + bias_j
+ * The variance is taken around the mean.  weight and bias (each may be NULL:
+ * ones, zeros) have type w_dtype; y is dense in x's type; mean and rstd
+ * [rows] (binary32, each may be NULL) are what the backward pass needs.
+ * eps >= 0.  rows and cols up to 2^31 - 1 (TQ_ERR_UNSUPPORTED beyond). */
+tq_status tq_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t x_row_stride,
+                        const void* weight, const void* bias, int w_dtype, float eps, void* y, float* mean,
+                        float* rstd, void* stream);
+
+/* Layer norm and the per-token s8 quantizer in one pass: q [rows, cols] and
+ * scale [rows] are, bit for bit, those of tq_quant_per_token (TQ_S8,
+ * [-127, 127], symmetric) on tq_layer_norm's y. */
+tq_status tq_layer_norm_quant_per_token(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t x_row_stride,
+                                        const void* weight, const void* bias, int w_dtype, float eps, int8_t* q,
+                                        float* scale, float* mean, float* rstd, void* stream);
+
+/* Layer norm backward from the saved x, mean and rstd.  With g = dy * weight
+ * and h = (x - mean) * rstd:
+ *   dx = rstd * (g - sum_j(g) / cols - h * sum_j(g h) / cols)
+ *   dweight_j = sum_rows dy h,   dbias_j = sum_rows dy
+ * dy and dx (dense) have x's type, dweight and dbias w_dtype; each output may
+ * be NULL.  With no rows dweight and dbias are zeros.  `workspace` (needed for
+ * dweight or dbias): tq_layer_norm_backward_workspace_bytes(rows, cols) bytes,
+ * 16-byte aligned, contents ignored. */
+size_t tq_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+tq_status tq_layer_norm_backward(const void* dy, const void* x, int x_dtype, int64_t rows, int64_t cols,
+                                 int64_t dy_row_stride, int64_t x_row_stride, const void* weight, int w_dtype,
+                                 const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* The W8A8 product with an epilogue, for any M (single tokens included), N
+ * and K <= 131071.  qx, sx, qw, sw as in tq_w8a8_linear:
+ *   z[m][n] = ((float)sum_k qx[m][k] * qw[n][k] * sx[m]) * sw[n] + bias[n]
+ *   y[m][n] = act(z[m][n]) + residual[m][n]
+ * in binary32, in that order, y rounded once to y_dtype; without bias, act and
+ * residual the bits are tq_w8a8_linear's.  act (tq_act): none, relu, silu
+ * z / (1 + exp(-z)), gelu z * Phi(z), or its tanh form.  bias [N] (bias_dtype)
+ * and residual [M, N] (y_dtype, row stride residual_row_stride) may be NULL;
+ * preact, if not NULL, gets z rounded to y_dtype, for the backward pass.  y and
+ * preact are dense and overlap no input; y may be the residual itself (same
+ * address, stride N).  Operands whose rows start at 16-byte addresses (base and
+ * K) take the fastest kernels. */
+tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_t* qw, const float* sw, int64_t M,
+                                  int64_t N, int64_t K, const void* bias, int bias_dtype, int act,
+                                  const void* residual, int64_t residual_row_stride, void* y, void* preact,
+                                  int y_dtype, void* stream);
+
+/* Backward of that epilogue: dz = dy * act'(preact) (dense [M, N], all in
+ * dtype) and dbias[n] = sum_m of the dz before its rounding (binary32 [N], may
+ * be NULL; zeros when M is 0).  The residual's gradient is dy.  dz may be dy or
+ * preact itself.  relu's slope at 0 is 0.  `workspace` (needed for dbias):
+ * tq_linear_epilogue_backward_workspace_bytes(M, N) bytes, 16-byte aligned. */
+size_t tq_linear_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
+tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dtype, int64_t M, int64_t N, int act,
+                                      void* dz, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation against a teacher's top logits.  Student logits [rows, vocab]
+ * (row stride row_stride); top_idx [rows, k] (32- or 64-bit integers:
+ * idx_bits) and top_val [rows, k] (val_dtype) are the teacher's k largest
+ * logits of each row, k <= 1024.  An index outside [0, vocab) (-1, say) is a
+ * padding entry and counts nowhere; a row without entries has loss 0 and
+ * gradient 0, whatever its logits hold.  With s = 1 / temperature:
+ *   log q_j = s z_j - log sum_i exp(s z_i)
+ *   teacher_lse == NULL: p = softmax(s top_val) over the row's entries, and
+ *     loss = sum_k p_k (log p_k - log q_(i_k))
+ *     dlogits_j = dloss s (q_j - p_j)              (p_j = 0 off the entries)
+ *   teacher_lse [rows] (log-sum-exp of all the teacher's s * logits): p_k =
+ *     exp(s top_val_k - teacher_lse), and the rest of the vocabulary is one
+ *     more outcome, p_r = max(0, 1 - sum p) against q_r, q's mass outside the
+ *     entries (summed there, not taken as a difference):
+ *     loss = sum_k p_k (log p_k - log q_(i_k)) + p_r (log p_r - log q_r)
+ *     dlogits_j = dloss s (q_j Z - p_j) at entries, dloss s q_j (Z - p_r / q_r)
+ *     elsewhere, Z = sum p + p_r.
+ * An outcome with p = 0 adds nothing.  Logits of -inf are tokens that cannot be
+ * drawn (gradient 0; the loss is +inf where the teacher gives them mass); a row
+ * of nothing but -inf has gradient 0 and, if it has entries, loss +inf.
+ * Entries that repeat a column count each, and its gradient takes their sum.
+ * loss [rows]; no reduction and no factor T^2 are applied.  temperature > 0.
+ *
+ * tq_topk_distill writes the loss and what the backward pass needs: stats
+ * [rows, 2] = the row's largest logit and the sum of exp(s (z - it)), rest_sum
+ * [rows] the same sum outside the entries (only with teacher_lse); both may be
+ * NULL.  tq_topk_distill_backward turns dloss [rows] (NULL: ones) into dlogits
+ * (logits' type, row stride d_row_stride).  tq_topk_distill_grad does both in
+ * one call, for a program that knows dloss beforehand: where a workgroup can
+ * hold a row, the logits are read once.  dlogits may be the logits themselves
+ * (same address and stride).  `workspace`: tq_topk_distill_workspace_bytes(rows,
+ * vocab) bytes, 16-byte aligned, contents ignored. */
+size_t tq_topk_distill_workspace_bytes(int64_t rows, int64_t vocab);
+tq_status tq_topk_distill(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                          const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
+                          const float* teacher_lse, float temperature, float* loss, float* stats, float* rest_sum,
+                          void* workspace, size_t workspace_bytes, void* stream);
+tq_status tq_topk_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                   const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
+                                   const float* teacher_lse, float temperature, const float* stats,
+                                   const float* rest_sum, const float* dloss, void* dlogits, int64_t d_row_stride,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+tq_status tq_topk_distill_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                               const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
+                               const float* teacher_lse, float temperature, const float* dloss, float* loss,
+                               void* dlogits, int64_t d_row_stride, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 #ifdef __cplusplus
 }

@@ -34,12 +34,14 @@ FTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 CODE = {"s8": 0, "u8": 1, "s4": 2, "u4": 3}
 FP4_KIND = {"nvfp4": 0, "mxfp4": 1}
 FP4_GROUP = {"nvfp4": 16, "mxfp4": 32}
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 _SHAPE = ctypes.POINTER(ctypes.c_int64)
 
 _SIGS = {
@@ -95,6 +97,19 @@ _SIGS = {
     "tq_dequant_mxfp8": ([_P, _P, _I64, _I64, _P, _I, _P], _I),
     "tq_quant_mxfp8_backward": ([_P, _I, _P, _I64, _I64, _P, _P, _P], _I),
     "tq_dequant_mxfp8_backward": ([_P, _I, _P, _I64, _I64, _P, _P], _I),
+    "tq_layer_norm": ([_P, _I, _I64, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P], _I),
+    "tq_layer_norm_quant_per_token": ([_P, _I, _I64, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P], _I),
+    "tq_layer_norm_backward_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_layer_norm_backward": ([_P, _P, _I, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "tq_w8a8_linear_epilogue": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I, _P, _I64, _P, _P, _I, _P], _I),
+    "tq_linear_epilogue_backward_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_linear_epilogue_backward": ([_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _SZ, _P], _I),
+    "tq_topk_distill_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_topk_distill": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _P, _SZ, _P], _I),
+    "tq_topk_distill_backward": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _P, _I64, _P,
+                                  _SZ, _P], _I),
+    "tq_topk_distill_grad": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _I64, _P, _SZ, _P],
+                             _I),
     "tq_stream_mix": ([_P, _P, _I64, _I, _I, _I, _I, _P], _I),
 }
 
@@ -786,3 +801,220 @@ def tq_fp4_linear(x, packed, block_scale, global_scale, kind="nvfp4", out_dtype=
           _ptr(global_scale) if global_scale is not None else None, FP4_KIND[kind], M, N, K, _ptr(y), FTYPE[out_dtype],
           _stream(x.device))
     return y
+
+
+# ------------------------------------------------------------------ layer norm
+def _rows_of(t, name):
+    """(rows, cols, row stride) of t viewed as [rows, cols], its leading
+    dimensions flattened; copies t only where they do not flatten."""
+    _ft(t)
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dim() == 0:
+        raise ValueError("%s needs at least one dimension" % name)
+    cols = t.shape[-1]
+    if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < cols):
+        if not t.is_contiguous():
+            t = t.contiguous()
+        return t, (t.numel() // cols if cols else 0), cols, cols
+    return t, t.shape[0], cols, t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _params(x, cols, weight, bias):
+    """The parameters' common type; the tensors checked against the row."""
+    dt = None
+    for name, p in (("weight", weight), ("bias", bias)):
+        if p is None:
+            continue
+        if p.device != x.device or p.shape != (cols,):
+            raise ValueError("%s must be a vector of %d elements on x's device" % (name, cols))
+        if dt is not None and p.dtype != dt:
+            raise ValueError("weight and bias must have one type")
+        dt = p.dtype
+    if dt is not None and dt not in FTYPE:
+        raise TypeError("unsupported float dtype %s" % dt)
+    return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous(),
+            FTYPE[dt if dt is not None else torch.float32])
+
+
+def _row_vector(t, rows, x, name):
+    if t.dtype != torch.float32 or t.numel() != rows or t.device != x.device:
+        raise ValueError("%s must be float32 with one value per row, on the input's device" % name)
+    return t.contiguous()
+
+
+def tq_layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """Layer norm over the last dimension: (y, mean, rstd), y in x's type and
+    shape, mean and rstd float32 with one value per row."""
+    xr, rows, cols, ld = _rows_of(x, "x")
+    w, b, wdt = _params(x, cols, weight, bias)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+    mean, rstd = stats[0], stats[1]
+    _call("tq_layer_norm", _ptr(xr), _ft(x), rows, cols, ld, _ptr(w), _ptr(b), wdt, eps, _ptr(y), _ptr(mean),
+          _ptr(rstd), _stream(x.device))
+    return y, mean, rstd
+
+
+def tq_layer_norm_quant_per_token(x, weight=None, bias=None, eps=1e-5, stats=False):
+    """Layer norm and the symmetric per-token s8 quantizer in one pass: int8
+    codes of x's shape and one scale per row; with ``stats`` also mean and
+    rstd, for the backward pass."""
+    xr, rows, cols, ld = _rows_of(x, "x")
+    w, b, wdt = _params(x, cols, weight, bias)
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    kept = torch.empty((2, rows), dtype=torch.float32, device=x.device) if stats else None
+    _call("tq_layer_norm_quant_per_token", _ptr(xr), _ft(x), rows, cols, ld, _ptr(w), _ptr(b), wdt, eps, _ptr(q),
+          _ptr(scale), _ptr(kept[0]) if stats else None, _ptr(kept[1]) if stats else None, _stream(x.device))
+    return (q, scale, kept[0], kept[1]) if stats else (q, scale)
+
+
+def tq_layer_norm_backward(dy, x, weight, mean, rstd, param_dtype=None):
+    """(dx, dweight, dbias) of tq_layer_norm from the saved x, mean and rstd;
+    dx in x's type and shape, the parameters' gradients in the weight's type
+    (``param_dtype``, float32 by default, where the weight is None)."""
+    if dy.dtype != x.dtype or dy.shape != x.shape or dy.device != x.device:
+        raise ValueError("dy must have x's dtype, shape and device")
+    xr, rows, cols, ldx = _rows_of(x, "x")
+    dyr, _, _, ldy = _rows_of(dy, "dy")
+    w, _, wdt = _params(x, cols, weight, None)
+    pdt = weight.dtype if weight is not None else (param_dtype or torch.float32)
+    mean, rstd = _row_vector(mean, rows, x, "mean"), _row_vector(rstd, rows, x, "rstd")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    grads = torch.empty((2, cols), dtype=pdt, device=x.device)
+    nws = _lib.tq_layer_norm_backward_workspace_bytes(rows, cols)
+    ws = torch.empty((max(1, nws),), dtype=torch.uint8, device=x.device)
+    _call("tq_layer_norm_backward", _ptr(dyr), _ptr(xr), _ft(x), rows, cols, ldy, ldx, _ptr(w), FTYPE[pdt], _ptr(mean),
+          _ptr(rstd), _ptr(dx), _ptr(grads[0]), _ptr(grads[1]), _ptr(ws), nws, _stream(x.device))
+    return dx, grads[0], grads[1]
+
+
+def tq_layer_norm_backward_workspace_bytes(rows, cols):
+    return int(_lib.tq_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+# ------------------------------------------------ W8A8 product with an epilogue
+def _codes(t, name):
+    if t.dtype not in (torch.int8, torch.uint8) or t.dim() != 2 or not t.is_cuda:
+        raise TypeError("%s must be a 2-D CUDA (HIP) tensor of s8 codes" % name)
+    return t.contiguous()
+
+
+def tq_w8a8_linear_epilogue(qx, sx, qw, sw, bias=None, act="none", residual=None, out_dtype=torch.bfloat16,
+                            preact=False):
+    """y = act(x W^T + bias) + residual from s8 activation codes qx [M, K]
+    (per-row scales sx) and s8 weight codes qw [N, K] (per-channel scales sw);
+    with ``preact`` also the value before the activation, for
+    tq_linear_epilogue_backward."""
+    qx, qw = _codes(qx, "qx"), _codes(qw, "qw")
+    M, K = qx.shape
+    N = qw.shape[0]
+    if qw.shape[1] != K or qw.device != qx.device:
+        raise ValueError("qx and qw must share K and their device")
+    sx, sw = _row_vector(sx, M, qx, "sx"), _row_vector(sw, N, qx, "sw")
+    _, b, bdt = _params(qx, N, None, bias)
+    ldr = N
+    if residual is not None:
+        if residual.shape != (M, N) or residual.dtype != out_dtype or residual.device != qx.device:
+            raise ValueError("residual must be [M, N] in the output's type, on qx's device")
+        residual, _, _, ldr = _rows_of(residual, "residual")
+    y = torch.empty((M, N), dtype=out_dtype, device=qx.device)
+    z = torch.empty((M, N), dtype=out_dtype, device=qx.device) if preact else None
+    _call("tq_w8a8_linear_epilogue", _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), M, N, K, _ptr(b), bdt, ACT[act],
+          _ptr(residual), ldr, _ptr(y), _ptr(z), FTYPE[out_dtype], _stream(qx.device))
+    return (y, z) if preact else y
+
+
+def tq_linear_epilogue_backward(dy, preact, act="none"):
+    """(dz, dbias) of the epilogue: dz = dy * act'(preact) in dy's type, dbias
+    its float32 column sums (before dz is rounded)."""
+    if dy.dim() != 2 or preact.shape != dy.shape or preact.dtype != dy.dtype or preact.device != dy.device:
+        raise ValueError("dy and preact must be [M, N] of one type on one device")
+    dy, preact = _dev_float(dy, "dy"), _dev_float(preact, "preact")
+    M, N = dy.shape
+    dz = torch.empty_like(dy)
+    dbias = torch.empty((N,), dtype=torch.float32, device=dy.device)
+    nws = _lib.tq_linear_epilogue_backward_workspace_bytes(M, N)
+    ws = torch.empty((max(1, nws),), dtype=torch.uint8, device=dy.device)
+    _call("tq_linear_epilogue_backward", _ptr(dy), _ptr(preact), _ft(dy), M, N, ACT[act], _ptr(dz), _ptr(dbias),
+          _ptr(ws), nws, _stream(dy.device))
+    return dz, dbias
+
+
+def tq_linear_epilogue_backward_workspace_bytes(M, N):
+    return int(_lib.tq_linear_epilogue_backward_workspace_bytes(M, N))
+
+
+# ------------------------------------------- distillation from the top logits
+def _distill_args(logits, top_idx, top_val, teacher_lse):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    if top_idx.dtype not in (torch.int32, torch.int64):
+        raise TypeError("top_idx must be int32 or int64")
+    _ft(top_val)
+    z, rows, vocab, ld = _rows_of(logits, "logits")
+    if top_idx.dim() != 2 or top_idx.shape[0] != rows or top_val.shape != top_idx.shape:
+        raise ValueError("top_idx and top_val must be [rows, k]")
+    if top_idx.device != logits.device or top_val.device != logits.device:
+        raise ValueError("top_idx and top_val must be on the logits' device")
+    if teacher_lse is not None:
+        teacher_lse = _row_vector(teacher_lse, rows, logits, "teacher_lse")
+    nws = _lib.tq_topk_distill_workspace_bytes(rows, vocab)
+    ws = torch.empty((max(1, nws),), dtype=torch.uint8, device=logits.device)
+    idx, val = top_idx.contiguous(), top_val.contiguous()
+    head = (_ptr(z), _ft(logits), rows, vocab, ld, _ptr(idx), 32 if idx.dtype == torch.int32 else 64, _ptr(val),
+            _ft(val), idx.shape[1], _ptr(teacher_lse))
+    return head, (z, idx, val, teacher_lse), rows, vocab, ws, nws
+
+
+def tq_topk_distill(logits, top_idx, top_val, temperature=1.0, teacher_lse=None):
+    """Per-row loss of student logits [rows, vocab] against the teacher's top
+    logits (top_idx, top_val [rows, k]; index -1 pads).  With ``teacher_lse``
+    (log-sum-exp of the teacher's logits / temperature) the rest of the
+    vocabulary counts as one more outcome; without, the teacher's
+    probabilities are normalised over its entries.  Returns (loss, stats,
+    rest_sum), the latter two for tq_topk_distill_backward."""
+    head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
+    dev = logits.device
+    loss = torch.empty((rows,), dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    rest = torch.empty((rows,), dtype=torch.float32, device=dev) if teacher_lse is not None else None
+    _call("tq_topk_distill", *head, temperature, _ptr(loss), _ptr(stats), _ptr(rest), _ptr(ws), nws, _stream(dev))
+    return loss, stats, rest
+
+
+def tq_topk_distill_backward(logits, top_idx, top_val, stats, dloss=None, temperature=1.0, teacher_lse=None,
+                             rest_sum=None):
+    """dlogits of tq_topk_distill from its inputs and statistics; ``dloss``
+    [rows] is the gradient of the losses (ones by default)."""
+    head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
+    if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != logits.device:
+        raise ValueError("stats must be tq_topk_distill's [rows, 2]")
+    if (teacher_lse is None) != (rest_sum is None):
+        raise ValueError("rest_sum goes with teacher_lse")
+    stats = stats.contiguous()
+    rest_sum = None if rest_sum is None else _row_vector(rest_sum, rows, logits, "rest_sum")
+    dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
+    dz = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    _call("tq_topk_distill_backward", *head, temperature, _ptr(stats), _ptr(rest_sum), _ptr(dloss), _ptr(dz), vocab,
+          _ptr(ws), nws, _stream(logits.device))
+    return dz
+
+
+def tq_topk_distill_grad(logits, top_idx, top_val, dloss=None, temperature=1.0, teacher_lse=None, inplace=False):
+    """(loss, dlogits) in one call, for a program that knows ``dloss`` (ones by
+    default) beforehand; ``inplace`` writes the gradient over the logits."""
+    head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
+    dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
+    loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
+    if inplace and kept[0] is not logits:
+        raise ValueError("in place needs logits whose rows are contiguous")
+    dz = logits if inplace else torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    _call("tq_topk_distill_grad", *head, temperature, _ptr(dloss), _ptr(loss), _ptr(dz),
+          head[4] if inplace else vocab, _ptr(ws), nws, _stream(logits.device))
+    return loss, dz
+
+
+def tq_topk_distill_workspace_bytes(rows, vocab):
+    return int(_lib.tq_topk_distill_workspace_bytes(rows, vocab))

@@ -1,0 +1,839 @@
+// tq_distill.hip -- distillation of a student from its teacher's top logits:
+// the loss of every row, its gradient, and both in one call.
+//
+//   s = 1 / T;  entry k of a row is (i_k, t_k), a padding entry when i_k lies
+//   outside [0, V);  log q_j = s z_j - lse(s z)
+//   without the teacher's normaliser: p = softmax(s t) over the row's entries,
+//     L = sum_k p_k (log p_k - log q_{i_k}),  dL/dz_j = s (q_j - sum_{i_k = j} p_k)
+//   with it (log-sum-exp of all the teacher's s t): p_k = exp(s t_k - teacher_lse),
+//     p_r = max(0, 1 - sum p), q_r = the student's mass outside the entries,
+//     L gains p_r (log p_r - log q_r), and with Z = sum p + p_r
+//     dL/dz_j = s (q_j Z - p_j) for an entry's j, s q_j (Z - p_r / q_r) elsewhere.
+//   A row without entries has loss 0 and gradient 0.
+//
+// q_r is summed over the entries' complement, not taken as 1 - sum q, which
+// would lose it where the student agrees with the teacher.  To know which
+// columns are entries, a workgroup keeps one bit per column of its part of the
+// row in LDS; the gradient finds an entry's probability by the rank of its bit
+// (a prefix count per 32-column word, then the bits below it), so each element
+// is written once, in order, with no scatter afterwards.
+//
+// All sums are binary32, relative to the row's largest logit.  Every kernel is
+// bound by HBM: the loss reads the logits once, the gradient reads them and
+// writes as much; in one call the row is held in registers between the two.
+#include "tq_llm.h"
+
+namespace tq {
+
+constexpr int DT_K = 1024;               // most entries per row
+constexpr int DT_COEF = 8;               // floats of a row's coefficients
+
+struct Entries {
+    const void* idx;
+    int idx64;
+    const void* val;
+    int val_dt;
+    int K;
+    const float* tlse;                   // null: the probabilities are normalised over the entries
+};
+
+// Entry k's column, or -1 for a padding entry.
+__device__ __forceinline__ int entry_col(const Entries& e, int64_t row, int k, int V)
+{
+    const int64_t at = row * e.K + k;
+    const int64_t i = e.idx64 ? static_cast<const int64_t*>(e.idx)[at] : static_cast<const int32_t*>(e.idx)[at];
+    return i >= 0 && i < V ? (int)i : -1;
+}
+__device__ __forceinline__ float entry_val(const Entries& e, int64_t row, int k)
+{
+    return load1_rt(e.val, e.val_dt, row * e.K + k, 0.0f);
+}
+
+// 2^x by the exponential unit (x of a probability, at most 0 up to rounding;
+// results below 2^-126 are flushed, far under any sum they join).
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
+
+// The logit that a row's exponentials are taken relative to.
+__device__ __forceinline__ float base_of(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+// What a row's gradient needs: dL/dz_j = e_j (in or out) - sg p_j with
+// e_j = 2^((z_j - m) c), the sums' reciprocals folded into `in` and `out`.
+struct Coef {
+    float m, in, out, sg, tm, ti;
+    bool some;
+};
+
+__device__ __forceinline__ float entry_p(const Entries& e, const Coef& q, float t, float s, float c)
+{
+    return e.tlse ? ex2((t * s - q.tm) * LOG2E) : ex2((t - q.tm) * c) * q.ti;
+}
+
+// The coefficients from the student's sums S, R (relative to m), the
+// teacher's base tm and sum (`tsum`: of 2^((t - tm) c) without, of p with the
+// normaliser) and whether the row has entries at all.
+__device__ __forceinline__ Coef make_coef(bool rest, bool some, float m, float S, float R, float tm, float tsum,
+                                          float s, float g, float* p_rest)
+{
+    Coef q;
+    q.m = base_of(m);
+    q.some = some;
+    q.sg = s * g;
+    q.tm = tm;
+    q.ti = rest ? 1.0f : 1.0f / tsum;
+    const float pr = rest && some ? __builtin_fmaxf(0.0f, 1.0f - tsum) : 0.0f;
+    const float Z = rest ? tsum + pr : 1.0f;
+    const float is = S == 0.0f ? 0.0f : 1.0f / S;    // a row of -inf logits has no gradient
+    q.in = q.sg * Z * is;
+    q.out = pr > 0.0f && R > 0.0f ? q.sg * (Z * is - pr / R) : q.in;
+    // it multiplies exponentials that may be 0
+    if (__builtin_isinf(q.out)) q.out = __builtin_copysignf(3.4028234664e38f, q.out);
+    if (S == 0.0f) {
+        q.out = 0.0f;
+        q.sg = 0.0f;
+    }
+    *p_rest = pr;
+    return q;
+}
+
+// Entry k's part of the loss.
+__device__ __forceinline__ float entry_loss(const Entries& e, float t, float z, float s, float c, float tm, float tsum,
+                                            float m, float S)
+{
+    const float logp = e.tlse ? (t * s - tm) : ((t - tm) * s - lg2(tsum) * LN2);
+    const float p = e.tlse ? ex2(logp * LOG2E) : ex2((t - tm) * c) / tsum;
+    if (p == 0.0f) return 0.0f;
+    if (S == 0.0f) return __builtin_inff();
+    return p * (logp - ((z - base_of(m)) * s - lg2(S) * LN2));
+}
+__device__ __forceinline__ float rest_loss(float pr, float R, float S)
+{
+    if (pr == 0.0f) return 0.0f;
+    return S == 0.0f ? __builtin_inff() : pr * LN2 * (lg2(pr) - (lg2(R) - lg2(S)));
+}
+
+// ------------------------------------------------------------ entry columns
+// One bit per column of the workgroup's part of the row, a count of the bits
+// before each word, and the entries' values by rank.
+template <int NT, int WORDS>
+struct Marks {
+    uint32_t bits[WORDS];
+    uint16_t before[WORDS];
+    float value[DT_K];
+    int waves[NT / 64];
+    int twice;
+};
+
+template <int NT, int WORDS>
+__device__ __forceinline__ void marks_clear(Marks<NT, WORDS>& k)
+{
+    for (int i = threadIdx.x; i < WORDS; i += NT) k.bits[i] = 0;
+    if (threadIdx.x == 0) k.twice = 0;
+}
+
+// Marks column `at` (relative to the part).
+template <int NT, int WORDS>
+__device__ __forceinline__ void mark(Marks<NT, WORDS>& k, int at)
+{
+    const uint32_t bit = 1u << (at & 31);
+    if (atomicOr(&k.bits[at >> 5], bit) & bit) k.twice = 1;
+}
+
+// The eight bits of columns at .. at + 7.
+template <int NT, int WORDS>
+__device__ __forceinline__ uint32_t marks8(const Marks<NT, WORDS>& k, int at)
+{
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(k.bits);
+    uint32_t m = b[at >> 3];
+    if (at & 7) m = (m | (uint32_t)b[(at >> 3) + 1] << 8) >> (at & 7) & 0xffu;
+    return m;
+}
+
+template <int NT, int WORDS>
+__device__ __forceinline__ int rank_of(const Marks<NT, WORDS>& k, int at)
+{
+    return k.before[at >> 5] + __popc(k.bits[at >> 5] & ((1u << (at & 31)) - 1));
+}
+
+// Counts the bits before every word (after a barrier behind the marking;
+// contains one barrier, and needs one before the ranks are used).
+template <int NT, int WORDS>
+__device__ __forceinline__ void marks_count(Marks<NT, WORDS>& k)
+{
+    constexpr int PER = (WORDS + NT - 1) / NT;
+    const int t = threadIdx.x, first = t * PER;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (first + i < WORDS) n += __popc(k.bits[first + i]);
+    int upto = n;                        // over this lane and those before it
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d, 64);
+        if ((t & 63) >= d) upto += o;
+    }
+    if ((t & 63) == 63) k.waves[t >> 6] = upto;
+    __syncthreads();
+    int at = upto - n;
+#pragma unroll 1
+    for (int w = 0; w < (t >> 6); ++w) at += k.waves[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (first + i < WORDS) {
+            k.before[first + i] = (uint16_t)at;
+            at += __popc(k.bits[first + i]);
+        }
+}
+
+// Writes every entry's sg p to its rank.  Entries of one column (a row should
+// not have any) are added in entry order by one thread.
+template <int NT, int WORDS>
+__device__ __forceinline__ void marks_fill(Marks<NT, WORDS>& k, const Entries& e, const Coef& q, int64_t row, int V,
+                                           int c0, int n, float s, float c)
+{
+    const int t = threadIdx.x;
+    if (!k.twice) {
+#pragma unroll 1
+        for (int i = t; i < e.K; i += NT) {
+            const int col = entry_col(e, row, i, V) - c0;
+            if (col >= 0 && col < n) k.value[rank_of(k, col)] = q.sg * entry_p(e, q, entry_val(e, row, i), s, c);
+        }
+    } else {
+#pragma unroll 1
+        for (int r = t; r < e.K; r += NT) {
+            float v = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < e.K; ++i) {
+                const int col = entry_col(e, row, i, V) - c0;
+                if (col >= 0 && col < n && rank_of(k, col) == r)
+                    v += q.sg * entry_p(e, q, entry_val(e, row, i), s, c);
+            }
+            k.value[r] = v;
+        }
+    }
+}
+
+// The gradient of eight elements.
+template <int NT, int WORDS>
+__device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, int at, float c, float v[8])
+{
+    const uint32_t m = marks8(k, at);
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        e[i] = ex2((v[i] - q.m) * c);
+        v[i] = e[i] * q.out;
+    }
+    if (m) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (m >> i & 1) v[i] = e[i] * q.in - k.value[rank_of(k, at + i)];
+    }
+}
+
+// --------------------------------------------------------------- statistics
+// k_distill_stats: a workgroup per row and part of the row (CH columns): the
+// part's largest logit m, the sum of 2^((z - m) c) over all its columns and
+// over those that are no entries (only with REST).
+template <int FT, bool REST, int CH>
+__global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ z, int64_t ldz, int V, int parts,
+                                                       Entries ent, float c, float* __restrict__ part)
+{
+    constexpr int U = 4;
+    __shared__ uint32_t bits[REST ? CH / 32 + 1 : 1];
+    __shared__ float red[4][3];
+    const int t = threadIdx.x;
+    const int64_t row = blockIdx.x / (unsigned)parts;
+    const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * CH;
+    const int n = V - c0 < CH ? V - c0 : CH, nvec = (n + 7) / 8;
+    const int64_t base = row * ldz + c0;
+    if constexpr (REST) {
+        for (int i = t; i < CH / 32 + 1; i += 256) bits[i] = 0;
+        __syncthreads();
+        for (int k = t; k < ent.K; k += 256) {
+            const int col = entry_col(ent, row, k, V) - c0;
+            if (col >= 0 && col < n) atomicOr(&bits[col >> 5], 1u << (col & 31));
+        }
+        __syncthreads();
+    }
+    float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
+    auto add = [&](float v[8], int lo, uint32_t mask) {
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, v[i]);
+        if (top > m) {
+            const float f = ex2((m - top) * c);   // m = -inf: 0
+            S *= f;
+            R *= f;
+            m = top;
+        }
+        const float b = base_of(m);
+        float sum = 0.0f, in = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = ex2((v[i] - b) * c), y = i >= lo ? x : 0.0f;
+            sum += y;
+            if constexpr (REST) in += mask >> i & 1 ? 0.0f : y;
+        }
+        S += sum;
+        if constexpr (REST) R += in;
+    };
+    if (n >= 8) {
+        for (int v0 = t; v0 < nvec; v0 += 256 * U) {
+            Raw8<FT> raw[U];
+            Vec8 at[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                at[u] = vec8(v0 + 256 * u, n);
+                raw[u] = load8_any<FT>(z, base + at[u].at);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (at[u].lo == 8) continue;
+                float v[8];
+                widen8<FT>(raw[u], v);
+                uint32_t mask = 0;
+                if constexpr (REST) {
+                    const uint8_t* b = reinterpret_cast<const uint8_t*>(bits);
+                    mask = b[at[u].at >> 3];
+                    if (at[u].at & 7) mask = (mask | (uint32_t)b[(at[u].at >> 3) + 1] << 8) >> (at[u].at & 7);
+                }
+                add(v, at[u].lo, mask);
+            }
+        }
+    } else if (t < n) {
+        float v[8];
+        v[0] = load1<FT>(z, base + t);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v[i] = -__builtin_inff();
+        // the seven other places hold nothing: their exponentials are zeros
+        add(v, 0, REST ? bits[0] >> t & 1 : 0);
+    }
+    const float mw = wave_max(m);
+    {
+        const float f = ex2((m - base_of(mw)) * c);
+        S = wave_sum(S * f);             // f = 0 where the lane met nothing above -inf
+        R = wave_sum(R * f);
+    }
+    if ((t & 63) == 0) {
+        red[t >> 6][0] = mw;
+        red[t >> 6][1] = S;
+        red[t >> 6][2] = R;
+    }
+    __syncthreads();
+    if (t != 0) return;
+    m = __builtin_fmaxf(__builtin_fmaxf(red[0][0], red[1][0]), __builtin_fmaxf(red[2][0], red[3][0]));
+    S = 0.0f;
+    R = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = ex2((red[w][0] - base_of(m)) * c);
+        S += red[w][1] * f;
+        R += red[w][2] * f;
+    }
+    float* to = part + ((int64_t)row * parts + p) * 3;
+    to[0] = m;
+    to[1] = S;
+    to[2] = R;
+}
+
+// k_distill_rows: a wave per row.  FROM_PARTS joins the row's parts and
+// writes the loss and the row's statistics (stats[row] = {largest logit, sum of
+// exp(s (z - it))}, rest[row] the same sum over the columns outside the
+// entries); otherwise it reads those statistics.  `coef` (may be null
+// in the first form) gets what the gradient needs.
+template <int FT, bool FROM_PARTS>
+__global__ __launch_bounds__(256) void k_distill_rows(const void* __restrict__ z, int64_t ldz, int64_t rows, int V,
+                                                      Entries ent, float s, float c, const float* __restrict__ part,
+                                                      int parts, const float* __restrict__ dloss,
+                                                      float* __restrict__ loss, float* __restrict__ stats,
+                                                      float* __restrict__ rest_sum, float* __restrict__ coef)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (row >= rows) return;
+    const bool rest = ent.tlse != nullptr;
+    float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
+    if constexpr (FROM_PARTS) {
+        const float* from = part + row * parts * 3;
+        for (int i = lane; i < parts; i += 64) m = __builtin_fmaxf(m, from[3 * i]);
+        m = wave_max(m);
+        const float b = base_of(m);
+        for (int i = lane; i < parts; i += 64) {
+            const float f = ex2((from[3 * i] - b) * c);
+            S += from[3 * i + 1] * f;
+            R += from[3 * i + 2] * f;
+        }
+        S = wave_sum(S);
+        R = wave_sum(R);
+    } else {
+        m = stats[2 * row];
+        S = stats[2 * row + 1];
+        R = rest ? rest_sum[row] : 0.0f;
+    }
+    // the teacher
+    float tm = -__builtin_inff(), tsum = 0.0f;
+    bool some = false;
+    for (int k = lane; k < ent.K; k += 64)
+        if (entry_col(ent, row, k, V) >= 0) {
+            some = true;
+            tm = __builtin_fmaxf(tm, entry_val(ent, row, k));
+        }
+    some = __any(some);
+    tm = rest ? ent.tlse[row] : base_of(wave_max(tm));
+    for (int k = lane; k < ent.K; k += 64)
+        if (entry_col(ent, row, k, V) >= 0) {
+            const float t = entry_val(ent, row, k);
+            tsum += rest ? ex2((t * s - tm) * LOG2E) : ex2((t - tm) * c);
+        }
+    tsum = wave_sum(tsum);
+    if (!rest && tsum == 0.0f) some = false;      // every entry at -inf
+    float pr;
+    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+    if constexpr (FROM_PARTS) {
+        float l = 0.0f;
+        if (some)
+            for (int k = lane; k < ent.K; k += 64) {
+                const int col = entry_col(ent, row, k, V);
+                if (col >= 0)
+                    l += entry_loss(ent, entry_val(ent, row, k), load1<FT>(z, row * ldz + col), s, c, tm, tsum, m, S);
+            }
+        l = wave_sum(l) + (lane == 0 && some ? rest_loss(pr, R, S) : 0.0f);
+        if (lane == 0) {
+            loss[row] = l;
+            if (stats) {
+                stats[2 * row] = m;
+                stats[2 * row + 1] = S;
+            }
+            if (rest_sum) rest_sum[row] = R;
+        }
+    }
+    if (coef && lane == 0) {
+        float* to = coef + row * DT_COEF;
+        to[0] = q.m;
+        to[1] = q.in;
+        to[2] = q.out;
+        to[3] = q.sg;
+        to[4] = q.tm;
+        to[5] = q.ti;
+        to[6] = some ? 1.0f : 0.0f;
+    }
+}
+
+// k_distill_grad: a workgroup per row and part of the row.
+template <int FT, int CH>
+__global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz, int V, int parts, Entries ent,
+                                                      float s, float c, const float* __restrict__ coef, void* dz,
+                                                      int64_t lddz)
+{
+    constexpr int U = 2;
+    __shared__ Marks<256, CH / 32 + 1> k;
+    const int t = threadIdx.x;
+    const int64_t row = blockIdx.x / (unsigned)parts;
+    const int c0 = (int)(blockIdx.x % (unsigned)parts) * CH;
+    const int n = V - c0 < CH ? V - c0 : CH, nvec = (n + 7) / 8;
+    const int64_t from = row * ldz + c0, to = row * lddz + c0;
+    Coef q;
+    {
+        const float* f = coef + row * DT_COEF;
+        q.m = f[0];
+        q.in = f[1];
+        q.out = f[2];
+        q.sg = f[3];
+        q.tm = f[4];
+        q.ti = f[5];
+        q.some = f[6] != 0.0f;
+    }
+    if (!q.some) {                       // uniform: no entries, no gradient
+        for (int j = t; j < n; j += 256) store1<FT>(dz, to + j, 0.0f);
+        return;
+    }
+    marks_clear(k);
+    __syncthreads();
+    for (int i = t; i < ent.K; i += 256) {
+        const int col = entry_col(ent, row, i, V) - c0;
+        if (col >= 0 && col < n) mark(k, col);
+    }
+    __syncthreads();
+    marks_count(k);
+    __syncthreads();
+    marks_fill(k, ent, q, row, V, c0, n, s, c);
+    __syncthreads();
+    if (n < 8) {
+        if (t < n) {
+            float v[8] = {load1<FT>(z, from + t), 0, 0, 0, 0, 0, 0, 0};
+            grad8(k, q, t, c, v);
+            store1<FT>(dz, to + t, v[0]);
+        }
+        return;
+    }
+    for (int v0 = t; v0 < nvec; v0 += 256 * U) {
+        Raw8<FT> raw[U];
+        Vec8 at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            at[u] = vec8(v0 + 256 * u, n);
+            raw[u] = load8_any<FT>(z, from + at[u].at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (at[u].lo == 8) continue;
+            float v[8];
+            widen8<FT>(raw[u], v);
+            grad8(k, q, at[u].at, c, v);
+            store8_own<FT>(dz, to, at[u], v);
+        }
+    }
+}
+
+// k_distill_held: loss and gradient of a row in one read: NT threads hold the
+// row (8 <= V <= 8 NT W) in registers in its own type.
+template <int FT, int NT, int W>
+__global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz, int V, Entries ent, float s, float c,
+                                                     const float* __restrict__ dloss, float* __restrict__ loss,
+                                                     void* dz, int64_t lddz)
+{
+    constexpr int NW = NT / 64;
+    __shared__ Marks<NT, NT * W / 4 + 1> k;
+    __shared__ float rmax[2][NW], rsum[4][NW];
+    const int t = threadIdx.x, wave = t >> 6;
+    constexpr int ES = FT == F32 ? 4 : 2;
+    const int64_t row = blockIdx.x;
+    const char* from = static_cast<const char*>(z) + row * ldz * ES;
+    char* to = static_cast<char*>(dz) + row * lddz * ES;
+    const bool rest = ent.tlse != nullptr;
+    Raw8<FT> raw[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) raw[w] = load8_off<FT>(from, (uint32_t)vec8(w * NT + t, V).at * ES);
+    marks_clear(k);
+    __syncthreads();
+    float tm = -__builtin_inff();
+    int some = 0;
+#pragma unroll 1
+    for (int i = t; i < ent.K; i += NT) {
+        const int col = entry_col(ent, row, i, V);
+        if (col >= 0) {
+            some = 1;
+            mark(k, col);
+            tm = __builtin_fmaxf(tm, entry_val(ent, row, i));
+        }
+    }
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < W; ++w) {        // repeated elements do not change a maximum
+        float v[8];
+        widen8<FT>(raw[w], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+    }
+    m = wave_max(m);
+    tm = wave_max(tm);
+    if ((t & 63) == 0) {
+        rmax[0][wave] = m;
+        rmax[1][wave] = tm;
+    }
+    some = __syncthreads_or(some);
+    m = rmax[0][0];
+    tm = rmax[1][0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+        m = __builtin_fmaxf(m, rmax[0][w]);
+        tm = __builtin_fmaxf(tm, rmax[1][w]);
+    }
+    const float b = base_of(m);
+    tm = rest ? ent.tlse[row] : base_of(tm);
+    float S = 0.0f, R = 0.0f, tsum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const Vec8 at = vec8(afresh(w * NT + t), V);
+        if (at.lo == 8) continue;
+        float v[8], x = 0.0f;
+        keep_raw<FT>(raw[w]);
+        widen8<FT>(raw[w], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = ex2((v[i] - b) * c);
+            v[i] = i >= at.lo ? v[i] : 0.0f;
+            x += v[i];
+        }
+        S += x;
+        if (rest) {
+            const uint32_t mask = marks8(k, at.at);
+            if (mask) {
+                x = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x += mask >> i & 1 ? 0.0f : v[i];
+            }
+            R += x;
+        }
+        __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
+    }
+#pragma unroll 1
+    for (int i = t; i < ent.K; i += NT)
+        if (entry_col(ent, row, i, V) >= 0) {
+            const float x = entry_val(ent, row, i);
+            tsum += rest ? ex2((x * s - tm) * LOG2E) : ex2((x - tm) * c);
+        }
+    S = wave_sum(S);
+    R = wave_sum(R);
+    tsum = wave_sum(tsum);
+    if ((t & 63) == 0) {
+        rsum[0][wave] = S;
+        rsum[1][wave] = R;
+        rsum[2][wave] = tsum;
+    }
+    marks_count(k);                      // its barrier also publishes the sums
+    __syncthreads();
+    S = 0.0f;
+    R = 0.0f;
+    tsum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        S += rsum[0][w];
+        R += rsum[1][w];
+        tsum += rsum[2][w];
+    }
+    if (!rest && tsum == 0.0f) some = 0;
+    float pr;
+    const Coef q = make_coef(rest, some != 0, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+    if (!q.some) {                       // uniform
+        if (t == 0) loss[row] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const Vec8 at = vec8(afresh(w * NT + t), V);
+            const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (at.lo < 8) store8_own_off<FT>(to, at, v);
+        }
+        return;
+    }
+    marks_fill(k, ent, q, row, V, 0, V, s, c);
+    float l = 0.0f;
+#pragma unroll 1
+    for (int i = t; i < ent.K; i += NT) {
+        const int col = entry_col(ent, row, i, V);
+        if (col >= 0) l += entry_loss(ent, entry_val(ent, row, i), load1<FT>(from, col), s, c, tm, tsum, m, S);
+    }
+    l = wave_sum(l);
+    if ((t & 63) == 0) rsum[3][wave] = l;
+    __syncthreads();                     // also before the first store: dz may be z
+    if (t == 0) {
+        l = rest_loss(pr, R, S);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) l += rsum[3][w];
+        loss[row] = l;
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const Vec8 at = vec8(afresh(w * NT + t), V);
+        if (at.lo == 8) continue;
+        float v[8];
+        keep_raw<FT>(raw[w]);
+        widen8<FT>(raw[w], v);
+        grad8(k, q, at.at, c, v);
+        store8_own_off<FT>(to, at, v);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+// Columns per part: the longest of 32768, 16384, 8192 and 4096 that still
+// gives the chip DT_GROUPS workgroups.
+constexpr int64_t DT_GROUPS = 2048;
+constexpr int DT_CH[] = {32768, 16384, 8192, 4096};
+inline int distill_ch(int64_t rows, int64_t V)
+{
+    for (int ch : DT_CH)
+        if (rows * cdiv(V, ch) >= DT_GROUPS) return ch;
+    return DT_CH[3];
+}
+
+#define TQ_CH_SWITCH(ch, ...)                                                                \
+    do {                                                                                     \
+        if ((ch) == 32768) { constexpr int CHV = 32768; __VA_ARGS__; }                       \
+        else if ((ch) == 16384) { constexpr int CHV = 16384; __VA_ARGS__; }                  \
+        else if ((ch) == 8192) { constexpr int CHV = 8192; __VA_ARGS__; }                    \
+        else { constexpr int CHV = 4096; __VA_ARGS__; }                                      \
+    } while (0)
+
+struct Distill {
+    const void* z;
+    int64_t ldz, rows;
+    int V;
+    Entries ent;
+    float s, c;
+};
+
+template <int FT>
+static void stats_launch(const Distill& d, int ch, float* part, hipStream_t st)
+{
+    const int parts = (int)cdiv(d.V, ch);
+    const dim3 grid((unsigned)(d.rows * parts));
+    if (d.ent.tlse)
+        TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
+                                            parts, d.ent, d.c, part));
+    else
+        TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
+                                            parts, d.ent, d.c, part));
+}
+
+template <int FT, bool FROM_PARTS>
+static void rows_launch(const Distill& d, int parts, const float* part, const float* dloss, float* loss, float* stats,
+                        float* rest_sum, float* coef, hipStream_t st)
+{
+    hipLaunchKernelGGL((k_distill_rows<FT, FROM_PARTS>), dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.z, d.ldz,
+                       d.rows, d.V, d.ent, d.s, d.c, part, parts, dloss, loss, stats, rest_sum, coef);
+}
+
+template <int FT>
+static void grad_launch(const Distill& d, int ch, const float* coef, void* dz, int64_t lddz, hipStream_t st)
+{
+    const int parts = (int)cdiv(d.V, ch);
+    TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV>), dim3((unsigned)(d.rows * parts)), dim3(256), 0, st,
+                                        d.z, d.ldz, d.V, parts, d.ent, d.s, d.c, coef, dz, lddz));
+}
+
+// The row is held from this many rows on (fewer leave CUs idle, and the
+// parts of a row spread over them instead), where a workgroup can hold it.
+constexpr int64_t DT_HELD_ROWS = 128;
+template <int FT>
+static bool held_launch(const Distill& d, const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
+{
+    constexpr int H = FT == F32 ? 2 : 1;  // binary32 rows hold half as many elements
+    if (d.rows < DT_HELD_ROWS || d.V < 8 || d.V > (FT == F32 ? 65536 : 98304)) return false;
+#define TQ_HELD(NT, W)                                                                                            \
+    hipLaunchKernelGGL((k_distill_held<FT, NT, W>), dim3((unsigned)d.rows), dim3(NT), 0, st, d.z, d.ldz, d.V, d.ent, \
+                       d.s, d.c, dloss, loss, dz, lddz)
+    if (d.V <= 8192) TQ_HELD(256, 4);
+    else if (d.V <= 32768 / H) TQ_HELD(256, 16 / H);
+    else if (d.V <= 65536 / H) TQ_HELD(512, 16 / H);
+    else TQ_HELD(1024, FT == F32 ? 8 : 12);
+#undef TQ_HELD
+    return true;
+}
+
+static bool natural(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+// Checks what the three calls share and fills `d`; *work is false where there
+// is nothing to do.
+static tq_status distill_check(const void* logits, int dt, int64_t rows, int64_t vocab, int64_t ldz, const void* idx,
+                               int idx_bits, const void* val, int val_dt, int64_t K, const float* teacher_lse,
+                               float temperature, Distill* d, bool* work)
+{
+    *work = false;
+    if (!valid_ftype(dt) || !valid_ftype(val_dt) || (idx_bits != 32 && idx_bits != 64)) return TQ_ERR_INVALID;
+    if (rows < 0 || vocab < 0 || K < 1) return TQ_ERR_INVALID;
+    if (!(temperature > 0.0f) || temperature > 3.0e38f) return TQ_ERR_INVALID;
+    if (rows == 0) return TQ_OK;
+    if (vocab == 0 || !logits || ldz < vocab || !idx || !val) return TQ_ERR_INVALID;
+    if (K > DT_K || vocab > 0x7fffff00 || rows > 0x7fffffff || rows * cdiv(vocab, DT_CH[3]) > 0x7fffffff)
+        return TQ_ERR_UNSUPPORTED;
+    if (!natural(logits, ftype_size(dt)) || !natural(idx, idx_bits / 8) || !natural(val, ftype_size(val_dt)) ||
+        !natural(teacher_lse, 4))
+        return TQ_ERR_ALIGN;
+    d->z = logits;
+    d->ldz = ldz;
+    d->rows = rows;
+    d->V = (int)vocab;
+    d->ent = Entries{idx, idx_bits == 64, val, val_dt, (int)K, teacher_lse};
+    d->s = (float)(1.0 / (double)temperature);
+    d->c = (float)(1.4426950408889634 / (double)temperature);
+    *work = true;
+    return TQ_OK;
+}
+
+static tq_status workspace_check(const void* ws, size_t have, int64_t rows, int64_t vocab)
+{
+    if (!ws || have < tq_topk_distill_workspace_bytes(rows, vocab)) return TQ_ERR_INVALID;
+    return aligned16(ws) ? TQ_OK : TQ_ERR_ALIGN;
+}
+
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" {
+
+size_t tq_topk_distill_workspace_bytes(int64_t rows, int64_t vocab)
+{
+    if (rows <= 0 || vocab <= 0) return 0;
+    return (size_t)rows * (DT_COEF + 3 * (size_t)cdiv(vocab, distill_ch(rows, vocab))) * sizeof(float);
+}
+
+tq_status tq_topk_distill(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                          const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
+                          const float* teacher_lse, float temperature, float* loss, float* stats, float* rest_sum,
+                          void* workspace, size_t workspace_bytes, void* stream)
+{
+    Distill d;
+    bool work;
+    tq_status r = distill_check(logits, dtype, rows, vocab, row_stride, top_idx, idx_bits, top_val, val_dtype, k,
+                                teacher_lse, temperature, &d, &work);
+    if (r != TQ_OK || !work) return r;
+    if (!loss) return TQ_ERR_INVALID;
+    if (!natural(loss, 4) || !natural(stats, 4) || !natural(rest_sum, 4)) return TQ_ERR_ALIGN;
+    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab)) != TQ_OK) return r;
+    const int ch = distill_ch(rows, vocab);
+    float* part = static_cast<float*>(workspace) + rows * DT_COEF;
+    hipStream_t st = as_stream(stream);
+    TQ_LLM_FT_SWITCH(dtype, {
+        stats_launch<FTV>(d, ch, part, st);
+        rows_launch<FTV, true>(d, (int)cdiv(vocab, ch), part, nullptr, loss, stats, teacher_lse ? rest_sum : nullptr,
+                               nullptr, st);
+    });
+    return launch_status();
+}
+
+tq_status tq_topk_distill_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                   const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
+                                   const float* teacher_lse, float temperature, const float* stats,
+                                   const float* rest_sum, const float* dloss, void* dlogits, int64_t d_row_stride,
+                                   void* workspace, size_t workspace_bytes, void* stream)
+{
+    Distill d;
+    bool work;
+    tq_status r = distill_check(logits, dtype, rows, vocab, row_stride, top_idx, idx_bits, top_val, val_dtype, k,
+                                teacher_lse, temperature, &d, &work);
+    if (r != TQ_OK || !work) return r;
+    if (!stats || (teacher_lse && !rest_sum) || !dlogits || d_row_stride < vocab) return TQ_ERR_INVALID;
+    if (!natural(stats, 4) || !natural(rest_sum, 4) || !natural(dloss, 4) || !natural(dlogits, ftype_size(dtype)))
+        return TQ_ERR_ALIGN;
+    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab)) != TQ_OK) return r;
+    float* coef = static_cast<float*>(workspace);
+    hipStream_t st = as_stream(stream);
+    TQ_LLM_FT_SWITCH(dtype, {
+        rows_launch<FTV, false>(d, 0, nullptr, dloss, nullptr, const_cast<float*>(stats), const_cast<float*>(rest_sum),
+                                coef, st);
+        grad_launch<FTV>(d, distill_ch(rows, vocab), coef, dlogits, d_row_stride, st);
+    });
+    return launch_status();
+}
+
+tq_status tq_topk_distill_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                               const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
+                               const float* teacher_lse, float temperature, const float* dloss, float* loss,
+                               void* dlogits, int64_t d_row_stride, void* workspace, size_t workspace_bytes,
+                               void* stream)
+{
+    Distill d;
+    bool work;
+    tq_status r = distill_check(logits, dtype, rows, vocab, row_stride, top_idx, idx_bits, top_val, val_dtype, k,
+                                teacher_lse, temperature, &d, &work);
+    if (r != TQ_OK || !work) return r;
+    if (!loss || !dlogits || d_row_stride < vocab) return TQ_ERR_INVALID;
+    if (!natural(loss, 4) || !natural(dloss, 4) || !natural(dlogits, ftype_size(dtype))) return TQ_ERR_ALIGN;
+    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab)) != TQ_OK) return r;
+    const int ch = distill_ch(rows, vocab);
+    float* coef = static_cast<float*>(workspace);
+    float* part = coef + rows * DT_COEF;
+    hipStream_t st = as_stream(stream);
+    TQ_LLM_FT_SWITCH(dtype, {
+        if (!held_launch<FTV>(d, dloss, loss, dlogits, d_row_stride, st)) {
+            stats_launch<FTV>(d, ch, part, st);
+            rows_launch<FTV, true>(d, (int)cdiv(vocab, ch), part, dloss, loss, nullptr, nullptr, coef, st);
+            grad_launch<FTV>(d, ch, coef, dlogits, d_row_stride, st);
+        }
+    });
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,619 @@
+// tq_norm.hip -- layer norm over the last dimension: the forward pass, the
+// forward pass fused with the per-token s8 quantizer that feeds the W8A8
+// product, and the backward pass with the reduction of the weight's and the
+// bias's gradient.
+//
+//   mu = sum_j x_j / C,  v = sum_j (x_j - mu)^2 / C,  r = 1 / sqrt(v + eps)
+//   y_j = (x_j - mu) r w_j + b_j
+//   backward, with g = dy w and h = (x - mu) r:
+//   dx = r (g - sum(g)/C - h sum(g h)/C),  dw_j = sum_rows dy h,  db_j = sum_rows dy
+//
+// All statistics and sums are binary32; the variance is taken around the mean
+// from the values held in registers (one read of the row, no E[x^2] - mu^2
+// cancellation).  Outputs are rounded once to their type.  The fused form
+// rounds y to x's type before it takes the row's maximum, so that its codes
+// and scales are those of tq_layer_norm followed by tq_quant_per_token.
+//
+// Every kernel is bound by HBM: 2 bytes in and 2 out per bf16 element
+// forwards, 4 in and 2 out backwards.
+#include "tq_llm.h"
+
+namespace tq {
+
+enum { OUT_Y = 0, OUT_S8 = 1 };
+
+// One sum over the NT threads of a row (a wave's own when NT is 64).  `slot`
+// alternates so that a row's second sum needs no barrier before it.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float* slot)
+{
+    v = wave_sum(v);
+    if constexpr (NT > 64) {
+        const int t = threadIdx.x;
+        if ((t & 63) == 0) slot[t >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NT / 64; ++k) v += slot[k];
+    }
+    return v;
+}
+template <int NT>
+__device__ __forceinline__ float row_max(float v, float* slot)
+{
+    v = wave_max(v);
+    if constexpr (NT > 64) {
+        const int t = threadIdx.x;
+        if ((t & 63) == 0) slot[t >> 6] = v;
+        __syncthreads();
+        v = slot[0];
+#pragma unroll
+        for (int k = 1; k < NT / 64; ++k) v = __builtin_fmaxf(v, slot[k]);
+    }
+    return v;
+}
+
+// The value as x's type holds it.
+template <int FT>
+__device__ __forceinline__ float as_stored(float v)
+{
+    if constexpr (FT == F32) return v;
+    else if constexpr (FT == BF16) return as_f((uint32_t)to_bf16_bits(v) << 16);
+    else return (float)__builtin_bit_cast(_Float16, to_f16_bits(v));
+}
+
+// Symmetric s8 codes of a row: scale = amax / 127 (1 if that is 0), code =
+// clamp(rne(v / scale)), both divisions correctly rounded.
+struct S8Row {
+    float s, y;
+    bool fast;
+};
+__device__ __forceinline__ S8Row s8_row(float amax)
+{
+    S8Row r;
+    r.s = amax / 127.0f;
+    r.s = r.s == 0.0f ? 1.0f : r.s;
+    r.fast = scale_in_fast_range(r.s);
+    r.y = r.fast ? rcp_rn(r.s) : 0.0f;
+    return r;
+}
+template <int FT>
+__device__ __forceinline__ float s8_code(float v, const S8Row& r)
+{
+    const float q = r.fast && __builtin_fabsf(v) <= 0x1p86f ? div_q<FT>(v, r.s, r.y) : v / r.s;
+    return int_code_f(q, 0.0f, MAGIC - 127.0f, MAGIC + 127.0f);
+}
+
+// k_ln_rows: NT threads per row, W vectors of eight elements per thread, the
+// row held in registers (8 <= cols <= 8 * NT * W).  NT = 64 puts four rows in
+// a workgroup and needs no barrier.
+template <int FT, int NT, int W, int OUT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_rows(
+    const void* __restrict__ x, int64_t ldx, int64_t rows, int64_t cols, const void* __restrict__ weight,
+    const void* __restrict__ bias, int wdt, float eps, void* __restrict__ y, float* __restrict__ scale,
+    float* __restrict__ mean, float* __restrict__ rstd)
+{
+    constexpr int RPB = NT < 256 ? 256 / NT : 1;
+    __shared__ float slots[3][NT / 64];
+    const int t = threadIdx.x % NT;
+    const int64_t row = (int64_t)blockIdx.x * RPB + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    if (row >= rows) return;     // only with NT == 64, whose rows meet no barrier
+
+    Vec8 at[W];
+    Raw8<FT> raw[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        at[w] = vec8(w * NT + t, (int)cols);
+        raw[w] = load8_any<FT>(x, row * ldx + at[w].at);
+    }
+    float v[W][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        widen8<FT>(raw[w], v[w]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += i >= at[w].lo ? v[w][i] : 0.0f;
+    }
+    const float mu = row_sum<NT>(s, slots[0]) / (float)cols;
+    RawAny rw[W], rb[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        rw[w] = load8_rt(weight, wdt, at[w].at);
+        rb[w] = load8_rt(bias, wdt, at[w].at);
+    }
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[w][i] -= mu;
+            const float d = i >= at[w].lo ? v[w][i] : 0.0f;
+            s = __builtin_fmaf(d, d, s);
+        }
+    const float r = 1.0f / __builtin_sqrtf(row_sum<NT>(s, slots[1]) / (float)cols + eps);
+    if (t == 0) {
+        if (mean) mean[row] = mu;
+        if (rstd) rstd[row] = r;
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        float ww[8], bb[8];
+        widen8_rt(rw[w], weight, wdt, 1.0f, ww);
+        widen8_rt(rb[w], bias, wdt, 0.0f, bb);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[w][i] = __builtin_fmaf(v[w][i] * r, ww[i], bb[i]);
+        if constexpr (OUT == OUT_Y) {
+            if (at[w].lo < 8) store8_own<FT>(y, row * cols, at[w], v[w]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[w][i] = as_stored<FT>(v[w][i]);
+                amax = __builtin_fmaxf(amax, i >= at[w].lo ? __builtin_fabsf(v[w][i]) : 0.0f);
+            }
+        }
+    }
+    if constexpr (OUT == OUT_S8) {
+        amax = row_max<NT>(amax, slots[2]);
+        const S8Row p = s8_row(amax);
+        if (t == 0) scale[row] = p.s;
+        uint8_t* q = static_cast<uint8_t*>(y) + row * cols;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (at[w].lo == 8) continue;
+            float c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = s8_code<FT>(v[w][i], p);
+            if (at[w].lo == 0) {
+                const u32x2_any o = {pack_bytes4(c[0], c[1], c[2], c[3]), pack_bytes4(c[4], c[5], c[6], c[7])};
+                *reinterpret_cast<u32x2_any*>(q + at[w].at) = o;
+            } else {
+#pragma unroll
+                for (int i = 1; i < 8; ++i)
+                    if (i >= at[w].lo) q[at[w].at + i] = (uint8_t)as_u(c[i]);
+            }
+        }
+    }
+}
+
+// k_ln_loop: rows of any length (below 8 elements, or longer than a workgroup
+// holds): a workgroup per row reads it once for the mean, once around the
+// mean and once for the output (the later reads meet the caches), and once
+// more for the codes.
+template <int FT, int OUT>
+__global__ __launch_bounds__(1024) void k_ln_loop(const void* __restrict__ x, int64_t ldx, int64_t cols,
+                                                  const void* __restrict__ weight, const void* __restrict__ bias,
+                                                  int wdt, float eps, void* __restrict__ y, float* __restrict__ scale,
+                                                  float* __restrict__ mean, float* __restrict__ rstd)
+{
+    __shared__ float slots[3][16];
+    const int t = threadIdx.x;
+    const int64_t row = blockIdx.x, base = row * ldx;
+    float s = 0.0f;
+    for (int64_t j = t; j < cols; j += 1024) s += load1<FT>(x, base + j);
+    const float mu = row_sum<1024>(s, slots[0]) / (float)cols;
+    s = 0.0f;
+    for (int64_t j = t; j < cols; j += 1024) {
+        const float d = load1<FT>(x, base + j) - mu;
+        s = __builtin_fmaf(d, d, s);
+    }
+    const float r = 1.0f / __builtin_sqrtf(row_sum<1024>(s, slots[1]) / (float)cols + eps);
+    if (t == 0) {
+        if (mean) mean[row] = mu;
+        if (rstd) rstd[row] = r;
+    }
+    auto value = [&](int64_t j) {
+        return __builtin_fmaf((load1<FT>(x, base + j) - mu) * r, load1_rt(weight, wdt, j, 1.0f),
+                              load1_rt(bias, wdt, j, 0.0f));
+    };
+    if constexpr (OUT == OUT_Y) {
+        for (int64_t j = t; j < cols; j += 1024) store1<FT>(y, row * cols + j, value(j));
+    } else {
+        float amax = 0.0f;
+        for (int64_t j = t; j < cols; j += 1024) amax = __builtin_fmaxf(amax, __builtin_fabsf(as_stored<FT>(value(j))));
+        const S8Row p = s8_row(row_max<1024>(amax, slots[2]));
+        if (t == 0) scale[row] = p.s;
+        for (int64_t j = t; j < cols; j += 1024)
+            static_cast<uint8_t*>(y)[row * cols + j] = (uint8_t)as_u(s8_code<FT>(as_stored<FT>(value(j)), p));
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// k_ln_bwd: teams of NT threads, a team per row at a time, W vectors per
+// thread.  A workgroup of BT threads walks the rows blockIdx + k gridDim (in
+// units of its BT / NT teams); each thread keeps the sums of dy h and dy of
+// its own columns in registers over all its rows, the teams add theirs in LDS
+// in a fixed order at the end, and the workgroup leaves one row of partial
+// sums.  The rows of the next step are
+// loaded before the sums of the present one are taken.
+template <int FT, int NT, int W, int BT>
+__global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int64_t lddy, const void* __restrict__ x,
+                                               int64_t ldx, int64_t rows, int64_t cols,
+                                               const void* __restrict__ weight, int wdt,
+                                               const float* __restrict__ mean, const float* __restrict__ rstd,
+                                               void* __restrict__ dx, float* __restrict__ part, int64_t ldp)
+{
+    constexpr int TEAMS = BT / NT, NW = NT / 64;
+    __shared__ float slots[2][TEAMS][NW][2];
+    __shared__ float fold[TEAMS > 1 ? 8 * NT * W : 1];
+    const int t = threadIdx.x % NT, team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+
+    Vec8 at[W];
+    float ww[W][8], dw[W][8], db[W][8];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        at[w] = vec8(w * NT + t, (int)cols);
+        widen8_rt(load8_rt(weight, wdt, at[w].at), weight, wdt, 1.0f, ww[w]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dw[w][i] = 0.0f;
+            db[w][i] = 0.0f;
+        }
+    }
+    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    const int64_t first = (int64_t)blockIdx.x * TEAMS;
+    const float rc = 1.0f / (float)cols;
+    Raw8<FT> nx[W], ny[W];
+    float nmu = 0.0f, nr = 0.0f;
+    // a team past the last row reads the last row again; its sums stay out
+    auto fetch = [&](int64_t row) {
+        row = row < rows ? row : rows - 1;
+        nmu = mean[row];
+        nr = rstd[row];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            nx[w] = load8_any<FT>(x, row * ldx + at[w].at);
+            ny[w] = load8_any<FT>(dy, row * lddy + at[w].at);
+        }
+    };
+    fetch(first + team);
+    int turn = 0;
+    for (int64_t base = first; base < rows; base += step, turn ^= 1) {
+        const int64_t row = base + team;
+        const bool mine = row < rows;
+        Raw8<FT> cx[W], cy[W];
+        const float mu = nmu, r = nr;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            cx[w] = nx[w];
+            cy[w] = ny[w];
+        }
+        if (base + step < rows) fetch(row + step);
+        float sg = 0.0f, sgh = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            float h[8], d[8];
+            widen8<FT>(cx[w], h);
+            widen8<FT>(cy[w], d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool own = mine && i >= at[w].lo;
+                h[i] = (h[i] - mu) * r;
+                const float dd = own ? d[i] : 0.0f, hh = own ? h[i] : 0.0f;
+                const float g = dd * ww[w][i];
+                sg += g;
+                sgh = __builtin_fmaf(g, hh, sgh);
+                dw[w][i] = __builtin_fmaf(dd, hh, dw[w][i]);
+                db[w][i] += dd;
+            }
+        }
+        sg = wave_sum(sg);
+        sgh = wave_sum(sgh);
+        if constexpr (NW > 1) {
+            if ((t & 63) == 0) {
+                slots[turn][team][t >> 6][0] = sg;
+                slots[turn][team][t >> 6][1] = sgh;
+            }
+            __syncthreads();
+            sg = 0.0f;
+            sgh = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                sg += slots[turn][team][k][0];
+                sgh += slots[turn][team][k][1];
+            }
+        }
+        if (!mine || !dx) continue;
+        const float c1 = sg * rc, c2 = sgh * rc;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            float h[8], d[8];
+            widen8<FT>(cx[w], h);
+            widen8<FT>(cy[w], d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] = (h[i] - mu) * r;
+                d[i] = (d[i] * ww[w][i] - c1 - h[i] * c2) * r;
+            }
+            if (at[w].lo < 8) store8_own<FT>(dx, row * cols, at[w], d);
+        }
+    }
+    if (!part) return;
+    // the teams' sums, added in team order, first those of dw, then of db
+    float* to = part + (int64_t)blockIdx.x * 2 * ldp;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        if constexpr (TEAMS > 1) {
+            for (int k = 1; k < TEAMS; ++k) {
+                __syncthreads();
+                if (team == k) {
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) fold[(w * 8 + i) * NT + t] = o ? db[w][i] : dw[w][i];
+                }
+                __syncthreads();
+                if (team == 0) {
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) (o ? db : dw)[w][i] += fold[(w * 8 + i) * NT + t];
+                }
+            }
+        }
+        if (team == 0) {
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                if (at[w].lo < 8) store8_own<F32>(to + o * ldp, 0, at[w], o ? db[w] : dw[w]);
+        }
+    }
+}
+
+// Rows of any length: a workgroup per row for dx (two reads), and a second
+// kernel for the column sums, a workgroup per 256 columns and chunk of rows.
+template <int FT>
+__global__ __launch_bounds__(1024) void k_ln_bwd_loop(const void* __restrict__ dy, int64_t lddy,
+                                                      const void* __restrict__ x, int64_t ldx, int64_t cols,
+                                                      const void* __restrict__ weight, int wdt,
+                                                      const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                      void* __restrict__ dx)
+{
+    __shared__ float slots[2][16];
+    const int t = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const float mu = mean[row], r = rstd[row];
+    float sg = 0.0f, sgh = 0.0f;
+    for (int64_t j = t; j < cols; j += 1024) {
+        const float h = (load1<FT>(x, row * ldx + j) - mu) * r;
+        const float g = load1<FT>(dy, row * lddy + j) * load1_rt(weight, wdt, j, 1.0f);
+        sg += g;
+        sgh = __builtin_fmaf(g, h, sgh);
+    }
+    const float c1 = row_sum<1024>(sg, slots[0]) / (float)cols, c2 = row_sum<1024>(sgh, slots[1]) / (float)cols;
+    for (int64_t j = t; j < cols; j += 1024) {
+        const float h = (load1<FT>(x, row * ldx + j) - mu) * r;
+        const float g = load1<FT>(dy, row * lddy + j) * load1_rt(weight, wdt, j, 1.0f);
+        store1<FT>(dx, row * cols + j, (g - c1 - h * c2) * r);
+    }
+}
+
+template <int FT>
+__global__ __launch_bounds__(256) void k_ln_bwd_cols(const void* __restrict__ dy, int64_t lddy,
+                                                     const void* __restrict__ x, int64_t ldx, int64_t rows,
+                                                     int64_t cols, int64_t chunk, const float* __restrict__ mean,
+                                                     const float* __restrict__ rstd, float* __restrict__ part,
+                                                     int64_t ldp)
+{
+    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (j >= cols) return;
+    const int64_t r0 = blockIdx.y * chunk, r1 = r0 + chunk < rows ? r0 + chunk : rows;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        const float d = load1<FT>(dy, r * lddy + j);
+        dw = __builtin_fmaf(d, (load1<FT>(x, r * ldx + j) - mean[r]) * rstd[r], dw);
+        db += d;
+    }
+    float* to = part + (int64_t)blockIdx.y * 2 * ldp + j;
+    to[0] = dw;
+    to[ldp] = db;
+}
+
+// ------------------------------------------------------------- column sums
+// A workgroup takes 64 columns of one output: 16 lanes of four columns by 16
+// rows of partials at a time, then the 16 row sums in order through LDS.
+__global__ __launch_bounds__(256) void k_colsum(const float* __restrict__ part, int64_t parts, int outs, int64_t ld,
+                                                int64_t cols, void* __restrict__ out0, void* __restrict__ out1, int dt)
+{
+    __shared__ float4 sums[16][16];
+    const int o = blockIdx.y;
+    void* out = o ? out1 : out0;
+    if (!out) return;            // uniform in the workgroup
+    const int c4 = threadIdx.x & 15, rl = threadIdx.x >> 4;
+    const int64_t col = (int64_t)blockIdx.x * 64 + 4 * c4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (col < cols) {
+        for (int64_t p = rl; p < parts; p += 16) {
+            const float4 a = *reinterpret_cast<const float4*>(part + (p * outs + o) * ld + col);
+            s.x += a.x;
+            s.y += a.y;
+            s.z += a.z;
+            s.w += a.w;
+        }
+    }
+    sums[rl][c4] = s;
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const int c = threadIdx.x;
+    const int64_t j = (int64_t)blockIdx.x * 64 + c;
+    if (j >= cols) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += reinterpret_cast<const float*>(&sums[k][c >> 2])[c & 3];
+    store1_rt(out, dt, j, v);
+}
+
+void colsum_launch(const float* part, int64_t parts, int outs, int64_t ld, int64_t cols, void* out0, void* out1,
+                   int dt, hipStream_t st)
+{
+    const dim3 grid((unsigned)cdiv(cols, 64), out1 ? 2u : 1u);
+    hipLaunchKernelGGL(k_colsum, grid, dim3(256), 0, st, part, parts, outs, ld, cols, out0, out1, dt);
+}
+
+// ---------------------------------------------------------------- launches
+constexpr int64_t LN_HELD = 16384;       // longest row that a workgroup holds in registers
+constexpr int64_t LN_BWD_HELD = 8192;    // and with the column sums beside it, in the backward pass
+constexpr int64_t LN_PARTS = 256;        // workgroups of the backward pass, one row of partials each
+constexpr int64_t LN_COL_CHUNKS = 64;    // row chunks of the column kernel of long rows
+
+inline bool ln_held(int64_t cols, int64_t most) { return cols >= 8 && cols <= most; }
+
+template <int FT, int OUT>
+static void ln_launch(const void* x, int64_t ldx, int64_t rows, int64_t cols, const void* w, const void* b, int wdt,
+                      float eps, void* y, float* scale, float* mean, float* rstd, hipStream_t st)
+{
+#define TQ_LN(NT, W)                                                                                              \
+    hipLaunchKernelGGL((k_ln_rows<FT, NT, W, OUT>), dim3((unsigned)cdiv(rows, NT < 256 ? 256 / NT : 1)),          \
+                       dim3(NT < 256 ? 256 : NT), 0, st, x, ldx, rows, cols, w, b, wdt, eps, y, scale, mean, rstd)
+    if (!ln_held(cols, LN_HELD))
+        hipLaunchKernelGGL((k_ln_loop<FT, OUT>), dim3((unsigned)rows), dim3(1024), 0, st, x, ldx, cols, w, b, wdt, eps,
+                           y, scale, mean, rstd);
+    else if (cols <= 512) TQ_LN(64, 1);
+    else if (cols <= 1024) TQ_LN(64, 2);
+    else if (cols <= 2048) TQ_LN(256, 1);
+    else if (cols <= 4096) TQ_LN(256, 2);
+    else if (cols <= 8192) TQ_LN(512, 2);
+    else TQ_LN(1024, 2);
+#undef TQ_LN
+}
+
+// Workgroup count of the backward pass: the rows are dealt out evenly.
+inline int64_t ln_bwd_groups(int64_t rows, int teams)
+{
+    const int64_t want = cdiv(rows, teams);
+    return want < LN_PARTS ? want : LN_PARTS;
+}
+
+template <int FT>
+static void ln_bwd_launch(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows, int64_t cols,
+                          const void* w, int wdt, const float* mean, const float* rstd, void* dx, void* dw, void* db,
+                          float* ws, hipStream_t st)
+{
+    const int64_t ld = colsum_ld(cols);
+    float* part = dw || db ? ws : nullptr;
+    int64_t parts = 0;
+#define TQ_LNB(NT, W, BT)                                                                                         \
+    do {                                                                                                          \
+        parts = ln_bwd_groups(rows, BT / NT);                                                                     \
+        hipLaunchKernelGGL((k_ln_bwd<FT, NT, W, BT>), dim3((unsigned)parts), dim3(BT), 0, st, dy, lddy, x, ldx,   \
+                           rows, cols, w, wdt, mean, rstd, dx, part, ld);                                         \
+    } while (0)
+    if (!ln_held(cols, LN_BWD_HELD)) {
+        if (dx)
+            hipLaunchKernelGGL((k_ln_bwd_loop<FT>), dim3((unsigned)rows), dim3(1024), 0, st, dy, lddy, x, ldx, cols, w,
+                               wdt, mean, rstd, dx);
+        if (part) {
+            parts = rows < LN_COL_CHUNKS ? rows : LN_COL_CHUNKS;
+            const int64_t chunk = cdiv(rows, parts);
+            parts = cdiv(rows, chunk);
+            hipLaunchKernelGGL((k_ln_bwd_cols<FT>), dim3((unsigned)cdiv(cols, 256), (unsigned)parts), dim3(256), 0, st,
+                               dy, lddy, x, ldx, rows, cols, chunk, mean, rstd, part, ld);
+        }
+    }
+    else if (cols <= 512) TQ_LNB(64, 1, 512);
+    else if (cols <= 1024) TQ_LNB(64, 2, 512);
+    else if (cols <= 2048) TQ_LNB(128, 2, 512);
+    else if (cols <= 4096) TQ_LNB(256, 2, 512);
+    else TQ_LNB(512, 2, 512);
+#undef TQ_LNB
+    if (part) colsum_launch(part, parts, 2, ld, cols, dw, db, wdt, st);
+}
+
+__global__ __launch_bounds__(256) void k_zero_vec(void* __restrict__ p, int dt, int64_t n)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) store1_rt(p, dt, i, 0.0f);
+}
+
+void zero_vec_launch(void* p, int dt, int64_t n, hipStream_t st)
+{
+    if (p && n > 0) hipLaunchKernelGGL(k_zero_vec, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, st, p, dt, n);
+}
+
+static bool natural(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(ftype_size(dt) - 1)) == 0; }
+
+// A workgroup per row, and columns counted in 32 bits.
+static bool ln_fits(int64_t rows, int64_t cols)
+{
+    return rows <= 0x7fffffff && cols <= 0x7fffffff;
+}
+
+static tq_status ln_check(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void* w,
+                          const void* b, int wdt, float eps)
+{
+    if (!valid_ftype(x_dtype) || rows < 0 || cols < 0 || !(eps >= 0.0f)) return TQ_ERR_INVALID;
+    if ((w || b) && !valid_ftype(wdt)) return TQ_ERR_INVALID;
+    if (rows == 0 || cols == 0) return TQ_OK;
+    if (!x || ldx < cols) return TQ_ERR_INVALID;
+    if (!ln_fits(rows, cols)) return TQ_ERR_UNSUPPORTED;
+    if (!natural(x, x_dtype) || (w && !natural(w, wdt)) || (b && !natural(b, wdt))) return TQ_ERR_ALIGN;
+    return TQ_OK;
+}
+
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" {
+
+tq_status tq_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t x_row_stride,
+                        const void* weight, const void* bias, int w_dtype, float eps, void* y, float* mean,
+                        float* rstd, void* stream)
+{
+    const tq_status s = ln_check(x, x_dtype, rows, cols, x_row_stride, weight, bias, w_dtype, eps);
+    if (s != TQ_OK || rows == 0 || cols == 0) return s;
+    if (!y) return TQ_ERR_INVALID;
+    if (!natural(y, x_dtype) || !natural(mean, TQ_F32) || !natural(rstd, TQ_F32)) return TQ_ERR_ALIGN;
+    TQ_LLM_FT_SWITCH(x_dtype, (ln_launch<FTV, OUT_Y>(x, x_row_stride, rows, cols, weight, bias, w_dtype, eps, y,
+                                                     nullptr, mean, rstd, as_stream(stream))));
+    return launch_status();
+}
+
+tq_status tq_layer_norm_quant_per_token(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t x_row_stride,
+                                        const void* weight, const void* bias, int w_dtype, float eps, int8_t* q,
+                                        float* scale, float* mean, float* rstd, void* stream)
+{
+    const tq_status s = ln_check(x, x_dtype, rows, cols, x_row_stride, weight, bias, w_dtype, eps);
+    if (s != TQ_OK || rows == 0 || cols == 0) return s;
+    if (!q || !scale) return TQ_ERR_INVALID;
+    if (!natural(scale, TQ_F32) || !natural(mean, TQ_F32) || !natural(rstd, TQ_F32)) return TQ_ERR_ALIGN;
+    TQ_LLM_FT_SWITCH(x_dtype, (ln_launch<FTV, OUT_S8>(x, x_row_stride, rows, cols, weight, bias, w_dtype, eps, q,
+                                                      scale, mean, rstd, as_stream(stream))));
+    return launch_status();
+}
+
+size_t tq_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0) return 0;
+    const int64_t parts = ln_held(cols, LN_BWD_HELD) ? LN_PARTS : LN_COL_CHUNKS;
+    return (size_t)(rows < parts ? rows : parts) * 2 * (size_t)colsum_ld(cols) * sizeof(float);
+}
+
+tq_status tq_layer_norm_backward(const void* dy, const void* x, int x_dtype, int64_t rows, int64_t cols,
+                                 int64_t dy_row_stride, int64_t x_row_stride, const void* weight, int w_dtype,
+                                 const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream)
+{
+    if ((dweight || dbias) && !valid_ftype(w_dtype)) return TQ_ERR_INVALID;
+    const tq_status s = ln_check(x, x_dtype, rows, cols, x_row_stride, weight, nullptr, w_dtype, 0.0f);
+    if (s != TQ_OK || cols == 0) return s;
+    if ((dweight && !natural(dweight, w_dtype)) || (dbias && !natural(dbias, w_dtype))) return TQ_ERR_ALIGN;
+    hipStream_t st = as_stream(stream);
+    if (rows == 0) {             // no rows: the sums are empty, not unwritten
+        zero_vec_launch(dweight, w_dtype, cols, st);
+        zero_vec_launch(dbias, w_dtype, cols, st);
+        return launch_status();
+    }
+    if (!dy || !mean || !rstd || dy_row_stride < cols) return TQ_ERR_INVALID;
+    if (!dx && !dweight && !dbias) return TQ_OK;
+    if (!natural(dy, x_dtype) || !natural(dx, x_dtype) || !natural(mean, TQ_F32) || !natural(rstd, TQ_F32))
+        return TQ_ERR_ALIGN;
+    if (dweight || dbias) {
+        if (!workspace || workspace_bytes < tq_layer_norm_backward_workspace_bytes(rows, cols)) return TQ_ERR_INVALID;
+        if (!aligned16(workspace)) return TQ_ERR_ALIGN;
+    }
+    TQ_LLM_FT_SWITCH(x_dtype, (ln_bwd_launch<FTV>(dy, dy_row_stride, x, x_row_stride, rows, cols, weight, w_dtype, mean,
+                                                  rstd, dx, dweight, dbias, static_cast<float*>(workspace), st)));
+    return launch_status();
+}
+
+}  // extern "C"
