@@ -9,6 +9,8 @@
 // order of operations, and y (and z, where it is asked for) is rounded once.
 #include "tq_llm.h"
 
+#include <type_traits>
+
 namespace tq {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -29,34 +31,48 @@ __device__ __forceinline__ Logistic logistic(float u)
     return r;
 }
 
+// v / (1 + 2^x): where 2^x overflows the quotient is v's zero.
+__device__ __forceinline__ float times_logistic(float v, float x)
+{
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
+}
+
 constexpr float GELU_C = 0.79788456080286535588f;      // sqrt(2 / pi)
 constexpr float GELU_A = 0.044715f;
 constexpr float SQRT_HALF = 0.70710678118654752440f;
 
-// act(v) of eight values; the branch on `act` is uniform.  The tanh form of
-// gelu is v times a logistic: (1 + tanh u) / 2 = 1 / (1 + exp(-2u)).
-__device__ __forceinline__ void act8(int act, float v[8])
+// act(v).  The tanh form of gelu is v times a logistic: (1 + tanh u) / 2 = 1 /
+// (1 + exp(-2u)).
+template <int ACT>
+__device__ __forceinline__ float act1(float v)
+{
+    if constexpr (ACT == TQ_ACT_RELU) return v > 0.0f || v != v ? v : 0.0f;
+    else if constexpr (ACT == TQ_ACT_SILU) return times_logistic(v, -LOG2E * v);
+    else if constexpr (ACT == TQ_ACT_GELU) return 0.5f * v * erfcf(-v * SQRT_HALF);
+    else if constexpr (ACT == TQ_ACT_GELU_TANH)
+        return times_logistic(v, v * __builtin_fmaf(-2.0f * LOG2E * GELU_C * GELU_A * v, v, -2.0f * LOG2E * GELU_C));
+    else return v;
+}
+
+// f(integral constant of `act`): one uniform branch for what f does with it.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f)
 {
     switch (act) {
-    case TQ_ACT_RELU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] > 0.0f || v[i] != v[i] ? v[i] : 0.0f;
-        break;
-    case TQ_ACT_SILU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * logistic(v[i]).p;
-        break;
-    case TQ_ACT_GELU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.5f * v[i] * erfcf(-v[i] * SQRT_HALF);
-        break;
-    case TQ_ACT_GELU_TANH:
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = v[i] * logistic(2.0f * GELU_C * v[i] * __builtin_fmaf(GELU_A * v[i], v[i], 1.0f)).p;
-        break;
-    default: break;
+    case TQ_ACT_RELU: f(std::integral_constant<int, TQ_ACT_RELU>()); break;
+    case TQ_ACT_SILU: f(std::integral_constant<int, TQ_ACT_SILU>()); break;
+    case TQ_ACT_GELU: f(std::integral_constant<int, TQ_ACT_GELU>()); break;
+    case TQ_ACT_GELU_TANH: f(std::integral_constant<int, TQ_ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, TQ_ACT_NONE>()); break;
     }
+}
+
+__device__ __forceinline__ void act8(int act, float v[8])
+{
+    with_act(act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act1<decltype(a)::value>(v[i]);
+    });
 }
 
 // d[i] *= act'(z[i]).  A slope's second term v p' vanishes with p' (a value
@@ -107,53 +123,82 @@ struct Epi {
     int64_t M, N;
 };
 
-// Eight consecutive columns col .. col + 7 of one row, from their sums.
 template <int YT>
-__device__ __forceinline__ void epilogue8(const Epi& e, int64_t row, int64_t col, const int acc[8])
+__device__ __forceinline__ void store8_first(void* p, int64_t at, int n, const float v[8])
 {
-    const float sx = e.sx[row];
-    const int64_t at = row * e.N + col;
-    float v[8];
-    if (col + 8 <= e.N) {
-        float sw[8], b[8];
-        widen8<F32>(load8_any<F32>(e.sw, col), sw);
-        const RawAny rb = load8_rt(e.bias, e.bias_dt, col);
-        Raw8<YT> rr;
-        if (e.res) rr = load8_any<YT>(e.res, row * e.ldr + col);
-        widen8_rt(rb, e.bias, e.bias_dt, 0.0f, b);
+    if (n == 8) {
+        store8_any<YT>(p, at, v);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)acc[i] * sx * sw[i];
-        if (e.bias) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += b[i];
-        }
-        if (e.z) store8_any<YT>(e.z, at, v);
-        act8(e.act, v);
-        if (e.res) {
-            float r[8];
-            widen8<YT>(rr, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
-        }
-        store8_any<YT>(e.y, at, v);
+        for (int i = 0; i < 8; ++i)
+            if (i < n) store1<YT>(p, at + i, v[i]);
+    }
+}
+
+// What eight columns col .. col + 7 need for every row: scales and bias (zeros
+// past N), and how many of them there are.
+struct Cols8 {
+    int64_t col;
+    int n;
+    float sw[8], b[8];
+};
+__device__ __forceinline__ Cols8 cols8(const Epi& e, int64_t col)
+{
+    Cols8 c;
+    c.col = col;
+    c.n = e.N - col >= 8 ? 8 : e.N - col > 0 ? (int)(e.N - col) : 0;
+    if (c.n == 8) {
+        widen8<F32>(load8_any<F32>(e.sw, col), c.sw);
+        widen8_rt(load8_rt(e.bias, e.bias_dt, col), e.bias, e.bias_dt, 0.0f, c.b);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[i] = 0.0f;
-            if (col + i < e.N) {
-                v[i] = (float)acc[i] * sx * e.sw[col + i];
-                if (e.bias) v[i] += load1_rt(e.bias, e.bias_dt, col + i, 0.0f);
-                if (e.z) store1<YT>(e.z, at + i, v[i]);
-            }
+            c.sw[i] = i < c.n ? e.sw[col + i] : 0.0f;
+            c.b[i] = i < c.n ? load1_rt(e.bias, e.bias_dt, col + i, 0.0f) : 0.0f;
         }
-        act8(e.act, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < e.N) {
-                if (e.res) v[i] += load1<YT>(e.res, row * e.ldr + col + i);
-                store1<YT>(e.y, at + i, v[i]);
-            }
     }
+    return c;
+}
+
+// The residual of those columns in one row (apart from its use, so that it can
+// be loaded ahead); e.res is not null.
+template <int YT>
+__device__ __forceinline__ Raw8<YT> residual8(const Epi& e, const Cols8& c, int64_t row)
+{
+    if (c.n == 8) return load8_any<YT>(e.res, row * e.ldr + c.col);
+    Raw8<YT> r = {};
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < c.n) {
+            if constexpr (YT == F32) w[i] = as_u(load1<F32>(e.res, row * e.ldr + c.col + i));
+            else w[i / 2] |= (uint32_t)static_cast<const uint16_t*>(e.res)[row * e.ldr + c.col + i] << (16 * (i & 1));
+        }
+    return r;
+}
+
+// Finishes eight columns of one row from their sums.
+template <int YT>
+__device__ __forceinline__ void epilogue8(const Epi& e, const Cols8& c, int64_t row, float sx, const int acc[8],
+                                          const Raw8<YT>& res)
+{
+    const int64_t at = row * e.N + c.col;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)acc[i] * sx * c.sw[i];
+    if (e.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += c.b[i];
+    }
+    if (e.z) store8_first<YT>(e.z, at, c.n, v);
+    act8(e.act, v);
+    if (e.res) {
+        float r[8];
+        widen8<YT>(res, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+    store8_first<YT>(e.y, at, c.n, v);
 }
 
 // Sixteen codes at any byte address, zeros from code K of the row on.
@@ -246,7 +291,8 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
         for (int v = 0; v < NWV; ++v)
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] += sums[v][m][c + i];
-        epilogue8<YT>(e, m, n0 + c, s);
+        const Cols8 cc = cols8(e, n0 + c);
+        epilogue8<YT>(e, cc, m, e.sx[m], s, e.res ? residual8<YT>(e, cc, m) : Raw8<YT>{});
     }
 }
 
@@ -259,35 +305,148 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
 // end each wave lays its quarter out in LDS and finishes it eight columns at a
 // time, so that stores are whole and the epilogue's code exists once.
 constexpr int ET = 128;
-constexpr int EPITCH = 68;               // ints between rows of a staged quarter
 __device__ __forceinline__ int eslot(int row, int chunk) { return row * ET + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
-// Finishes a wave's 64 x 64 sums acc[i][j][r] = row 16 i + l % 16, column
-// 16 j + 4 (l / 16) + r through its own part of LDS.
-template <int YT>
-__device__ __forceinline__ void finish64(const Epi& e, int64_t m0, int64_t n0, const v4i (&acc)[4][4], int* stage)
+// A lane's own part of a staged half: 32 rows of 16 NT sums, 4 apart beyond
+// them so that sixteen rows' 16-byte stores spread over the banks, and the row
+// scales of all 16 NT rows behind them.
+template <int NT>
+struct Stage {
+    static constexpr int PITCH = 16 * NT + 4, LPR = 2 * NT, RPI = 64 / LPR;   // lanes per row, rows per instruction
+    static constexpr int INTS = 32 * PITCH + 16 * NT;
+};
+
+template <int NT>
+__device__ __forceinline__ void stage_scales(const Epi& e, int64_t m0, int* stage)
+{
+    const int lane = threadIdx.x & 63;
+    float* sx = reinterpret_cast<float*>(stage + 32 * Stage<NT>::PITCH);
+#pragma unroll
+    for (int i = 0; i < NT / 4; ++i) {
+        const int64_t row = m0 + 64 * i + lane;
+        sx[64 * i + lane] = e.sx[row < e.M ? row : e.M - 1];
+    }
+}
+
+// acc[i][j][r] = row 16 i + l % 16, column 16 j + 4 (l / 16) + r.  A wave's LDS
+// accesses stay in order; the fences keep the compiler's in order too.
+template <int NT>
+__device__ __forceinline__ void stage_half(int h, const v4i (&acc)[NT][NT], int* stage)
 {
     const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<v4i*>(&stage[(16 * i + l16) * EPITCH + 16 * j + 4 * g4]) = acc[i][j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int c = 8 * (lane & 7);
-    if (n0 + c >= e.N) return;
-    for (int r = lane >> 3; r < 64; r += 8) {
-        if (m0 + r >= e.M) break;
-        int s[8];
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<v4i*>(&stage[(16 * i + l16) * Stage<NT>::PITCH + 16 * j + 4 * g4]) = acc[2 * h + i][j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// A quarter that lies inside the output: no bounds, the activation and the
+// residual known, 32-bit offsets from the quarter's corner, two rows' worth of
+// independent work at a time.
+template <int YT, int NT, int ACT, bool RES, bool NTS>
+__device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int64_t m0, int64_t n0,
+                                              const v4i (&acc)[NT][NT], int* stage)
+{
+    using S = Stage<NT>;
+    constexpr int ES = YT == F32 ? 4 : 2;
+    const int lane = threadIdx.x & 63;
+    const int c = 8 * (lane % S::LPR), r0 = lane / S::LPR;
+    const float* sx = reinterpret_cast<const float*>(stage + 32 * S::PITCH);
+    char* y = static_cast<char*>(e.y) + (m0 * e.N + n0) * ES;
+    const char* res = RES ? static_cast<const char*>(e.res) + (m0 * e.ldr + n0) * ES : nullptr;
+    const uint32_t ystep = (uint32_t)e.N * ES, rstep = (uint32_t)e.ldr * ES;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const v4i v = *reinterpret_cast<const v4i*>(&stage[r * EPITCH + c + 4 * h]);
+    for (int h = 0; h < NT / 2; ++h) {
+        stage_half<NT>(h, acc, stage);
+        uint32_t yo = (uint32_t)(32 * h + r0) * ystep + c * ES, ro = (uint32_t)(32 * h + r0) * rstep + c * ES;
+#pragma unroll 1
+        for (int r = r0; r < 32; r += 2 * S::RPI) {
+            Raw8<YT> rr[2];
+            float v[2][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[4 * h + i] = v[i];
+            for (int k = 0; k < 2; ++k)
+                if constexpr (RES) rr[k] = load8_off<YT>(res, ro + k * S::RPI * rstep);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int* p = &stage[(r + k * S::RPI) * S::PITCH + c];
+                const v4i s0 = *reinterpret_cast<const v4i*>(p), s1 = *reinterpret_cast<const v4i*>(p + 4);
+                const float sc = sx[32 * h + r + k * S::RPI];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = (float)(i < 4 ? s0[i] : s1[i - 4]) * sc * cc.sw[i];
+            }
+            if (e.bias) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] += cc.b[i];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = act1<ACT>(v[k][i]);
+                if constexpr (RES) {
+                    float w[8];
+                    widen8<YT>(rr[k], w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] += w[i];
+                }
+                store8_off<YT, NTS>(y, yo + k * S::RPI * ystep, v[k]);
+            }
+            yo += 2 * S::RPI * ystep;
+            ro += 2 * S::RPI * rstep;
         }
-        epilogue8<YT>(e, m0 + r, n0 + c, s);
     }
+}
+
+// Any quarter: bounds, and the value before the activation where it is asked
+// for.
+template <int YT, int NT>
+__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, const v4i (&acc)[NT][NT],
+                                           int* stage)
+{
+    using S = Stage<NT>;
+    const int lane = threadIdx.x & 63;
+    const int c = 8 * (lane % S::LPR), r0 = lane / S::LPR;
+    const float* sx = reinterpret_cast<const float*>(stage + 32 * S::PITCH);
+#pragma unroll
+    for (int h = 0; h < NT / 2; ++h) {
+        const int64_t mh = m0 + 32 * h;
+        if (mh >= e.M) return;           // uniform
+        stage_half<NT>(h, acc, stage);
+        const int rows = cc.n == 0 ? 0 : e.M - mh < 32 ? (int)(e.M - mh) : 32;
+#pragma unroll 1
+        for (int r = r0; r < rows; r += S::RPI) {
+            Raw8<YT> res = {};
+            if (e.res) res = residual8<YT>(e, cc, mh + r);
+            const v4i s0 = *reinterpret_cast<const v4i*>(&stage[r * S::PITCH + c]);
+            const v4i s1 = *reinterpret_cast<const v4i*>(&stage[r * S::PITCH + c + 4]);
+            const int s[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
+            epilogue8<YT>(e, cc, mh + r, sx[32 * h + r], s, res);
+        }
+    }
+}
+
+// A wave's square of 16 NT sums, 32 rows at a time through the wave's own part
+// of LDS, so that its stores are whole rows of the square and the epilogue's
+// code exists once per activation.  A lane keeps its eight columns for all
+// rows, so their scales and bias are read once.
+template <int YT, int NT, bool NTS = false>
+__device__ __forceinline__ void finish_quarter(const Epi& e, int64_t m0, int64_t n0, const v4i (&acc)[NT][NT],
+                                               int* stage)
+{
+    const Cols8 cc = cols8(e, n0 + 8 * ((threadIdx.x & 63) % Stage<NT>::LPR));
+    if (m0 >= e.M) return;               // uniform
+    stage_scales<NT>(e, m0, stage);
+    const bool inside = m0 + 16 * NT <= e.M && n0 + 16 * NT <= e.N && e.N <= 1 << 22 && e.ldr <= 1 << 22;
+    if (inside && !e.z)
+        with_act(e.act, [&](auto a) {
+            if (e.res) finish_inside<YT, NT, decltype(a)::value, true, NTS>(e, cc, m0, n0, acc, stage);
+            else finish_inside<YT, NT, decltype(a)::value, false, NTS>(e, cc, m0, n0, acc, stage);
+        });
+    else finish_any<YT, NT>(e, cc, m0, acc, stage);
 }
 
 template <int YT>
@@ -296,7 +455,7 @@ __global__ __launch_bounds__(256) void k_epi_tile(const int8_t* __restrict__ qx,
 {
     __shared__ __attribute__((aligned(16))) union {
         uint8_t in[2][2][ET * ET];
-        int out[4][64 * EPITCH];
+        int out[4][Stage<4>::INTS];
     } lds;
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l16 = lane & 15, g4 = lane >> 4, wm = w >> 1, wn = w & 1;
@@ -353,7 +512,211 @@ __global__ __launch_bounds__(256) void k_epi_tile(const int8_t* __restrict__ qx,
         }
     }
     __syncthreads();                     // the operands give way to the staged sums
-    finish64<YT>(e, m0 + 64 * wm, n0 + 64 * wn, acc, lds.out[w]);
+    finish_quarter<YT, 4>(e, m0 + 64 * wm, n0 + 64 * wn, acc, lds.out[w]);
+}
+
+// k_epi_ring: operands whose rows start at 16-byte addresses.  A TILE x TILE
+// output tile per workgroup of four waves, wave w the quarter (w / 2, w % 2),
+// so each operand byte that enters LDS meets TILE products and each one read
+// from LDS TILE / 2.  LDS is a ring of RING units, a unit one operand's
+// [TILE x 128 codes] slice: unit 2 kb holds the activations of block kb, unit
+// 2 kb + 1 its weights.  Units arrive by direct global -> LDS loads (lane l of
+// an instruction writes 16 bytes at base + 16 l, so the swizzle of eslot is
+// applied to the address it reads).  A block is two 64-code steps; while the
+// matrix cores work on one step's operands the next step's are read from LDS
+// into a second set of registers.  One barrier per block, between its steps:
+// there every wave has read both units, so their slots are refilled with the
+// units RING ahead, and the next block's units have landed (those after it may
+// still be on their way: the wait counts loads, it does not drain them).
+//
+// Where K is no multiple of 128, the block that the rest makes comes first
+// (integer sums have no order): its missing chunks come from sixteen zero
+// bytes on the weights' side, and the activations' side reads any valid chunk
+// there.  All later loads are whole.
+//
+// The products are issued from asm that adds in place: the compiler, left to
+// choose, gives the sums new registers and moves them back, and a 256 x 256
+// tile's sums take all 256 accumulation registers.
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ const uint4 zero_codes = {0, 0, 0, 0};
+
+// The loads are issued from asm, so that the compiler adds no wait of its own
+// for them (they count in vmcnt; the kernel waits explicitly): every lane
+// writes 16 bytes at M0 + 16 * lane.  Nothing else uses M0.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ uint64_t uniform_address(const void* p)
+{
+    const uint64_t v = (uint64_t)(size_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ void lds_load(uint64_t base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load_at(const void* g, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// c += w x, 16 x 16 x 64 codes.  The sums of one tile are next touched NT^2
+// products later, far behind the matrix core's own latency.
+__device__ __forceinline__ void add_product(v4i& c, v4i w, v4i x)
+{
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(w), "v"(x));
+}
+
+// The wait instruction's operand: at most `vm` loads and `lgkm` LDS accesses
+// still under way.
+constexpr int WAIT(int vm, int lgkm) { return (vm & 15) | (vm >> 4) << 14 | 0x70 | lgkm << 8; }
+
+// Tile of a workgroup.  Workgroup i of a launch goes to XCD i % 8; the launch
+// index is renumbered so that each XCD (each L2) takes one contiguous run of
+// tiles, walked in slabs of up to `slab` column tiles, columns fastest.
+__device__ __forceinline__ void tile_of(int64_t nt, int64_t mt, int slab, int64_t& tm, int64_t& tn)
+{
+    const int64_t T = nt * mt, i = blockIdx.x;
+    const int64_t xcd = i % 8, loc = i / 8, q = T / 8, r = T % 8;
+    const int64_t L = xcd < r ? xcd * (q + 1) + loc : r * (q + 1) + (xcd - r) * q + loc;
+    const int64_t per = (int64_t)slab * mt, first = (L / per) * slab;
+    const int64_t wide = nt - first < slab ? nt - first : slab;
+    const int64_t at = L % per;
+    tn = first + at % wide;
+    tm = at / wide;
+}
+
+template <int YT, int TILE, int RING, int WGS>
+__global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
+                                                     int64_t K, int64_t nt, int64_t mt, int slab, Epi e)
+{
+    constexpr int UNIT = TILE * ET;      // bytes of a unit
+    constexpr int U = TILE / 32;         // loads per wave and unit
+    constexpr int Q = TILE / 2;          // rows and columns of a wave's quarter
+    constexpr int NT = Q / 16;           // 16-wide tiles along either side of it
+    constexpr int AHEAD = (RING - 4) * U;   // loads that may be in flight behind the next block's
+    constexpr int PER = NT / 2;          // products per LDS read
+    __shared__ __attribute__((aligned(16))) uint8_t ring[RING * UNIT];
+
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int l16 = lane & 15, g4 = lane >> 4, wm = w >> 1, wn = w & 1;
+    int64_t tm, tn;
+    tile_of(nt, mt, slab, tm, tn);
+    const int64_t m0 = tm * TILE, n0 = tn * TILE;
+    const int nkb = (int)((K + ET - 1) / ET);
+
+    // loads of a unit: instruction q of wave w fills rows Q/2 w + 8 q .. + 7, lane l row l / 8, slot l % 8
+    const int fr = (TILE / 4) * w + (lane >> 3);
+    const int8_t* ga = qx + m0 * K;
+    const int8_t* gb = qw + n0 * K;
+    uint32_t oa[U], ob[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        const int r = fr + 8 * q;
+        const int ra = m0 + r < e.M ? r : (int)(e.M - 1 - m0), rb = n0 + r < e.N ? r : (int)(e.N - 1 - n0);
+        const uint32_t chunk = (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) << 4);
+        oa[q] = (uint32_t)ra * (uint32_t)K + chunk;
+        ob[q] = (uint32_t)rb * (uint32_t)K + chunk;
+    }
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_void*)ring) + (uint32_t)w * (UNIT / 4);
+    const int rest = K % ET != 0;        // block 0 is the rest, block kb > 0 starts at code (kb - rest) 128
+    const int64_t k_rest = K / ET * ET;
+    auto load_unit = [&](int unit, int slot) {
+        const int b = unit >> 1;
+        const int64_t k0 = rest && b == 0 ? k_rest : (int64_t)(b - rest) * ET;
+        const bool weights = unit & 1;
+        const int8_t* base = (weights ? gb : ga) + k0;
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int chunk = (lane & 7) ^ (((fr + 8 * q) >> 1) & 7);
+            const int8_t* p = base + (weights ? ob[q] : oa[q]);
+            const bool in = k0 + 16 * chunk < K;
+            const void* from = in ? (const void*)p : weights ? (const void*)&zero_codes : (const void*)(p - 16 * chunk);
+            lds_load_at(from, lds0 + (uint32_t)slot * UNIT + 1024u * q);
+        }
+    };
+
+    v4i acc[NT][NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = v4i{};
+
+    // lane l reads row l % 16, chunk 4 s + l / 16 of a tile of 16 rows
+    const int key = l16 >> 1;
+    const int la[2] = {(Q * wm + l16) * ET + ((g4 ^ key) << 4), (Q * wm + l16) * ET + (((4 + g4) ^ key) << 4)};
+    const int lb[2] = {(Q * wn + l16) * ET + ((g4 ^ key) << 4), (Q * wn + l16) * ET + (((4 + g4) ^ key) << 4)};
+    v4i av[2][NT], bv[2][NT];
+
+    const int units = 2 * nkb;
+    int sa = 0, sb = 1;                  // slots of the present block's units
+    for (int u = 0; u < (units < RING ? units : RING); ++u) load_unit(u, u);
+    if (units >= RING) __builtin_amdgcn_s_waitcnt(WAIT((RING - 2) * U, 15));
+    else __builtin_amdgcn_s_waitcnt(WAIT(0, 15));
+    asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        av[0][i] = *reinterpret_cast<const v4i*>(&ring[sa * UNIT + la[0] + 16 * ET * i]);
+        bv[0][i] = *reinterpret_cast<const v4i*>(&ring[sb * UNIT + lb[0] + 16 * ET * i]);
+    }
+    // RING is odd: the units to come at block kb are the weights of block kb + RING / 2 and the activations after
+    uint64_t wnext = uniform_address(gb + (int64_t)(RING / 2 - rest) * ET);
+    uint64_t xnext = uniform_address(ga + (int64_t)(RING / 2 + 1 - rest) * ET);
+    for (int kb = 0; kb < nkb; ++kb, wnext += ET, xnext += ET) {
+        const uint8_t* pa = ring + sa * UNIT + la[1];
+        const uint8_t* pb = ring + sb * UNIT + lb[1];
+        __builtin_amdgcn_s_waitcnt(WAIT(63, 0));   // the first step's operands, before more reads join them
+#pragma unroll
+        for (int g = 0; g < 2 * NT; ++g) {   // first step's products, second step's operands
+            if (g < NT) {
+                bv[1][g] = *reinterpret_cast<const v4i*>(pb + 16 * ET * g);
+                av[1][g] = *reinterpret_cast<const v4i*>(pa + 16 * ET * g);
+            }
+#pragma unroll
+            for (int x = 0; x < PER; ++x) add_product(acc[g / 2][PER * (g % 2) + x], bv[0][PER * (g % 2) + x], av[0][g / 2]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // both units read (lgkmcnt 0); the next block's two have landed
+        const int next = 2 * kb + RING;
+        if (next <= units) __builtin_amdgcn_s_waitcnt(WAIT(AHEAD, 0));
+        else __builtin_amdgcn_s_waitcnt(WAIT(0, 0));
+        asm volatile("s_barrier" ::: "memory");
+        const uint32_t fa = lds0 + (uint32_t)sa * UNIT, fb = lds0 + (uint32_t)sb * UNIT;
+        const bool more_w = next < units, more_x = next + 1 < units;
+        sa = sa + 2 < RING ? sa + 2 : sa + 2 - RING;
+        sb = sb + 2 < RING ? sb + 2 : sb + 2 - RING;
+        // after the last block these slots hold older units, whose operands no product takes
+        const uint8_t* na = ring + sa * UNIT + la[0];
+        const uint8_t* nb = ring + sb * UNIT + lb[0];
+#pragma unroll
+        for (int g = 0; g < 2 * NT; ++g) {   // second step's products, the next block's first operands
+            if (g < NT) {
+                bv[0][g] = *reinterpret_cast<const v4i*>(nb + 16 * ET * g);
+                av[0][g] = *reinterpret_cast<const v4i*>(na + 16 * ET * g);
+            }
+            if (g < U) {
+                if (more_w) lds_load(wnext, ob[g], fa + 1024u * g);
+            } else if (g < 2 * U) {
+                if (more_x) lds_load(xnext, oa[g - U], fb + 1024u * (g - U));
+            }
+#pragma unroll
+            for (int x = 0; x < PER; ++x) add_product(acc[g / 2][PER * (g % 2) + x], bv[1][PER * (g % 2) + x], av[1][g / 2]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // The last products' sums need up to 19 wait states before they are read, which the compiler cannot see behind
+    // asm; the empty statements after the wait, in order as volatile asm is, keep every read behind it.
+    asm volatile("s_nop 15\n\ts_nop 7");
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    asm volatile("s_barrier" ::: "memory");   // the ring gives way to the staged sums
+    finish_quarter<YT, NT, TILE == 256>(e, m0 + Q * wm, n0 + Q * wn, acc, reinterpret_cast<int*>(ring) + w * (RING * UNIT / 16));
 }
 
 // ------------------------------------------------------ backward of epilogue
@@ -469,6 +832,20 @@ static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const 
         return;
     }
 #undef TQ_FEW
+    if (K >= ET && K % 16 == 0 && aligned16(qx) && aligned16(qw)) {
+#define TQ_RING(TILE, RING, WGS)                                                                             \
+    do {                                                                                                     \
+        const int64_t nt = cdiv(e.N, TILE), mt = cdiv(e.M, TILE);                                            \
+        const int slab = (int)std::min<int64_t>(cdiv(nt, 8), 16);                                            \
+        hipLaunchKernelGGL((k_epi_ring<YT, TILE, RING, WGS>), dim3((unsigned)(nt * mt)), dim3(256), 0, st, qx, qw, \
+                           K, nt, mt, slab, e);                                                              \
+    } while (0)
+        if (cdiv(e.M, 256) * cdiv(e.N, 256) >= 256) TQ_RING(256, 5, 1);
+        else if (cdiv(e.M, 128) * cdiv(e.N, 128) > 256) TQ_RING(128, 5, 2);
+        else TQ_RING(128, 9, 1);
+#undef TQ_RING
+        return;
+    }
     const dim3 grid((unsigned)cdiv(e.N, ET), (unsigned)cdiv(e.M, ET));
     hipLaunchKernelGGL((k_epi_tile<YT>), grid, dim3(256), 0, st, qx, qw, K, e);
 }
