@@ -135,11 +135,18 @@ def _call(name, *args):
 
 # ------------------------------------------------------------ marshalling
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the device's current stream as an integer (torch's own accessor builds a
+# Stream object first, 1.9 us against 0.1: a sixth of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _ft(t):
@@ -805,36 +812,42 @@ def tq_fp4_linear(x, packed, block_scale, global_scale, kind="nvfp4", out_dtype=
 
 # ------------------------------------------------------------------ layer norm
 def _rows_of(t, name):
-    """(rows, cols, row stride) of t viewed as [rows, cols], its leading
+    """(t, rows, cols, row stride) of t viewed as [rows, cols], its leading
     dimensions flattened; copies t only where they do not flatten."""
-    _ft(t)
+    if t.dtype not in FTYPE:
+        raise TypeError("unsupported float dtype %s" % t.dtype)
     if not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-    if t.dim() == 0:
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        if t.is_contiguous():
+            return t, rows, cols, cols
+        if t.stride(1) == 1 and (rows <= 1 or t.stride(0) >= cols):
+            return t, rows, cols, t.stride(0) if rows > 1 else cols
+    elif not shape:
         raise ValueError("%s needs at least one dimension" % name)
-    cols = t.shape[-1]
-    if t.dim() != 2 or t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < cols):
-        if not t.is_contiguous():
-            t = t.contiguous()
-        return t, (t.numel() // cols if cols else 0), cols, cols
-    return t, t.shape[0], cols, t.stride(0) if t.shape[0] > 1 else cols
+    t = t.contiguous()
+    cols = shape[-1]
+    return t, (t.numel() // cols if cols else 0), cols, cols
 
 
 def _params(x, cols, weight, bias):
-    """The parameters' common type; the tensors checked against the row."""
+    """weight and bias checked against the row, and their common type."""
     dt = None
     for name, p in (("weight", weight), ("bias", bias)):
         if p is None:
             continue
-        if p.device != x.device or p.shape != (cols,):
+        if p.shape != (cols,) or p.device != x.device:
             raise ValueError("%s must be a vector of %d elements on x's device" % (name, cols))
         if dt is not None and p.dtype != dt:
             raise ValueError("weight and bias must have one type")
         dt = p.dtype
-    if dt is not None and dt not in FTYPE:
+    if dt is None:
+        return None, None, 0
+    if dt not in FTYPE:
         raise TypeError("unsupported float dtype %s" % dt)
-    return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous(),
-            FTYPE[dt if dt is not None else torch.float32])
+    return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous(), FTYPE[dt])
 
 
 def _row_vector(t, rows, x, name):
@@ -843,16 +856,25 @@ def _row_vector(t, rows, x, name):
     return t.contiguous()
 
 
+def _f32(dev, *shape):
+    return torch.empty(shape, dtype=torch.float32, device=dev)
+
+
+def _workspace(dev, nbytes):
+    return torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+
+
 def tq_layer_norm(x, weight=None, bias=None, eps=1e-5):
     """Layer norm over the last dimension: (y, mean, rstd), y in x's type and
     shape, mean and rstd float32 with one value per row."""
     xr, rows, cols, ld = _rows_of(x, "x")
     w, b, wdt = _params(x, cols, weight, bias)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    _call("tq_layer_norm", _ptr(xr), _ft(x), rows, cols, ld, _ptr(w), _ptr(b), wdt, eps, _ptr(y), _ptr(mean),
-          _ptr(rstd), _stream(x.device))
+    dev = x.device
+    y = torch.empty_like(xr, memory_format=torch.contiguous_format)
+    mean = _f32(dev, rows)
+    rstd = torch.empty_like(mean)
+    _call("tq_layer_norm", xr.data_ptr(), FTYPE[x.dtype], rows, cols, ld, _ptr(w), _ptr(b), wdt, eps, y.data_ptr(),
+          mean.data_ptr(), rstd.data_ptr(), _stream(dev))
     return y, mean, rstd
 
 
@@ -862,12 +884,13 @@ def tq_layer_norm_quant_per_token(x, weight=None, bias=None, eps=1e-5, stats=Fal
     rstd, for the backward pass."""
     xr, rows, cols, ld = _rows_of(x, "x")
     w, b, wdt = _params(x, cols, weight, bias)
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    kept = torch.empty((2, rows), dtype=torch.float32, device=x.device) if stats else None
-    _call("tq_layer_norm_quant_per_token", _ptr(xr), _ft(x), rows, cols, ld, _ptr(w), _ptr(b), wdt, eps, _ptr(q),
-          _ptr(scale), _ptr(kept[0]) if stats else None, _ptr(kept[1]) if stats else None, _stream(x.device))
-    return (q, scale, kept[0], kept[1]) if stats else (q, scale)
+    dev = x.device
+    q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    scale = _f32(dev, rows)
+    mean, rstd = (torch.empty_like(scale), torch.empty_like(scale)) if stats else (None, None)
+    _call("tq_layer_norm_quant_per_token", xr.data_ptr(), FTYPE[x.dtype], rows, cols, ld, _ptr(w), _ptr(b), wdt, eps,
+          q.data_ptr(), scale.data_ptr(), _ptr(mean), _ptr(rstd), _stream(dev))
+    return (q, scale, mean, rstd) if stats else (q, scale)
 
 
 def tq_layer_norm_backward(dy, x, weight, mean, rstd, param_dtype=None):
@@ -881,13 +904,16 @@ def tq_layer_norm_backward(dy, x, weight, mean, rstd, param_dtype=None):
     w, _, wdt = _params(x, cols, weight, None)
     pdt = weight.dtype if weight is not None else (param_dtype or torch.float32)
     mean, rstd = _row_vector(mean, rows, x, "mean"), _row_vector(rstd, rows, x, "rstd")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    grads = torch.empty((2, cols), dtype=pdt, device=x.device)
+    dev = x.device
+    dx = torch.empty_like(xr, memory_format=torch.contiguous_format)
+    dw = torch.empty((cols,), dtype=pdt, device=dev)
+    db = torch.empty_like(dw)
     nws = _lib.tq_layer_norm_backward_workspace_bytes(rows, cols)
-    ws = torch.empty((max(1, nws),), dtype=torch.uint8, device=x.device)
-    _call("tq_layer_norm_backward", _ptr(dyr), _ptr(xr), _ft(x), rows, cols, ldy, ldx, _ptr(w), FTYPE[pdt], _ptr(mean),
-          _ptr(rstd), _ptr(dx), _ptr(grads[0]), _ptr(grads[1]), _ptr(ws), nws, _stream(x.device))
-    return dx, grads[0], grads[1]
+    ws = _workspace(dev, nws)
+    _call("tq_layer_norm_backward", dyr.data_ptr(), xr.data_ptr(), FTYPE[x.dtype], rows, cols, ldy, ldx, _ptr(w),
+          FTYPE[pdt], mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), _ptr(ws), nws,
+          _stream(dev))
+    return dx, dw, db
 
 
 def tq_layer_norm_backward_workspace_bytes(rows, cols):
@@ -920,9 +946,9 @@ def tq_w8a8_linear_epilogue(qx, sx, qw, sw, bias=None, act="none", residual=None
             raise ValueError("residual must be [M, N] in the output's type, on qx's device")
         residual, _, _, ldr = _rows_of(residual, "residual")
     y = torch.empty((M, N), dtype=out_dtype, device=qx.device)
-    z = torch.empty((M, N), dtype=out_dtype, device=qx.device) if preact else None
-    _call("tq_w8a8_linear_epilogue", _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), M, N, K, _ptr(b), bdt, ACT[act],
-          _ptr(residual), ldr, _ptr(y), _ptr(z), FTYPE[out_dtype], _stream(qx.device))
+    z = torch.empty_like(y) if preact else None
+    _call("tq_w8a8_linear_epilogue", qx.data_ptr(), sx.data_ptr(), qw.data_ptr(), sw.data_ptr(), M, N, K, _ptr(b), bdt,
+          ACT[act], _ptr(residual), ldr, y.data_ptr(), _ptr(z), FTYPE[out_dtype], _stream(qx.device))
     return (y, z) if preact else y
 
 
@@ -934,9 +960,9 @@ def tq_linear_epilogue_backward(dy, preact, act="none"):
     dy, preact = _dev_float(dy, "dy"), _dev_float(preact, "preact")
     M, N = dy.shape
     dz = torch.empty_like(dy)
-    dbias = torch.empty((N,), dtype=torch.float32, device=dy.device)
+    dbias = _f32(dy.device, N)
     nws = _lib.tq_linear_epilogue_backward_workspace_bytes(M, N)
-    ws = torch.empty((max(1, nws),), dtype=torch.uint8, device=dy.device)
+    ws = _workspace(dy.device, nws)
     _call("tq_linear_epilogue_backward", _ptr(dy), _ptr(preact), _ft(dy), M, N, ACT[act], _ptr(dz), _ptr(dbias),
           _ptr(ws), nws, _stream(dy.device))
     return dz, dbias
@@ -961,7 +987,7 @@ def _distill_args(logits, top_idx, top_val, teacher_lse):
     if teacher_lse is not None:
         teacher_lse = _row_vector(teacher_lse, rows, logits, "teacher_lse")
     nws = _lib.tq_topk_distill_workspace_bytes(rows, vocab)
-    ws = torch.empty((max(1, nws),), dtype=torch.uint8, device=logits.device)
+    ws = _workspace(logits.device, nws)
     idx, val = top_idx.contiguous(), top_val.contiguous()
     head = (_ptr(z), _ft(logits), rows, vocab, ld, _ptr(idx), 32 if idx.dtype == torch.int32 else 64, _ptr(val),
             _ft(val), idx.shape[1], _ptr(teacher_lse))
@@ -977,9 +1003,8 @@ def tq_topk_distill(logits, top_idx, top_val, temperature=1.0, teacher_lse=None)
     rest_sum), the latter two for tq_topk_distill_backward."""
     head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
     dev = logits.device
-    loss = torch.empty((rows,), dtype=torch.float32, device=dev)
-    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-    rest = torch.empty((rows,), dtype=torch.float32, device=dev) if teacher_lse is not None else None
+    loss, stats = _f32(dev, rows), _f32(dev, rows, 2)
+    rest = torch.empty_like(loss) if teacher_lse is not None else None
     _call("tq_topk_distill", *head, temperature, _ptr(loss), _ptr(stats), _ptr(rest), _ptr(ws), nws, _stream(dev))
     return loss, stats, rest
 
@@ -989,6 +1014,7 @@ def tq_topk_distill_backward(logits, top_idx, top_val, stats, dloss=None, temper
     """dlogits of tq_topk_distill from its inputs and statistics; ``dloss``
     [rows] is the gradient of the losses (ones by default)."""
     head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
+    head_logits = kept[0]
     if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != logits.device:
         raise ValueError("stats must be tq_topk_distill's [rows, 2]")
     if (teacher_lse is None) != (rest_sum is None):
@@ -996,7 +1022,7 @@ def tq_topk_distill_backward(logits, top_idx, top_val, stats, dloss=None, temper
     stats = stats.contiguous()
     rest_sum = None if rest_sum is None else _row_vector(rest_sum, rows, logits, "rest_sum")
     dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
-    dz = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    dz = torch.empty_like(head_logits, memory_format=torch.contiguous_format)
     _call("tq_topk_distill_backward", *head, temperature, _ptr(stats), _ptr(rest_sum), _ptr(dloss), _ptr(dz), vocab,
           _ptr(ws), nws, _stream(logits.device))
     return dz
@@ -1007,10 +1033,10 @@ def tq_topk_distill_grad(logits, top_idx, top_val, dloss=None, temperature=1.0, 
     default) beforehand; ``inplace`` writes the gradient over the logits."""
     head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
     dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
-    loss = torch.empty((rows,), dtype=torch.float32, device=logits.device)
+    loss = _f32(logits.device, rows)
     if inplace and kept[0] is not logits:
         raise ValueError("in place needs logits whose rows are contiguous")
-    dz = logits if inplace else torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    dz = logits if inplace else torch.empty_like(kept[0], memory_format=torch.contiguous_format)
     _call("tq_topk_distill_grad", *head, temperature, _ptr(dloss), _ptr(loss), _ptr(dz),
           head[4] if inplace else vocab, _ptr(ws), nws, _stream(logits.device))
     return loss, dz

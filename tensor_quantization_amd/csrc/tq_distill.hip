@@ -161,7 +161,7 @@ template <int NT, int WORDS>
 __device__ __forceinline__ void marks_count(Marks<NT, WORDS>& k)
 {
     constexpr int PER = (WORDS + NT - 1) / NT;
-    const int t = threadIdx.x, first = t * PER;
+    const int t = afresh((int)threadIdx.x), first = t * PER;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -169,7 +169,7 @@ __device__ __forceinline__ void marks_count(Marks<NT, WORDS>& k)
     int upto = n;                        // over this lane and those before it
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(upto, d, 64);
+        const int o = __builtin_amdgcn_ds_bpermute((t - d) << 2, upto);
         if ((t & 63) >= d) upto += o;
     }
     if ((t & 63) == 63) k.waves[t >> 6] = upto;
@@ -213,21 +213,28 @@ __device__ __forceinline__ void marks_fill(Marks<NT, WORDS>& k, const Entries& e
     }
 }
 
-// The gradient of eight elements.
-template <int NT, int WORDS>
-__device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, int at, float c, float v[8])
+// The gradient of eight elements, x(z) the exponential.  Entries are few: the
+// loop over their bits is rolled, and picks its element by selects.
+template <int NT, int WORDS, class X>
+__device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, int at, float v[8], X x)
 {
-    const uint32_t m = marks8(k, at);
+    uint32_t m = marks8(k, at);
     float e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        e[i] = ex2((v[i] - q.m) * c);
+        e[i] = x(v[i]);
         v[i] = e[i] * q.out;
     }
-    if (m) {
+#pragma unroll 1
+    while (m) {
+        const int b = __ffs(m) - 1;
+        m &= m - 1;
+        float g = e[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (m >> i & 1) v[i] = e[i] * q.in - k.value[rank_of(k, at + i)];
+        for (int i = 1; i < 8; ++i) g = b == i ? e[i] : g;
+        g = g * q.in - k.value[rank_of(k, at + b)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = b == i ? g : v[i];
     }
 }
 
@@ -459,10 +466,11 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     __syncthreads();
     marks_fill(k, ent, q, row, V, c0, n, s, c);
     __syncthreads();
+    auto x = [&](float v) { return ex2((v - q.m) * c); };
     if (n < 8) {
         if (t < n) {
             float v[8] = {load1<FT>(z, from + t), 0, 0, 0, 0, 0, 0, 0};
-            grad8(k, q, t, c, v);
+            grad8(k, q, t, v, x);
             store1<FT>(dz, to + t, v[0]);
         }
         return;
@@ -480,158 +488,225 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
             if (at[u].lo == 8) continue;
             float v[8];
             widen8<FT>(raw[u], v);
-            grad8(k, q, at[u].at, c, v);
+            grad8(k, q, at[u].at, v, x);
             store8_own<FT>(dz, to, at[u], v);
         }
     }
 }
 
 // k_distill_held: loss and gradient of a row in one read: NT threads hold the
-// row (8 <= V <= 8 NT W) in registers in its own type.
+// row (8 <= V <= 8 NT W) in registers in its own type.  The entries are marked
+// while the loads are under way, and every vector's exponentials are summed as
+// it arrives, so that only the gradient's own arithmetic follows the last load.
+// For that a wave takes its exponentials relative to the largest logit m of its
+// first vector instead of the row's, as 2^(z c - m c) with one rounding: a sum
+// in floating point loses nothing by it unless it overflows (a logit more than
+// 88 / s above m) or m c does; then S is no positive finite number, and the row
+// is summed again around its true maximum, the products taken after the
+// difference.
+//
+// A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's
+// gradient is computed its registers take the next row's vector, so that the
+// reads go on under the gradient's arithmetic and stores.
 template <int FT, int NT, int W>
-__global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz, int V, Entries ent, float s, float c,
+__global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz, uint32_t rows, int V, Entries ent, float s, float c,
                                                      const float* __restrict__ dloss, float* __restrict__ loss,
                                                      void* dz, int64_t lddz)
 {
-    constexpr int NW = NT / 64;
+    constexpr int NW = NT / 64, ES = FT == F32 ? 4 : 2;
     __shared__ Marks<NT, NT * W / 4 + 1> k;
-    __shared__ float rmax[2][NW], rsum[4][NW];
-    const int t = threadIdx.x, wave = t >> 6;
-    constexpr int ES = FT == F32 ? 4 : 2;
-    const int64_t row = blockIdx.x;
-    const char* from = static_cast<const char*>(z) + row * ldz * ES;
-    char* to = static_cast<char*>(dz) + row * lddz * ES;
+    __shared__ float red[6][NW], tails[8];
+    __shared__ int any;
     const bool rest = ent.tlse != nullptr;
+    // V / 8 whole vectors (absent ones read the last again), and an element more for the first V % 8 threads
+    const int nvec = V >> 3, ntail = V & 7;
     Raw8<FT> raw[W];
+    const char* from = static_cast<const char*>(z) + blockIdx.x * ldz * ES;
 #pragma unroll
-    for (int w = 0; w < W; ++w) raw[w] = load8_off<FT>(from, (uint32_t)vec8(w * NT + t, V).at * ES);
+    for (int w = 0; w < W; ++w) {
+        const int v = w * NT + (int)threadIdx.x;
+        raw[w] = load8_off<FT, true>(from, (uint32_t)(v < nvec ? v : nvec - 1) * (8 * ES));
+    }
+    const uint32_t step = gridDim.x;
+    for (uint32_t r = blockIdx.x; r < rows; r += step) {
+    // opaque, so that nothing computed from them is kept in registers over the rows
+    const int64_t row = afresh_uniform((int)r);
+    const int t = afresh((int)threadIdx.x), wave = t >> 6;
+    char* to = static_cast<char*>(dz) + row * lddz * ES;
+    from = static_cast<const char*>(z) + row * ldz * ES;
+    const bool more = r + step < rows;
+    const char* next = from + (more ? step * ldz * ES : 0);
+    // vector w of the next row (after the last row, one address of this one again)
+    auto ahead = [&](int w) {
+        const int at = afresh(afresh(t) + w * NT);
+        raw[w] = load8_off<FT, true>(next, more ? (uint32_t)(at < nvec ? at : nvec - 1) * (8 * ES) : 0u);
+    };
+    const float tail = t < ntail ? load1<FT>(from, 8 * nvec + t) : -__builtin_inff();
+    __syncthreads();                     // the row before is done with the marks
+    if (t < 8) tails[t] = tail;          // read by the same threads
+    if (t == 0) any = 0;
     marks_clear(k);
     __syncthreads();
     float tm = -__builtin_inff();
-    int some = 0;
 #pragma unroll 1
     for (int i = t; i < ent.K; i += NT) {
         const int col = entry_col(ent, row, i, V);
         if (col >= 0) {
-            some = 1;
+            any = 1;
             mark(k, col);
             tm = __builtin_fmaxf(tm, entry_val(ent, row, i));
         }
     }
-    float m = -__builtin_inff();
-#pragma unroll
-    for (int w = 0; w < W; ++w) {        // repeated elements do not change a maximum
-        float v[8];
-        widen8<FT>(raw[w], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
-    }
-    m = wave_max(m);
     tm = wave_max(tm);
-    if ((t & 63) == 0) {
-        rmax[0][wave] = m;
-        rmax[1][wave] = tm;
-    }
-    some = __syncthreads_or(some);
-    m = rmax[0][0];
-    tm = rmax[1][0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) {
-        m = __builtin_fmaxf(m, rmax[0][w]);
-        tm = __builtin_fmaxf(tm, rmax[1][w]);
-    }
-    const float b = base_of(m);
+    if ((t & 63) == 0) red[0][wave] = tm;
+    __syncthreads();
+    bool some = any != 0;
+    marks_count(k);
+    // one value per wave, joined across the lanes
+    const int lane = t & 63;
+    auto top = [&](int i) { return wave_max(lane < NW ? red[i][lane] : -__builtin_inff()); };
+    auto total = [&](int i) { return wave_sum(lane < NW ? red[i][lane] : 0.0f); };
+    tm = top(0);
     tm = rest ? ent.tlse[row] : base_of(tm);
-    float S = 0.0f, R = 0.0f, tsum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const Vec8 at = vec8(afresh(w * NT + t), V);
-        if (at.lo == 8) continue;
-        float v[8], x = 0.0f;
-        keep_raw<FT>(raw[w]);
-        widen8<FT>(raw[w], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = ex2((v[i] - b) * c);
-            v[i] = i >= at.lo ? v[i] : 0.0f;
-            x += v[i];
-        }
-        S += x;
-        if (rest) {
-            const uint32_t mask = marks8(k, at.at);
-            if (mask) {
-                x = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x += mask >> i & 1 ? 0.0f : v[i];
-            }
-            R += x;
-        }
-        __builtin_amdgcn_sched_barrier(0);   // one vector's values at a time
-    }
+    float tsum = 0.0f;
 #pragma unroll 1
     for (int i = t; i < ent.K; i += NT)
         if (entry_col(ent, row, i, V) >= 0) {
             const float x = entry_val(ent, row, i);
             tsum += rest ? ex2((x * s - tm) * LOG2E) : ex2((x - tm) * c);
         }
+
+    float m, S, R;
+    // the sums over this thread's vectors of x(z) and, in R, of those off the entries
+    auto sum = [&](auto x) {
+        S = t < ntail ? x(tails[t]) : 0.0f;
+        R = rest && t < ntail && !(marks8(k, 8 * nvec) >> t & 1) ? S : 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int at = afresh(afresh(t) + w * NT);
+            float v[8], part = 0.0f;
+            keep_raw<FT>(raw[w]);
+            widen8<FT>(raw[w], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = x(v[i]);
+                part += v[i];
+            }
+            const bool here = at < nvec;
+            S += here ? part : 0.0f;
+            if (rest) {
+                const uint32_t mask = here ? marks8(k, 8 * at) : 0;
+                if (mask) {
+                    part = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) part += mask >> i & 1 ? 0.0f : v[i];
+                }
+                R += here ? part : 0.0f;
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one vector at a time, in the order they arrive
+        }
+    };
+    {
+        float v[8];
+        widen8<FT>(raw[0], v);
+        m = v[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+        m = base_of(wave_max(m));
+        const float mc = m * c;
+        sum([&](float v) { return ex2(__builtin_fmaf(v, c, -mc)); });
+    }
     S = wave_sum(S);
     R = wave_sum(R);
     tsum = wave_sum(tsum);
     if ((t & 63) == 0) {
-        rsum[0][wave] = S;
-        rsum[1][wave] = R;
-        rsum[2][wave] = tsum;
+        red[1][wave] = m;
+        red[2][wave] = S;
+        red[3][wave] = R;
+        red[4][wave] = tsum;
     }
-    marks_count(k);                      // its barrier also publishes the sums
     __syncthreads();
-    S = 0.0f;
-    R = 0.0f;
-    tsum = 0.0f;
+    m = top(1);
+    const float f = lane < NW ? ex2((red[1][lane] - m) * c) : 0.0f;
+    S = wave_sum(lane < NW ? red[2][lane] * f : 0.0f);
+    R = wave_sum(lane < NW ? red[3][lane] * f : 0.0f);
+    tsum = total(4);
+    const bool near = S >= 0x1p-60f && S < 0x1p100f;
+    if (!near) {                         // uniform: around the row's own maximum
+        m = t < ntail ? tails[t] : -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        S += rsum[0][w];
-        R += rsum[1][w];
-        tsum += rsum[2][w];
-    }
-    if (!rest && tsum == 0.0f) some = 0;
-    float pr;
-    const Coef q = make_coef(rest, some != 0, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
-    if (!q.some) {                       // uniform
-        if (t == 0) loss[row] = 0.0f;
+        for (int w = 0; w < W; ++w) {    // repeated elements do not change a maximum
+            float v[8];
+            keep_raw<FT>(raw[w]);
+            widen8<FT>(raw[w], v);
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const Vec8 at = vec8(afresh(w * NT + t), V);
-            const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (at.lo < 8) store8_own_off<FT>(to, at, v);
+            for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
         }
-        return;
+        m = wave_max(m);
+        __syncthreads();
+        if ((t & 63) == 0) red[1][wave] = m;
+        __syncthreads();
+        m = top(1);
+        const float b = base_of(m);
+        sum([&](float v) { return ex2((v - b) * c); });
+        S = wave_sum(S);
+        R = wave_sum(R);
+        __syncthreads();
+        if ((t & 63) == 0) {
+            red[2][wave] = S;
+            red[3][wave] = R;
+        }
+        __syncthreads();
+        S = total(2);
+        R = total(3);
     }
-    marks_fill(k, ent, q, row, V, 0, V, s, c);
+    if (!rest && tsum == 0.0f) some = false;
+    float pr;
+    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+    if (q.some) marks_fill(k, ent, q, row, V, 0, V, s, c);
     float l = 0.0f;
 #pragma unroll 1
-    for (int i = t; i < ent.K; i += NT) {
+    for (int i = t; i < (q.some ? ent.K : 0); i += NT) {
         const int col = entry_col(ent, row, i, V);
         if (col >= 0) l += entry_loss(ent, entry_val(ent, row, i), load1<FT>(from, col), s, c, tm, tsum, m, S);
     }
     l = wave_sum(l);
-    if ((t & 63) == 0) rsum[3][wave] = l;
+    if ((t & 63) == 0) red[5][wave] = l;
     __syncthreads();                     // also before the first store: dz may be z
-    if (t == 0) {
-        l = rest_loss(pr, R, S);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) l += rsum[3][w];
-        loss[row] = l;
+    if (wave == 0) {
+        l = total(5) + rest_loss(pr, R, S);
+        if (t == 0) loss[row] = q.some ? l : 0.0f;
     }
+    // 2^(z c - m c) or 2^((z - m) c)
+    const float sub = near ? 0.0f : q.m, mc = near ? q.m * c : 0.0f;
+    auto x = [&](float v) { return ex2(__builtin_fmaf(v - sub, c, -mc)); };
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        const Vec8 at = vec8(afresh(w * NT + t), V);
-        if (at.lo == 8) continue;
+        const int at = afresh(afresh(t) + w * NT);
         float v[8];
         keep_raw<FT>(raw[w]);
         widen8<FT>(raw[w], v);
-        grad8(k, q, at.at, c, v);
-        store8_own_off<FT>(to, at, v);
+        // the old vector's registers are free before the new one's load is issued: it goes into the same ones, and no
+        // copy at the loop's end waits for it
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(v[i]));
         __builtin_amdgcn_sched_barrier(0);
+        ahead(w);
+        if (at < nvec) {
+            if (q.some) grad8(k, q, 8 * at, v, x);
+            else
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+            store8_off<FT, true>(to, (uint32_t)at * (8 * ES), v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (t < ntail) {
+        const int at = 8 * nvec + t;
+        const float e = x(tails[t]);
+        const bool entry = marks8(k, 8 * nvec) >> t & 1;
+        store1<FT>(to, at, !q.some ? 0.0f : entry ? e * q.in - k.value[rank_of(k, at)] : e * q.out);
+    }
     }
 }
 
@@ -699,14 +774,16 @@ template <int FT>
 static bool held_launch(const Distill& d, const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
 {
     constexpr int H = FT == F32 ? 2 : 1;  // binary32 rows hold half as many elements
-    if (d.rows < DT_HELD_ROWS || d.V < 8 || d.V > (FT == F32 ? 65536 : 98304)) return false;
+    if (d.rows < DT_HELD_ROWS || d.V < 8 || d.V > (FT == F32 ? 65536 : 131072)) return false;
+    // as many workgroups as fit on the chip by their registers
 #define TQ_HELD(NT, W)                                                                                            \
-    hipLaunchKernelGGL((k_distill_held<FT, NT, W>), dim3((unsigned)d.rows), dim3(NT), 0, st, d.z, d.ldz, d.V, d.ent, \
-                       d.s, d.c, dloss, loss, dz, lddz)
+    hipLaunchKernelGGL((k_distill_held<FT, NT, W>), dim3((unsigned)std::min<int64_t>(d.rows, 256 * (1024 / NT) * \
+                       (W * (FT == F32 ? 2 : 1) <= 8 ? 2 : 1))), dim3(NT), 0, st, d.z, d.ldz, (uint32_t)d.rows, d.V, \
+                       d.ent, d.s, d.c, dloss, loss, dz, lddz)
     if (d.V <= 8192) TQ_HELD(256, 4);
     else if (d.V <= 32768 / H) TQ_HELD(256, 16 / H);
     else if (d.V <= 65536 / H) TQ_HELD(512, 16 / H);
-    else TQ_HELD(1024, FT == F32 ? 8 : 12);
+    else TQ_HELD(1024, 16 / H);
 #undef TQ_HELD
     return true;
 }

@@ -118,14 +118,23 @@ template <int FT>
 __device__ __forceinline__ void keep_raw(Raw8<FT>& r)
 {
 #pragma unroll
-    for (int i = 0; i < (FT == F32 ? 2 : 1); ++i)
-        asm("" : "+v"(r.w[i].x), "+v"(r.w[i].y), "+v"(r.w[i].z), "+v"(r.w[i].w));
+    for (int i = 0; i < (FT == F32 ? 2 : 1); ++i) {
+        u32x4 v = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+        asm("" : "+v"(v));
+        r.w[i] = make_uint4(v.x, v.y, v.z, v.w);
+    }
 }
 
 // The same for an index: what is computed from it is computed again.
 __device__ __forceinline__ int afresh(int v)
 {
     asm volatile("" : "+v"(v));
+    return v;
+}
+
+__device__ __forceinline__ int afresh_uniform(int v)
+{
+    asm volatile("" : "+s"(v));
     return v;
 }
 
