@@ -697,7 +697,7 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
             else
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-            store8_off<FT, true>(to, (uint32_t)at * (8 * ES), v);
+            store8_off<FT, 1>(to, (uint32_t)at * (8 * ES), v);
         }
         __builtin_amdgcn_sched_barrier(0);
     }

@@ -17,20 +17,6 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
 // -------------------------------------------------------------- activations
-// 1 / (1 + exp(-u)) from t = exp(-|u|) <= 1, which cannot overflow.
-struct Logistic {
-    float p, pq;                         // the value and its slope p (1 - p)
-};
-__device__ __forceinline__ Logistic logistic(float u)
-{
-    const float t = __builtin_amdgcn_exp2f(-__builtin_fabsf(u) * LOG2E);
-    const float h = __builtin_amdgcn_rcpf(1.0f + t);
-    Logistic r;
-    r.p = u >= 0.0f ? h : t * h;
-    r.pq = t * h * h;
-    return r;
-}
-
 // v / (1 + 2^x): where 2^x overflows the quotient is v's zero.
 __device__ __forceinline__ float times_logistic(float v, float x)
 {
@@ -87,8 +73,8 @@ __device__ __forceinline__ void slope8(int act, const float z[8], float d[8])
     case TQ_ACT_SILU:
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const Logistic l = logistic(z[i]);
-            d[i] *= l.p + (l.pq == 0.0f ? 0.0f : z[i] * l.pq);
+            const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * z[i]));
+            d[i] *= __builtin_fmaf(z[i], __builtin_fmaf(-p, p, p), p);
         }
         break;
     case TQ_ACT_GELU:
@@ -101,9 +87,12 @@ __device__ __forceinline__ void slope8(int act, const float z[8], float d[8])
     case TQ_ACT_GELU_TANH:
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float zz = GELU_A * z[i] * z[i];
-            const Logistic l = logistic(2.0f * GELU_C * z[i] * (1.0f + zz));
-            d[i] *= l.p + (l.pq == 0.0f ? 0.0f : z[i] * (2.0f * GELU_C) * (1.0f + 3.0f * zz) * l.pq);
+            constexpr float A = -2.0f * LOG2E * GELU_C;
+            const float zz = z[i] * z[i];
+            const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[i] * __builtin_fmaf(zz, A * GELU_A, A)));
+            const float pq = __builtin_fmaf(-p, p, p);
+            const float u = z[i] * __builtin_fmaf(zz, 6.0f * GELU_C * GELU_A, 2.0f * GELU_C);
+            d[i] *= __builtin_fmaf(pq == 0.0f ? 0.0f : u, pq, p);
         }
         break;
     default: break;
@@ -201,13 +190,17 @@ __device__ __forceinline__ void epilogue8(const Epi& e, const Cols8& c, int64_t 
     store8_first<YT>(e.y, at, c.n, v);
 }
 
-// Sixteen codes at any byte address, zeros from code K of the row on.
+// Sixteen codes at any byte address.
+__device__ __forceinline__ v4i codes16_whole(const int8_t* p)
+{
+    const u32x4_byte v = *reinterpret_cast<const u32x4_byte*>(p);
+    return v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
+}
+
+// The same, zeros from code K of the row on.
 __device__ __forceinline__ v4i codes16(const int8_t* row, int64_t k, int64_t K)
 {
-    if (k + 16 <= K) {
-        const u32x4_byte v = *reinterpret_cast<const u32x4_byte*>(row + k);
-        return v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
-    }
+    if (k + 16 <= K) return codes16_whole(row + k);
     v4i r = v4i{};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -221,18 +214,36 @@ __device__ __forceinline__ v4i codes16(const int8_t* row, int64_t k, int64_t K)
 // k_epi_few (M <= 16 MT): bound by the weights, which are read once.  A
 // workgroup of NWV waves owns 16 output columns; the waves take the K axis in
 // turn, 128 codes at a time, so that a wave's two loads use whole 128-byte
-// lines; the sums meet in LDS.  The weights are the matrix core's first
-// operand (16 columns), the tokens its second (16 tokens, rows past M repeat
-// row M - 1), U blocks of both in flight per wave.
-template <int YT, int MT, int NWV>
+// lines; the sums meet in LDS, one thread per output.  The weights are the
+// matrix core's first operand (16 columns), the tokens its second (16 tokens,
+// rows past M repeat row M - 1), U blocks of both in flight per wave.  What an
+// output's epilogue needs is loaded before the weights are.
+template <int YT, int MT, int NWV, int U>
 __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
                                                       int64_t K, Epi e)
 {
-    constexpr int U = MT == 1 ? 4 : 2;
+    constexpr int NT = 64 * NWV, PER = MT * 256 > NT ? MT * 256 / NT : 1;   // outputs per thread
     __shared__ int sums[NWV][MT * 16][20];   // rows of 16 sums, 20 apart (16-byte steps that spread over the banks)
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l16 = lane & 15, g4 = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
+
+    // thread t finishes column t % 16 of tokens t / 16, + NT / 16, ...
+    const int64_t on = n0 + (t & 15);
+    float osx[PER], ores[PER], osw = 0.0f, ob = 0.0f;
+    bool mine[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int m = t / 16 + i * (NT / 16);
+        mine[i] = m < 16 * MT && m < e.M && on < e.N;
+        osx[i] = mine[i] ? e.sx[m] : 0.0f;
+        ores[i] = mine[i] && e.res ? load1<YT>(e.res, m * e.ldr + on) : 0.0f;
+    }
+    if (mine[0]) {
+        osw = e.sw[on];
+        ob = load1_rt(e.bias, e.bias_dt, on, 0.0f);
+    }
+
     const int64_t n = n0 + l16 < e.N ? n0 + l16 : e.N - 1;
     const int8_t* pw = qw + n * K;
     const int8_t* px[MT];
@@ -244,55 +255,59 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
     v4i acc[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = v4i{};
-    const int64_t nkb = (K + 127) / 128, whole = K / 128;
-    int64_t kb = w;
-    for (; kb + (U - 1) * NWV < whole; kb += U * NWV) {
-        v4i a[U][2], b[U][2][MT];
+    // this wave's whole blocks are w, w + NWV, ...: U of them under way, each slot refilled as it is used
+    const int nkb = (int)((K + 127) / 128), whole = (int)(K / 128);
+    v4i a[U][2], b[U][2][MT];
+    auto fetch = [&](int u, int kb) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int s = 0; s < 2; ++s) {
+            const int k = kb * 128 + 64 * s + 16 * g4;
+            a[u][s] = codes16_whole(pw + k);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int64_t k = (kb + u * NWV) * 128 + 64 * s + 16 * g4;
-                const u32x4_byte v = *reinterpret_cast<const u32x4_byte*>(pw + k);
-                a[u][s] = v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
+            for (int i = 0; i < MT; ++i) b[u][s][i] = codes16_whole(px[i] + k);
+        }
+    };
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const u32x4_byte x = *reinterpret_cast<const u32x4_byte*>(px[i] + k);
-                    b[u][s][i] = v4i{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
-                }
-            }
+    for (int u = 0; u < U; ++u)
+        if (w + u * NWV < whole) fetch(u, w + u * NWV);
+    for (int kb = w; kb < whole; kb += U * NWV)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            if (kb + u * NWV >= whole) break;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
                     acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][s], b[u][s][i], acc[i], 0, 0, 0);
-    }
-    for (; kb < nkb; kb += NWV)
+            if (kb + (u + U) * NWV < whole) fetch(u, kb + (u + U) * NWV);
+        }
+    if (whole < nkb && whole % NWV == w)     // the rest of K
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int64_t k = kb * 128 + 64 * s + 16 * g4;
-            const v4i a = codes16(pw, k, K);
+            const int64_t k = (int64_t)whole * 128 + 64 * s + 16 * g4;
+            const v4i r = codes16(pw, k, K);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, codes16(px[i], k, K), acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(r, codes16(px[i], k, K), acc[i], 0, 0, 0);
         }
     // lane l holds columns 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
     for (int i = 0; i < MT; ++i) *reinterpret_cast<v4i*>(&sums[w][16 * i + l16][4 * g4]) = acc[i];
     __syncthreads();
-    for (int j = t; j < MT * 32; j += 64 * NWV) {
-        const int m = j >> 1, c = 8 * (j & 1);
-        if (m >= e.M || n0 + c >= e.N) continue;
-        int s[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = 0;
-        for (int v = 0; v < NWV; ++v)
+    for (int i = 0; i < PER; ++i) {
+        const int m = t / 16 + i * (NT / 16);
+        if (!mine[i]) continue;
+        int s = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += sums[v][m][c + i];
-        const Cols8 cc = cols8(e, n0 + c);
-        epilogue8<YT>(e, cc, m, e.sx[m], s, e.res ? residual8<YT>(e, cc, m) : Raw8<YT>{});
+        for (int v = 0; v < NWV; ++v) s += sums[v][m][t & 15];
+        float v = (float)s * osx[i] * osw;
+        if (e.bias) v += ob;
+        const int64_t at = m * e.N + on;
+        if (e.z) store1<YT>(e.z, at, v);
+        with_act(e.act, [&](auto a) { v = act1<decltype(a)::value>(v); });
+        if (e.res) v += ores[i];
+        store1<YT>(e.y, at, v);
     }
 }
 
@@ -393,7 +408,7 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[k][i] += w[i];
                 }
-                store8_off<YT, NTS>(y, yo + k * S::RPI * ystep, v[k]);
+                store8_off<YT, NTS ? 1 : 0>(y, yo + k * S::RPI * ystep, v[k]);
             }
             yo += 2 * S::RPI * ystep;
             ro += 2 * S::RPI * rstep;
@@ -639,11 +654,16 @@ __global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict_
         }
     };
 
+    // The zeros are set here, ahead of the loads and their barrier (volatile statements keep their order): a write of
+    // an accumulation register needs wait states before a product reads it, which the compiler cannot see in asm.
     v4i acc[NT][NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = v4i{};
+        for (int j = 0; j < NT; ++j) {
+            acc[i][j] = v4i{};
+            asm volatile("" : "+a"(acc[i][j]));
+        }
 
     // lane l reads row l % 16, chunk 4 s + l / 16 of a tile of 16 rows
     const int key = l16 >> 1;
@@ -814,21 +834,25 @@ __global__ __launch_bounds__(256) void k_epi_bwd_thin(const void* __restrict__ d
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int64_t EPI_CHUNKS = 64;       // row chunks of the backward pass
-inline int64_t epi_chunk(int64_t M)      // rows per chunk: whole rounds of the four waves' four rows
+// Rows per chunk of the backward pass: whole rounds of the four waves' four
+// rows, in about EPI_GROUPS workgroups over the slabs of 512 columns (measured on
+// [8192, 11008] bf16: 1400 workgroups 115 us, 4096 109, 8192 106).
+constexpr int64_t EPI_GROUPS = 8192;
+inline int64_t epi_chunk(int64_t M, int64_t N)
 {
-    return cdiv(cdiv(M, EPI_CHUNKS), 16) * 16;
+    const int64_t chunks = std::max<int64_t>(1, EPI_GROUPS / cdiv(N, 512));
+    return cdiv(cdiv(M, chunks), 16) * 16;
 }
 
 template <int YT>
 static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Epi& e, hipStream_t st)
 {
-#define TQ_FEW(MT, NWV)                                                                                    \
-    hipLaunchKernelGGL((k_epi_few<YT, MT, NWV>), dim3((unsigned)cdiv(e.N, 16)), dim3(64 * NWV), 0, st, qx, qw, K, e)
+#define TQ_FEW(MT, NWV, U)                                                                                 \
+    hipLaunchKernelGGL((k_epi_few<YT, MT, NWV, U>), dim3((unsigned)cdiv(e.N, 16)), dim3(64 * NWV), 0, st, qx, qw, K, e)
     if (e.M <= 64) {
-        if (e.M <= 16) TQ_FEW(1, 8);
-        else if (e.M <= 32) TQ_FEW(2, 8);
-        else TQ_FEW(4, 8);
+        if (e.M <= 16) TQ_FEW(1, 8, 4);
+        else if (e.M <= 32) TQ_FEW(2, 8, 2);
+        else TQ_FEW(4, 8, 2);
         return;
     }
 #undef TQ_FEW
@@ -880,7 +904,7 @@ tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_
 size_t tq_linear_epilogue_backward_workspace_bytes(int64_t M, int64_t N)
 {
     if (M <= 0 || N <= 0) return 0;
-    return (size_t)cdiv(M, epi_chunk(M)) * (size_t)colsum_ld(N) * sizeof(float);
+    return (size_t)cdiv(M, epi_chunk(M, N)) * (size_t)colsum_ld(N) * sizeof(float);
 }
 
 tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dtype, int64_t M, int64_t N, int act,
@@ -902,7 +926,7 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
         if (!aligned16(workspace)) return TQ_ERR_ALIGN;
     }
     float* part = dbias ? static_cast<float*>(workspace) : nullptr;
-    const int64_t chunk = epi_chunk(M), chunks = cdiv(M, chunk), ld = colsum_ld(N);
+    const int64_t chunk = epi_chunk(M, N), chunks = cdiv(M, chunk), ld = colsum_ld(N);
     const dim3 grid((unsigned)cdiv(N, 512), (unsigned)chunks);
     TQ_LLM_FT_SWITCH(dtype, {
         if (N < 8)

@@ -409,43 +409,52 @@ __global__ __launch_bounds__(256) void k_ln_bwd_cols(const void* __restrict__ dy
 }
 
 // ------------------------------------------------------------- column sums
-// A workgroup takes 64 columns of one output: 16 lanes of four columns by 16
-// rows of partials at a time, then the 16 row sums in order through LDS.
+// A workgroup takes 32 columns of one output: 8 lanes of four columns by 32
+// rows of partials at a time, four such loads under way per thread, then the
+// 32 row sums in order through LDS.
 __global__ __launch_bounds__(256) void k_colsum(const float* __restrict__ part, int64_t parts, int outs, int64_t ld,
                                                 int64_t cols, void* __restrict__ out0, void* __restrict__ out1, int dt)
 {
-    __shared__ float4 sums[16][16];
+    __shared__ float4 sums[32][8];
     const int o = blockIdx.y;
     void* out = o ? out1 : out0;
     if (!out) return;            // uniform in the workgroup
-    const int c4 = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const int64_t col = (int64_t)blockIdx.x * 64 + 4 * c4;
+    const int c4 = threadIdx.x & 7, rl = threadIdx.x >> 3;
+    const int64_t col = (int64_t)blockIdx.x * 32 + 4 * c4;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (col < cols) {
-        for (int64_t p = rl; p < parts; p += 16) {
-            const float4 a = *reinterpret_cast<const float4*>(part + (p * outs + o) * ld + col);
-            s.x += a.x;
-            s.y += a.y;
-            s.z += a.z;
-            s.w += a.w;
+        for (int64_t p = rl; p < parts; p += 128) {
+            float4 a[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t q = p + 32 * k < parts ? p + 32 * k : p;
+                a[k] = *reinterpret_cast<const float4*>(part + (q * outs + o) * ld + col);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (p + 32 * k < parts) {
+                    s.x += a[k].x;
+                    s.y += a[k].y;
+                    s.z += a[k].z;
+                    s.w += a[k].w;
+                }
         }
     }
     sums[rl][c4] = s;
     __syncthreads();
-    if (threadIdx.x >= 64) return;
     const int c = threadIdx.x;
-    const int64_t j = (int64_t)blockIdx.x * 64 + c;
-    if (j >= cols) return;
+    const int64_t j = (int64_t)blockIdx.x * 32 + c;
+    if (c >= 32 || j >= cols) return;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v += reinterpret_cast<const float*>(&sums[k][c >> 2])[c & 3];
+    for (int k = 0; k < 32; ++k) v += reinterpret_cast<const float*>(&sums[k][c >> 2])[c & 3];
     store1_rt(out, dt, j, v);
 }
 
 void colsum_launch(const float* part, int64_t parts, int outs, int64_t ld, int64_t cols, void* out0, void* out1,
                    int dt, hipStream_t st)
 {
-    const dim3 grid((unsigned)cdiv(cols, 64), out1 ? 2u : 1u);
+    const dim3 grid((unsigned)cdiv(cols, 32), out1 ? 2u : 1u);
     hipLaunchKernelGGL(k_colsum, grid, dim3(256), 0, st, part, parts, outs, ld, cols, out0, out1, dt);
 }
 
