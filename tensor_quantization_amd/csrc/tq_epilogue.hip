@@ -322,50 +322,50 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
 constexpr int ET = 128;
 __device__ __forceinline__ int eslot(int row, int chunk) { return row * ET + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
-// A lane's own part of a staged half: 32 rows of 16 NT sums, 4 apart beyond
+// A wave's own part of a staged half: 32 rows of 16 NN sums, 4 apart beyond
 // them so that sixteen rows' 16-byte stores spread over the banks, and the row
-// scales of all 16 NT rows behind them.
-template <int NT>
+// scales of all 16 NM rows behind them.
+template <int NM, int NN>
 struct Stage {
-    static constexpr int PITCH = 16 * NT + 4, LPR = 2 * NT, RPI = 64 / LPR;   // lanes per row, rows per instruction
-    static constexpr int INTS = 32 * PITCH + 16 * NT;
+    static constexpr int PITCH = 16 * NN + 4, LPR = 2 * NN, RPI = 64 / LPR;   // lanes per row, rows per instruction
+    static constexpr int INTS = 32 * PITCH + 16 * NM;
 };
 
-template <int NT>
+template <int NM, int NN>
 __device__ __forceinline__ void stage_scales(const Epi& e, int64_t m0, int* stage)
 {
     const int lane = threadIdx.x & 63;
-    float* sx = reinterpret_cast<float*>(stage + 32 * Stage<NT>::PITCH);
+    float* sx = reinterpret_cast<float*>(stage + 32 * Stage<NM, NN>::PITCH);
 #pragma unroll
-    for (int i = 0; i < NT / 4; ++i) {
-        const int64_t row = m0 + 64 * i + lane;
-        sx[64 * i + lane] = e.sx[row < e.M ? row : e.M - 1];
+    for (int i = 0; i < NM; i += 4) {
+        const int64_t row = m0 + 16 * i + lane;
+        if (16 * i + lane < 16 * NM) sx[16 * i + lane] = e.sx[row < e.M ? row : e.M - 1];
     }
 }
 
 // acc[i][j][r] = row 16 i + l % 16, column 16 j + 4 (l / 16) + r.  A wave's LDS
 // accesses stay in order; the fences keep the compiler's in order too.
-template <int NT>
-__device__ __forceinline__ void stage_half(int h, const v4i (&acc)[NT][NT], int* stage)
+template <int NM, int NN>
+__device__ __forceinline__ void stage_half(int h, const v4i (&acc)[NM][NN], int* stage)
 {
     const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<v4i*>(&stage[(16 * i + l16) * Stage<NT>::PITCH + 16 * j + 4 * g4]) = acc[2 * h + i][j];
+        for (int j = 0; j < NN; ++j)
+            *reinterpret_cast<v4i*>(&stage[(16 * i + l16) * Stage<NM, NN>::PITCH + 16 * j + 4 * g4]) = acc[2 * h + i][j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// A quarter that lies inside the output: no bounds, the activation and the
-// residual known, 32-bit offsets from the quarter's corner, two rows' worth of
+// A part that lies inside the output: no bounds, the activation and the
+// residual known, 32-bit offsets from its corner, two rows' worth of
 // independent work at a time.
-template <int YT, int NT, int ACT, bool RES, bool NTS>
+template <int YT, int NM, int NN, int ACT, bool RES, bool NTS>
 __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int64_t m0, int64_t n0,
-                                              const v4i (&acc)[NT][NT], int* stage)
+                                              const v4i (&acc)[NM][NN], int* stage)
 {
-    using S = Stage<NT>;
+    using S = Stage<NM, NN>;
     constexpr int ES = YT == F32 ? 4 : 2;
     const int lane = threadIdx.x & 63;
     const int c = 8 * (lane % S::LPR), r0 = lane / S::LPR;
@@ -374,8 +374,8 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
     const char* res = RES ? static_cast<const char*>(e.res) + (m0 * e.ldr + n0) * ES : nullptr;
     const uint32_t ystep = (uint32_t)e.N * ES, rstep = (uint32_t)e.ldr * ES;
 #pragma unroll
-    for (int h = 0; h < NT / 2; ++h) {
-        stage_half<NT>(h, acc, stage);
+    for (int h = 0; h < NM / 2; ++h) {
+        stage_half<NM, NN>(h, acc, stage);
         uint32_t yo = (uint32_t)(32 * h + r0) * ystep + c * ES, ro = (uint32_t)(32 * h + r0) * rstep + c * ES;
 #pragma unroll 1
         for (int r = r0; r < 32; r += 2 * S::RPI) {
@@ -416,21 +416,21 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
     }
 }
 
-// Any quarter: bounds, and the value before the activation where it is asked
+// Any part: bounds, and the value before the activation where it is asked
 // for.
-template <int YT, int NT>
-__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, const v4i (&acc)[NT][NT],
+template <int YT, int NM, int NN>
+__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, const v4i (&acc)[NM][NN],
                                            int* stage)
 {
-    using S = Stage<NT>;
+    using S = Stage<NM, NN>;
     const int lane = threadIdx.x & 63;
     const int c = 8 * (lane % S::LPR), r0 = lane / S::LPR;
     const float* sx = reinterpret_cast<const float*>(stage + 32 * S::PITCH);
 #pragma unroll
-    for (int h = 0; h < NT / 2; ++h) {
+    for (int h = 0; h < NM / 2; ++h) {
         const int64_t mh = m0 + 32 * h;
         if (mh >= e.M) return;           // uniform
-        stage_half<NT>(h, acc, stage);
+        stage_half<NM, NN>(h, acc, stage);
         const int rows = cc.n == 0 ? 0 : e.M - mh < 32 ? (int)(e.M - mh) : 32;
 #pragma unroll 1
         for (int r = r0; r < rows; r += S::RPI) {
@@ -444,24 +444,24 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
     }
 }
 
-// A wave's square of 16 NT sums, 32 rows at a time through the wave's own part
-// of LDS, so that its stores are whole rows of the square and the epilogue's
+// A wave's 16 NM x 16 NN sums, 32 rows at a time through the wave's own part
+// of LDS, so that its stores are whole rows of its part and the epilogue's
 // code exists once per activation.  A lane keeps its eight columns for all
 // rows, so their scales and bias are read once.
-template <int YT, int NT, bool NTS = false>
-__device__ __forceinline__ void finish_quarter(const Epi& e, int64_t m0, int64_t n0, const v4i (&acc)[NT][NT],
+template <int YT, int NM, int NN, bool NTS = false>
+__device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0, const v4i (&acc)[NM][NN],
                                                int* stage)
 {
-    const Cols8 cc = cols8(e, n0 + 8 * ((threadIdx.x & 63) % Stage<NT>::LPR));
+    const Cols8 cc = cols8(e, n0 + 8 * ((threadIdx.x & 63) % Stage<NM, NN>::LPR));
     if (m0 >= e.M) return;               // uniform
-    stage_scales<NT>(e, m0, stage);
-    const bool inside = m0 + 16 * NT <= e.M && n0 + 16 * NT <= e.N && e.N <= 1 << 22 && e.ldr <= 1 << 22;
+    stage_scales<NM, NN>(e, m0, stage);
+    const bool inside = m0 + 16 * NM <= e.M && n0 + 16 * NN <= e.N && e.N <= 1 << 22 && e.ldr <= 1 << 22;
     if (inside && !e.z)
         with_act(e.act, [&](auto a) {
-            if (e.res) finish_inside<YT, NT, decltype(a)::value, true, NTS>(e, cc, m0, n0, acc, stage);
-            else finish_inside<YT, NT, decltype(a)::value, false, NTS>(e, cc, m0, n0, acc, stage);
+            if (e.res) finish_inside<YT, NM, NN, decltype(a)::value, true, NTS>(e, cc, m0, n0, acc, stage);
+            else finish_inside<YT, NM, NN, decltype(a)::value, false, NTS>(e, cc, m0, n0, acc, stage);
         });
-    else finish_any<YT, NT>(e, cc, m0, acc, stage);
+    else finish_any<YT, NM, NN>(e, cc, m0, acc, stage);
 }
 
 template <int YT>
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(256) void k_epi_tile(const int8_t* __restrict__ qx,
 {
     __shared__ __attribute__((aligned(16))) union {
         uint8_t in[2][2][ET * ET];
-        int out[4][Stage<4>::INTS];
+        int out[4][Stage<4, 4>::INTS];
     } lds;
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l16 = lane & 15, g4 = lane >> 4, wm = w >> 1, wn = w & 1;
@@ -527,16 +527,15 @@ __global__ __launch_bounds__(256) void k_epi_tile(const int8_t* __restrict__ qx,
         }
     }
     __syncthreads();                     // the operands give way to the staged sums
-    finish_quarter<YT, 4>(e, m0 + 64 * wm, n0 + 64 * wn, acc, lds.out[w]);
+    finish_part<YT, 4, 4>(e, m0 + 64 * wm, n0 + 64 * wn, acc, lds.out[w]);
 }
 
 // k_epi_ring: operands whose rows start at 16-byte addresses.  A TILE x TILE
-// output tile per workgroup of four waves, wave w the quarter (w / 2, w % 2),
-// so each operand byte that enters LDS meets TILE products and each one read
-// from LDS TILE / 2.  LDS is a ring of RING units, a unit one operand's
-// [TILE x 128 codes] slice: unit 2 kb holds the activations of block kb, unit
-// 2 kb + 1 its weights.  Units arrive by direct global -> LDS loads (lane l of
-// an instruction writes 16 bytes at base + 16 l, so the swizzle of eslot is
+// output tile per workgroup of WM x WN waves, a wave a TILE / WM x TILE / WN
+// part of it.  LDS is a ring of RING units, a unit one operand's [TILE x 128
+// codes] slice: unit 2 kb holds the activations of block kb, unit 2 kb + 1 its
+// weights.  Units arrive by direct global -> LDS loads (lane l of an
+// instruction writes 16 bytes at base + 16 l, so the swizzle of eslot is
 // applied to the address it reads).  A block is two 64-code steps; while the
 // matrix cores work on one step's operands the next step's are read from LDS
 // into a second set of registers.  One barrier per block, between its steps:
@@ -544,14 +543,24 @@ __global__ __launch_bounds__(256) void k_epi_tile(const int8_t* __restrict__ qx,
 // units RING ahead, and the next block's units have landed (those after it may
 // still be on their way: the wait counts loads, it does not drain them).
 //
+// 256 x 256 with 2 x 4 waves of 128 x 64: on [8192, 4096] x [11008, 4096] 314
+// us without and 333 us with bias and gelu (2350 / 2220 TOP/s; the platform
+// library's plain int8 product of that size 400 us, its best size 2336 TOP/s),
+// 2560 TOP/s at 8192^3.  Bound by the matrix cores at the clock that the chip
+// holds under them, and by LDS: per block 192 KB of operand reads and 64 KB of
+// arriving slices at 128 bytes a clock take as long as the products.  Four
+// waves of 128 x 128 read a third less but leave each SIMD one wave, whose
+// loads (about 58 clocks of issue each) then stop its products: 326 / 346 us.
+// Of the 333 us about 45 are the epilogue, which one workgroup per CU cannot
+// lay under the products of another.
+//
 // Where K is no multiple of 128, the block that the rest makes comes first
 // (integer sums have no order): its missing chunks come from sixteen zero
 // bytes on the weights' side, and the activations' side reads any valid chunk
 // there.  All later loads are whole.
 //
 // The products are issued from asm that adds in place: the compiler, left to
-// choose, gives the sums new registers and moves them back, and a 256 x 256
-// tile's sums take all 256 accumulation registers.
+// choose, gives the sums new registers and moves them back.
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ const uint4 zero_codes = {0, 0, 0, 0};
 
@@ -604,27 +613,30 @@ __device__ __forceinline__ void tile_of(int64_t nt, int64_t mt, int slab, int64_
     tm = at / wide;
 }
 
-template <int YT, int TILE, int RING, int WGS>
-__global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
+template <int YT, int TILE, int RING, int WM, int WN, int WGS>
+__global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
                                                      int64_t K, int64_t nt, int64_t mt, int slab, Epi e)
 {
     constexpr int UNIT = TILE * ET;      // bytes of a unit
-    constexpr int U = TILE / 32;         // loads per wave and unit
-    constexpr int Q = TILE / 2;          // rows and columns of a wave's quarter
-    constexpr int NT = Q / 16;           // 16-wide tiles along either side of it
-    constexpr int AHEAD = (RING - 4) * U;   // loads that may be in flight behind the next block's
-    constexpr int PER = NT / 2;          // products per LDS read
+    constexpr int WAVES = WM * WN;
+    constexpr int U = TILE / (8 * WAVES);          // loads per wave and unit
+    constexpr int QM = TILE / WM, QN = TILE / WN;  // rows and columns of a wave's part
+    constexpr int NM = QM / 16, NN = QN / 16;      // 16-wide tiles along its sides
+    constexpr int AHEAD = (RING - 4) * U;          // loads that may be in flight behind the next block's
+    constexpr int GROUPS = NM * NN >= 32 ? 16 : NM * NN >= 8 ? 8 : 4, PER = NM * NN / GROUPS;   // products go in groups, loads between them
+    static_assert(NM + NN <= 2 * GROUPS && 2 * U <= GROUPS && RING % 2 == 1 && TILE % (8 * WAVES) == 0, "schedule");
+    static_assert(4 * WAVES * Stage<NM, NN>::INTS <= RING * UNIT, "staging");
     __shared__ __attribute__((aligned(16))) uint8_t ring[RING * UNIT];
 
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int l16 = lane & 15, g4 = lane >> 4, wm = w >> 1, wn = w & 1;
+    const int l16 = lane & 15, g4 = lane >> 4, wm = w / WN, wn = w % WN;
     int64_t tm, tn;
     tile_of(nt, mt, slab, tm, tn);
     const int64_t m0 = tm * TILE, n0 = tn * TILE;
     const int nkb = (int)((K + ET - 1) / ET);
 
-    // loads of a unit: instruction q of wave w fills rows Q/2 w + 8 q .. + 7, lane l row l / 8, slot l % 8
-    const int fr = (TILE / 4) * w + (lane >> 3);
+    // loads of a unit: instruction q of wave w fills rows 8 (U w + q) .. + 7, lane l row l / 8, slot l % 8
+    const int fr = 8 * U * w + (lane >> 3);
     const int8_t* ga = qx + m0 * K;
     const int8_t* gb = qw + n0 * K;
     uint32_t oa[U], ob[U];
@@ -636,7 +648,7 @@ __global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict_
         oa[q] = (uint32_t)ra * (uint32_t)K + chunk;
         ob[q] = (uint32_t)rb * (uint32_t)K + chunk;
     }
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_void*)ring) + (uint32_t)w * (UNIT / 4);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_void*)ring) + (uint32_t)w * (1024 * U);
     const int rest = K % ET != 0;        // block 0 is the rest, block kb > 0 starts at code (kb - rest) 128
     const int64_t k_rest = K / ET * ET;
     auto load_unit = [&](int unit, int slot) {
@@ -656,20 +668,29 @@ __global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict_
 
     // The zeros are set here, ahead of the loads and their barrier (volatile statements keep their order): a write of
     // an accumulation register needs wait states before a product reads it, which the compiler cannot see in asm.
-    v4i acc[NT][NT];
+    v4i acc[NM][NN];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NM; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j = 0; j < NN; ++j) {
             acc[i][j] = v4i{};
             asm volatile("" : "+a"(acc[i][j]));
         }
 
     // lane l reads row l % 16, chunk 4 s + l / 16 of a tile of 16 rows
     const int key = l16 >> 1;
-    const int la[2] = {(Q * wm + l16) * ET + ((g4 ^ key) << 4), (Q * wm + l16) * ET + (((4 + g4) ^ key) << 4)};
-    const int lb[2] = {(Q * wn + l16) * ET + ((g4 ^ key) << 4), (Q * wn + l16) * ET + (((4 + g4) ^ key) << 4)};
-    v4i av[2][NT], bv[2][NT];
+    const int la[2] = {(QM * wm + l16) * ET + ((g4 ^ key) << 4), (QM * wm + l16) * ET + (((4 + g4) ^ key) << 4)};
+    const int lb[2] = {(QN * wn + l16) * ET + ((g4 ^ key) << 4), (QN * wn + l16) * ET + (((4 + g4) ^ key) << 4)};
+    v4i av[2][NM], bv[2][NN];
+    auto read = [&](int set, int x, const uint8_t* pa, const uint8_t* pb) {   // operand x of a step: weights first
+        if (x < NN) bv[set][x] = *reinterpret_cast<const v4i*>(pb + 16 * ET * x);
+        else if (x < NN + NM) av[set][x - NN] = *reinterpret_cast<const v4i*>(pa + 16 * ET * (x - NN));
+    };
+    auto products = [&](int set, int g) {
+#pragma unroll
+        for (int x = PER * g; x < PER * (g + 1); ++x) add_product(acc[x / NN][x % NN], bv[set][x % NN], av[set][x / NN]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
 
     const int units = 2 * nkb;
     int sa = 0, sb = 1;                  // slots of the present block's units
@@ -678,10 +699,7 @@ __global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict_
     else __builtin_amdgcn_s_waitcnt(WAIT(0, 15));
     asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        av[0][i] = *reinterpret_cast<const v4i*>(&ring[sa * UNIT + la[0] + 16 * ET * i]);
-        bv[0][i] = *reinterpret_cast<const v4i*>(&ring[sb * UNIT + lb[0] + 16 * ET * i]);
-    }
+    for (int x = 0; x < NM + NN; ++x) read(0, x, ring + sa * UNIT + la[0], ring + sb * UNIT + lb[0]);
     // RING is odd: the units to come at block kb are the weights of block kb + RING / 2 and the activations after
     uint64_t wnext = uniform_address(gb + (int64_t)(RING / 2 - rest) * ET);
     uint64_t xnext = uniform_address(ga + (int64_t)(RING / 2 + 1 - rest) * ET);
@@ -690,14 +708,10 @@ __global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict_
         const uint8_t* pb = ring + sb * UNIT + lb[1];
         __builtin_amdgcn_s_waitcnt(WAIT(63, 0));   // the first step's operands, before more reads join them
 #pragma unroll
-        for (int g = 0; g < 2 * NT; ++g) {   // first step's products, second step's operands
-            if (g < NT) {
-                bv[1][g] = *reinterpret_cast<const v4i*>(pb + 16 * ET * g);
-                av[1][g] = *reinterpret_cast<const v4i*>(pa + 16 * ET * g);
-            }
-#pragma unroll
-            for (int x = 0; x < PER; ++x) add_product(acc[g / 2][PER * (g % 2) + x], bv[0][PER * (g % 2) + x], av[0][g / 2]);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int g = 0; g < GROUPS; ++g) {   // first step's products, second step's operands
+            read(1, 2 * g, pa, pb);
+            read(1, 2 * g + 1, pa, pb);
+            products(0, g);
         }
         // both units read (lgkmcnt 0); the next block's two have landed
         const int next = 2 * kb + RING;
@@ -712,31 +726,28 @@ __global__ __launch_bounds__(256, WGS) void k_epi_ring(const int8_t* __restrict_
         const uint8_t* na = ring + sa * UNIT + la[0];
         const uint8_t* nb = ring + sb * UNIT + lb[0];
 #pragma unroll
-        for (int g = 0; g < 2 * NT; ++g) {   // second step's products, the next block's first operands
-            if (g < NT) {
-                bv[0][g] = *reinterpret_cast<const v4i*>(nb + 16 * ET * g);
-                av[0][g] = *reinterpret_cast<const v4i*>(na + 16 * ET * g);
-            }
+        for (int g = 0; g < GROUPS; ++g) {   // second step's products, the next block's first operands
+            read(0, 2 * g, na, nb);
+            read(0, 2 * g + 1, na, nb);
             if (g < U) {
                 if (more_w) lds_load(wnext, ob[g], fa + 1024u * g);
             } else if (g < 2 * U) {
                 if (more_x) lds_load(xnext, oa[g - U], fb + 1024u * (g - U));
             }
-#pragma unroll
-            for (int x = 0; x < PER; ++x) add_product(acc[g / 2][PER * (g % 2) + x], bv[1][PER * (g % 2) + x], av[1][g / 2]);
-            __builtin_amdgcn_sched_barrier(0);
+            products(1, g);
         }
     }
     // The last products' sums need up to 19 wait states before they are read, which the compiler cannot see behind
     // asm; the empty statements after the wait, in order as volatile asm is, keep every read behind it.
     asm volatile("s_nop 15\n\ts_nop 7");
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NM; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
+        for (int j = 0; j < NN; ++j) asm volatile("" : "+a"(acc[i][j]));
     __builtin_amdgcn_s_waitcnt(0x0070);
     asm volatile("s_barrier" ::: "memory");   // the ring gives way to the staged sums
-    finish_quarter<YT, NT, TILE == 256>(e, m0 + Q * wm, n0 + Q * wn, acc, reinterpret_cast<int*>(ring) + w * (RING * UNIT / 16));
+    finish_part<YT, NM, NN, TILE == 256>(e, m0 + QM * wm, n0 + QN * wn, acc,
+                                         reinterpret_cast<int*>(ring) + w * Stage<NM, NN>::INTS);
 }
 
 // ------------------------------------------------------ backward of epilogue
@@ -844,29 +855,46 @@ inline int64_t epi_chunk(int64_t M, int64_t N)
     return cdiv(cdiv(M, chunks), 16) * 16;
 }
 
+// The kernel of a product, by its shape.  Measured (us, K = 4096 unless given;
+// few tokens / 64 / 128 / 256 tile):
+//   24 x 4096      8.3 / 11.9 / 18 / 46      32 x 11008    19.2 / 11.9 / 21 / 47
+//   64 x 11008      30 / 12.0 / 21 / 49      512 x 4096       - / 16.6 / 19.5 / -
+//   640 x 4096       - / 24.5 / 20.0 / -     2048 x 4096      - / - / 35 / 51
+//   4096 x 4096      - / - / 87 / 60
+// The few-token kernel reads the tokens again for every 16 columns, which costs
+// more the more columns there are.  A tile kernel takes a time of its own per
+// round of resident workgroups (two 64 x 64 tiles or, up to 256 of them, one
+// 128 x 128 tile per CU), so the smallest tile that needs one round is taken,
+// and the largest once it fills the chip.  128 x 128 tiles beyond one round run
+// two to a CU on shorter rings.
 template <int YT>
 static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Epi& e, hipStream_t st)
 {
+    const bool rows16 = K >= ET && K % 16 == 0 && aligned16(qx) && aligned16(qw);
 #define TQ_FEW(MT, NWV, U)                                                                                 \
     hipLaunchKernelGGL((k_epi_few<YT, MT, NWV, U>), dim3((unsigned)cdiv(e.N, 16)), dim3(64 * NWV), 0, st, qx, qw, K, e)
-    if (e.M <= 64) {
-        if (e.M <= 16) TQ_FEW(1, 8, 4);
-        else if (e.M <= 32) TQ_FEW(2, 8, 2);
-        else TQ_FEW(4, 8, 2);
+    if (e.M <= 16) {
+        TQ_FEW(1, 8, 4);
+        return;
+    }
+    if (e.M <= 32 && (e.N <= 6144 || !rows16)) {
+        TQ_FEW(2, 8, 2);
         return;
     }
 #undef TQ_FEW
-    if (K >= ET && K % 16 == 0 && aligned16(qx) && aligned16(qw)) {
-#define TQ_RING(TILE, RING, WGS)                                                                             \
+    if (rows16) {
+#define TQ_RING(TILE, RING, WM, WN, WGS)                                                                     \
     do {                                                                                                     \
         const int64_t nt = cdiv(e.N, TILE), mt = cdiv(e.M, TILE);                                            \
         const int slab = (int)std::min<int64_t>(cdiv(nt, 8), 16);                                            \
-        hipLaunchKernelGGL((k_epi_ring<YT, TILE, RING, WGS>), dim3((unsigned)(nt * mt)), dim3(256), 0, st, qx, qw, \
-                           K, nt, mt, slab, e);                                                              \
+        hipLaunchKernelGGL((k_epi_ring<YT, TILE, RING, WM, WN, WGS>), dim3((unsigned)(nt * mt)),             \
+                           dim3(64 * WM * WN), 0, st, qx, qw, K, nt, mt, slab, e);                           \
     } while (0)
-        if (cdiv(e.M, 256) * cdiv(e.N, 256) >= 256) TQ_RING(256, 5, 1);
-        else if (cdiv(e.M, 128) * cdiv(e.N, 128) > 256) TQ_RING(128, 5, 2);
-        else TQ_RING(128, 9, 1);
+        const int64_t t128 = cdiv(e.M, 128) * cdiv(e.N, 128);
+        if (cdiv(e.M, 256) * cdiv(e.N, 256) >= 256) TQ_RING(256, 5, 2, 4, 1);
+        else if (t128 > 256) TQ_RING(128, 5, 2, 4, 2);
+        else if (cdiv(e.M, 64) * cdiv(e.N, 64) > 512) TQ_RING(128, 9, 2, 4, 1);
+        else TQ_RING(64, 9, 2, 2, 2);
 #undef TQ_RING
         return;
     }

@@ -59,6 +59,15 @@ def test_sizes(tq, M, N, K, ft):
     check(tq, M, N, K, ft, "gelu_tanh", True, True)
 
 
+# every tile size, with tiles that stick out on both sides and a K that ends inside a block
+@pytest.mark.parametrize("M,N,K", [(1000, 1100, 272), (1500, 1600, 528), (2100, 2200, 144), (4100, 4110, 400),
+                                   (4096, 4096, 2048), (40, 6200, 1040), (30, 7000, 208)])
+@pytest.mark.parametrize("ft,act", [("bf16", "silu"), ("f32", "none")])
+def test_tiles(tq, M, N, K, ft, act):
+    note("product tiles", M, N, K, ft)
+    check(tq, M, N, K, ft, act, True, ft == "bf16")
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("residual", [False, True])
