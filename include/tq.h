@@ -658,8 +658,8 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
  * one call, for a program that knows dloss beforehand: where a workgroup can
  * hold a row, the logits are read once.  dlogits may be the logits themselves
  * (same address and stride).  `workspace`: tq_topk_distill_workspace_bytes(rows,
- * vocab) bytes, 16-byte aligned, contents ignored. */
-size_t tq_topk_distill_workspace_bytes(int64_t rows, int64_t vocab);
+ * vocab, k) bytes, 16-byte aligned, contents ignored. */
+size_t tq_topk_distill_workspace_bytes(int64_t rows, int64_t vocab, int64_t k);
 tq_status tq_topk_distill(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
                           const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
                           const float* teacher_lse, float temperature, float* loss, float* stats, float* rest_sum,
@@ -668,7 +668,7 @@ tq_status tq_topk_distill_backward(const void* logits, int dtype, int64_t rows, 
                                    const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
                                    const float* teacher_lse, float temperature, const float* stats,
                                    const float* rest_sum, const float* dloss, void* dlogits, int64_t d_row_stride,
-                                   void* workspace, size_t workspace_bytes, void* stream);
+                                   void* stream);
 tq_status tq_topk_distill_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
                                const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
                                const float* teacher_lse, float temperature, const float* dloss, float* loss,

@@ -104,10 +104,10 @@ _SIGS = {
     "tq_w8a8_linear_epilogue": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I, _P, _I64, _P, _P, _I, _P], _I),
     "tq_linear_epilogue_backward_workspace_bytes": ([_I64, _I64], _SZ),
     "tq_linear_epilogue_backward": ([_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _SZ, _P], _I),
-    "tq_topk_distill_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_topk_distill_workspace_bytes": ([_I64, _I64, _I64], _SZ),
     "tq_topk_distill": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _P, _SZ, _P], _I),
-    "tq_topk_distill_backward": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _P, _I64, _P,
-                                  _SZ, _P], _I),
+    "tq_topk_distill_backward": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _P, _I64, _P],
+                                 _I),
     "tq_topk_distill_grad": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _I64, _P, _SZ, _P],
                              _I),
     "tq_stream_mix": ([_P, _P, _I64, _I, _I, _I, _I, _P], _I),
@@ -974,24 +974,28 @@ def tq_linear_epilogue_backward_workspace_bytes(M, N):
 
 # ------------------------------------------- distillation from the top logits
 def _distill_args(logits, top_idx, top_val, teacher_lse):
-    if logits.dim() != 2:
+    z, rows, vocab, ld = _rows_of(logits, "logits")
+    if len(logits.shape) != 2:
         raise ValueError("logits must be [rows, vocab]")
     if top_idx.dtype not in (torch.int32, torch.int64):
         raise TypeError("top_idx must be int32 or int64")
-    _ft(top_val)
-    z, rows, vocab, ld = _rows_of(logits, "logits")
-    if top_idx.dim() != 2 or top_idx.shape[0] != rows or top_val.shape != top_idx.shape:
+    shape = top_idx.shape
+    if len(shape) != 2 or shape[0] != rows or top_val.shape != shape:
         raise ValueError("top_idx and top_val must be [rows, k]")
-    if top_idx.device != logits.device or top_val.device != logits.device:
+    dev = logits.device
+    if top_idx.device != dev or top_val.device != dev:
         raise ValueError("top_idx and top_val must be on the logits' device")
     if teacher_lse is not None:
         teacher_lse = _row_vector(teacher_lse, rows, logits, "teacher_lse")
-    nws = _lib.tq_topk_distill_workspace_bytes(rows, vocab)
-    ws = _workspace(logits.device, nws)
     idx, val = top_idx.contiguous(), top_val.contiguous()
-    head = (_ptr(z), _ft(logits), rows, vocab, ld, _ptr(idx), 32 if idx.dtype == torch.int32 else 64, _ptr(val),
-            _ft(val), idx.shape[1], _ptr(teacher_lse))
-    return head, (z, idx, val, teacher_lse), rows, vocab, ws, nws
+    head = (z.data_ptr(), FTYPE[logits.dtype], rows, vocab, ld, idx.data_ptr(),
+            32 if idx.dtype == torch.int32 else 64, val.data_ptr(), _ft(val), shape[1], _ptr(teacher_lse))
+    return head, (z, idx, val, teacher_lse), rows, vocab, dev
+
+
+def _distill_workspace(dev, rows, vocab, k):
+    nws = _lib.tq_topk_distill_workspace_bytes(rows, vocab, k)
+    return _workspace(dev, nws), nws
 
 
 def tq_topk_distill(logits, top_idx, top_val, temperature=1.0, teacher_lse=None):
@@ -1001,11 +1005,12 @@ def tq_topk_distill(logits, top_idx, top_val, temperature=1.0, teacher_lse=None)
     vocabulary counts as one more outcome; without, the teacher's
     probabilities are normalised over its entries.  Returns (loss, stats,
     rest_sum), the latter two for tq_topk_distill_backward."""
-    head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
-    dev = logits.device
+    head, kept, rows, vocab, dev = _distill_args(logits, top_idx, top_val, teacher_lse)
+    ws, nws = _distill_workspace(dev, rows, vocab, head[9])
     loss, stats = _f32(dev, rows), _f32(dev, rows, 2)
     rest = torch.empty_like(loss) if teacher_lse is not None else None
-    _call("tq_topk_distill", *head, temperature, _ptr(loss), _ptr(stats), _ptr(rest), _ptr(ws), nws, _stream(dev))
+    _call("tq_topk_distill", *head, temperature, loss.data_ptr(), stats.data_ptr(), _ptr(rest), _ptr(ws), nws,
+          _stream(dev))
     return loss, stats, rest
 
 
@@ -1013,34 +1018,34 @@ def tq_topk_distill_backward(logits, top_idx, top_val, stats, dloss=None, temper
                              rest_sum=None):
     """dlogits of tq_topk_distill from its inputs and statistics; ``dloss``
     [rows] is the gradient of the losses (ones by default)."""
-    head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
-    head_logits = kept[0]
-    if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != logits.device:
+    head, kept, rows, vocab, dev = _distill_args(logits, top_idx, top_val, teacher_lse)
+    if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != dev:
         raise ValueError("stats must be tq_topk_distill's [rows, 2]")
     if (teacher_lse is None) != (rest_sum is None):
         raise ValueError("rest_sum goes with teacher_lse")
     stats = stats.contiguous()
     rest_sum = None if rest_sum is None else _row_vector(rest_sum, rows, logits, "rest_sum")
     dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
-    dz = torch.empty_like(head_logits, memory_format=torch.contiguous_format)
-    _call("tq_topk_distill_backward", *head, temperature, _ptr(stats), _ptr(rest_sum), _ptr(dloss), _ptr(dz), vocab,
-          _ptr(ws), nws, _stream(logits.device))
+    dz = torch.empty_like(kept[0], memory_format=torch.contiguous_format)
+    _call("tq_topk_distill_backward", *head, temperature, stats.data_ptr(), _ptr(rest_sum), _ptr(dloss),
+          dz.data_ptr(), vocab, _stream(dev))
     return dz
 
 
 def tq_topk_distill_grad(logits, top_idx, top_val, dloss=None, temperature=1.0, teacher_lse=None, inplace=False):
     """(loss, dlogits) in one call, for a program that knows ``dloss`` (ones by
     default) beforehand; ``inplace`` writes the gradient over the logits."""
-    head, kept, rows, vocab, ws, nws = _distill_args(logits, top_idx, top_val, teacher_lse)
+    head, kept, rows, vocab, dev = _distill_args(logits, top_idx, top_val, teacher_lse)
     dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
-    loss = _f32(logits.device, rows)
     if inplace and kept[0] is not logits:
         raise ValueError("in place needs logits whose rows are contiguous")
+    ws, nws = _distill_workspace(dev, rows, vocab, head[9])
+    loss = _f32(dev, rows)
     dz = logits if inplace else torch.empty_like(kept[0], memory_format=torch.contiguous_format)
-    _call("tq_topk_distill_grad", *head, temperature, _ptr(dloss), _ptr(loss), _ptr(dz),
-          head[4] if inplace else vocab, _ptr(ws), nws, _stream(logits.device))
+    _call("tq_topk_distill_grad", *head, temperature, _ptr(dloss), loss.data_ptr(), dz.data_ptr(),
+          head[4] if inplace else vocab, _ptr(ws), nws, _stream(dev))
     return loss, dz
 
 
-def tq_topk_distill_workspace_bytes(rows, vocab):
-    return int(_lib.tq_topk_distill_workspace_bytes(rows, vocab))
+def tq_topk_distill_workspace_bytes(rows, vocab, k):
+    return int(_lib.tq_topk_distill_workspace_bytes(rows, vocab, k))

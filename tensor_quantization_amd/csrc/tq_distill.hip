@@ -26,7 +26,6 @@
 namespace tq {
 
 constexpr int DT_K = 1024;               // most entries per row
-constexpr int DT_COEF = 8;               // floats of a row's coefficients
 
 struct Entries {
     const void* idx;
@@ -47,6 +46,21 @@ __device__ __forceinline__ int entry_col(const Entries& e, int64_t row, int k, i
 __device__ __forceinline__ float entry_val(const Entries& e, int64_t row, int k)
 {
     return load1_rt(e.val, e.val_dt, row * e.K + k, 0.0f);
+}
+
+// A row's entries, read once into LDS by the NT threads of a workgroup.
+struct EntryList {
+    int col[DT_K];
+    float val[DT_K];
+};
+template <int NT>
+__device__ __forceinline__ void load_entries(EntryList& l, const Entries& e, int64_t row, int V)
+{
+#pragma unroll 1
+    for (int i = threadIdx.x; i < e.K; i += NT) {
+        l.col[i] = entry_col(e, row, i, V);
+        l.val[i] = entry_val(e, row, i);
+    }
 }
 
 // 2^x by the exponential unit (x of a probability, at most 0 up to rounding;
@@ -188,15 +202,15 @@ __device__ __forceinline__ void marks_count(Marks<NT, WORDS>& k)
 // Writes every entry's sg p to its rank.  Entries of one column (a row should
 // not have any) are added in entry order by one thread.
 template <int NT, int WORDS>
-__device__ __forceinline__ void marks_fill(Marks<NT, WORDS>& k, const Entries& e, const Coef& q, int64_t row, int V,
+__device__ __forceinline__ void marks_fill(Marks<NT, WORDS>& k, const EntryList& l, const Entries& e, const Coef& q,
                                            int c0, int n, float s, float c)
 {
     const int t = threadIdx.x;
     if (!k.twice) {
 #pragma unroll 1
         for (int i = t; i < e.K; i += NT) {
-            const int col = entry_col(e, row, i, V) - c0;
-            if (col >= 0 && col < n) k.value[rank_of(k, col)] = q.sg * entry_p(e, q, entry_val(e, row, i), s, c);
+            const int col = l.col[i] - c0;
+            if (l.col[i] >= 0 && col >= 0 && col < n) k.value[rank_of(k, col)] = q.sg * entry_p(e, q, l.val[i], s, c);
         }
     } else {
 #pragma unroll 1
@@ -204,9 +218,9 @@ __device__ __forceinline__ void marks_fill(Marks<NT, WORDS>& k, const Entries& e
             float v = 0.0f;
 #pragma unroll 1
             for (int i = 0; i < e.K; ++i) {
-                const int col = entry_col(e, row, i, V) - c0;
-                if (col >= 0 && col < n && rank_of(k, col) == r)
-                    v += q.sg * entry_p(e, q, entry_val(e, row, i), s, c);
+                const int col = l.col[i] - c0;
+                if (l.col[i] >= 0 && col >= 0 && col < n && rank_of(k, col) == r)
+                    v += q.sg * entry_p(e, q, l.val[i], s, c);
             }
             k.value[r] = v;
         }
@@ -241,10 +255,13 @@ __device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, 
 // --------------------------------------------------------------- statistics
 // k_distill_stats: a workgroup per row and part of the row (CH columns): the
 // part's largest logit m, the sum of 2^((z - m) c) over all its columns and
-// over those that are no entries (only with REST).
+// over those that are no entries (only with REST), and the logits at its
+// entries, zk [rows, K] (for the loss, which may be taken after the gradient
+// has overwritten the logits).
 template <int FT, bool REST, int CH>
 __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ z, int64_t ldz, int V, int parts,
-                                                       Entries ent, float c, float* __restrict__ part)
+                                                       Entries ent, float c, float* __restrict__ part,
+                                                       float* __restrict__ zk)
 {
     constexpr int U = 4;
     __shared__ uint32_t bits[REST ? CH / 32 + 1 : 1];
@@ -257,12 +274,15 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
     if constexpr (REST) {
         for (int i = t; i < CH / 32 + 1; i += 256) bits[i] = 0;
         __syncthreads();
-        for (int k = t; k < ent.K; k += 256) {
-            const int col = entry_col(ent, row, k, V) - c0;
-            if (col >= 0 && col < n) atomicOr(&bits[col >> 5], 1u << (col & 31));
-        }
-        __syncthreads();
     }
+    for (int k = t; k < ent.K; k += 256) {
+        const int all = entry_col(ent, row, k, V), col = all - c0;
+        if (all >= 0 && col >= 0 && col < n) {
+            zk[row * ent.K + k] = load1<FT>(z, base + col);
+            if constexpr (REST) atomicOr(&bits[col >> 5], 1u << (col & 31));
+        }
+    }
+    if constexpr (REST) __syncthreads();
     float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
     auto add = [&](float v[8], int lo, uint32_t mask) {
         float top = v[0];
@@ -344,40 +364,21 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
     to[2] = R;
 }
 
-// k_distill_rows: a wave per row.  FROM_PARTS joins the row's parts and
-// writes the loss and the row's statistics (stats[row] = {largest logit, sum of
-// exp(s (z - it))}, rest[row] the same sum over the columns outside the
-// entries); otherwise it reads those statistics.  `coef` (may be null
-// in the first form) gets what the gradient needs.
-template <int FT, bool FROM_PARTS>
-__global__ __launch_bounds__(256) void k_distill_rows(const void* __restrict__ z, int64_t ldz, int64_t rows, int V,
-                                                      Entries ent, float s, float c, const float* __restrict__ part,
-                                                      int parts, const float* __restrict__ dloss,
-                                                      float* __restrict__ loss, float* __restrict__ stats,
-                                                      float* __restrict__ rest_sum, float* __restrict__ coef)
+// k_distill_rows: a wave per row joins the row's parts and writes the loss and
+// the row's statistics: stats[row] = {largest logit, sum of exp(s (z - it))},
+// rest_sum[row] the same sum over the columns outside the entries.
+__global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entries ent, float s, float c,
+                                                      const float* __restrict__ part, const float* __restrict__ zk,
+                                                      int parts, float* __restrict__ loss, float* __restrict__ stats,
+                                                      float* __restrict__ rest_sum)
 {
     const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (row >= rows) return;
     const bool rest = ent.tlse != nullptr;
     float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
-    if constexpr (FROM_PARTS) {
-        const float* from = part + row * parts * 3;
-        for (int i = lane; i < parts; i += 64) m = __builtin_fmaxf(m, from[3 * i]);
-        m = wave_max(m);
-        const float b = base_of(m);
-        for (int i = lane; i < parts; i += 64) {
-            const float f = ex2((from[3 * i] - b) * c);
-            S += from[3 * i + 1] * f;
-            R += from[3 * i + 2] * f;
-        }
-        S = wave_sum(S);
-        R = wave_sum(R);
-    } else {
-        m = stats[2 * row];
-        S = stats[2 * row + 1];
-        R = rest ? rest_sum[row] : 0.0f;
-    }
+    const float* from = part + row * parts * 3;
+    for (int i = lane; i < parts; i += 64) m = __builtin_fmaxf(m, from[3 * i]);
     // the teacher
     float tm = -__builtin_inff(), tsum = 0.0f;
     bool some = false;
@@ -386,6 +387,15 @@ __global__ __launch_bounds__(256) void k_distill_rows(const void* __restrict__ z
             some = true;
             tm = __builtin_fmaxf(tm, entry_val(ent, row, k));
         }
+    m = wave_max(m);
+    const float b = base_of(m);
+    for (int i = lane; i < parts; i += 64) {
+        const float f = ex2((from[3 * i] - b) * c);
+        S += from[3 * i + 1] * f;
+        R += from[3 * i + 2] * f;
+    }
+    S = wave_sum(S);
+    R = wave_sum(R);
     some = __any(some);
     tm = rest ? ent.tlse[row] : base_of(wave_max(tm));
     for (int k = lane; k < ent.K; k += 64)
@@ -395,76 +405,127 @@ __global__ __launch_bounds__(256) void k_distill_rows(const void* __restrict__ z
         }
     tsum = wave_sum(tsum);
     if (!rest && tsum == 0.0f) some = false;      // every entry at -inf
+    float l = 0.0f;
+    if (some)
+        for (int k = lane; k < ent.K; k += 64)
+            if (entry_col(ent, row, k, V) >= 0)
+                l += entry_loss(ent, entry_val(ent, row, k), zk[row * ent.K + k], s, c, tm, tsum, m, S);
+    l = wave_sum(l);
+    if (lane != 0) return;
     float pr;
-    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
-    if constexpr (FROM_PARTS) {
-        float l = 0.0f;
-        if (some)
-            for (int k = lane; k < ent.K; k += 64) {
-                const int col = entry_col(ent, row, k, V);
-                if (col >= 0)
-                    l += entry_loss(ent, entry_val(ent, row, k), load1<FT>(z, row * ldz + col), s, c, tm, tsum, m, S);
-            }
-        l = wave_sum(l) + (lane == 0 && some ? rest_loss(pr, R, S) : 0.0f);
-        if (lane == 0) {
-            loss[row] = l;
-            if (stats) {
-                stats[2 * row] = m;
-                stats[2 * row + 1] = S;
-            }
-            if (rest_sum) rest_sum[row] = R;
-        }
+    make_coef(rest, some, m, S, R, tm, tsum, s, 1.0f, &pr);
+    loss[row] = some ? l + rest_loss(pr, R, S) : 0.0f;
+    if (stats) {
+        stats[2 * row] = m;
+        stats[2 * row + 1] = S;
     }
-    if (coef && lane == 0) {
-        float* to = coef + row * DT_COEF;
-        to[0] = q.m;
-        to[1] = q.in;
-        to[2] = q.out;
-        to[3] = q.sg;
-        to[4] = q.tm;
-        to[5] = q.ti;
-        to[6] = some ? 1.0f : 0.0f;
-    }
+    if (rest_sum) rest_sum[row] = R;
 }
 
-// k_distill_grad: a workgroup per row and part of the row.
-template <int FT, int CH>
+// k_distill_grad: a workgroup per row and part of the row.  Every workgroup
+// derives the row's coefficients itself, from the parts' statistics
+// (FROM_PARTS; the row's first workgroup writes the loss too) or from saved
+// ones, while its first vectors are under way.
+template <int FT, int CH, bool FROM_PARTS>
 __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz, int V, int parts, Entries ent,
-                                                      float s, float c, const float* __restrict__ coef, void* dz,
-                                                      int64_t lddz)
+                                                      float s, float c, const float* __restrict__ part,
+                                                      const float* __restrict__ zk, const float* __restrict__ stats,
+                                                      const float* __restrict__ rest_sum,
+                                                      const float* __restrict__ dloss, float* __restrict__ loss,
+                                                      void* dz, int64_t lddz)
 {
     constexpr int U = 2;
     __shared__ Marks<256, CH / 32 + 1> k;
-    const int t = threadIdx.x;
+    __shared__ EntryList list;
+    __shared__ float red[6][4];
+    __shared__ int any;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int64_t row = blockIdx.x / (unsigned)parts;
-    const int c0 = (int)(blockIdx.x % (unsigned)parts) * CH;
+    const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * CH;
     const int n = V - c0 < CH ? V - c0 : CH, nvec = (n + 7) / 8;
     const int64_t from = row * ldz + c0, to = row * lddz + c0;
-    Coef q;
-    {
-        const float* f = coef + row * DT_COEF;
-        q.m = f[0];
-        q.in = f[1];
-        q.out = f[2];
-        q.sg = f[3];
-        q.tm = f[4];
-        q.ti = f[5];
-        q.some = f[6] != 0.0f;
+    const bool rest = ent.tlse != nullptr;
+    Raw8<FT> raw[U];
+    auto fetch = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = load8_any<FT>(z, from + vec8(v0 + 256 * u, n).at);
+    };
+    if (n >= 8) fetch(t);
+
+    if (t == 0) any = 0;
+    marks_clear(k);
+    load_entries<256>(list, ent, row, V);
+    float m = -__builtin_inff();
+    const float* of = part + row * parts * 3;
+    if constexpr (FROM_PARTS)
+        for (int i = t; i < parts; i += 256) m = __builtin_fmaxf(m, of[3 * i]);
+    __syncthreads();
+    float tm = -__builtin_inff();
+    for (int i = t; i < ent.K; i += 256) {
+        if (list.col[i] < 0) continue;
+        any = 1;
+        tm = __builtin_fmaxf(tm, list.val[i]);
+        const int col = list.col[i] - c0;
+        if (col >= 0 && col < n) mark(k, col);
     }
-    if (!q.some) {                       // uniform: no entries, no gradient
+    auto four = [&](int i) { return lane < 4 ? red[i][lane] : 0.0f; };
+    tm = wave_max(tm);
+    m = wave_max(m);
+    if (lane == 0) {
+        red[0][wave] = tm;
+        red[1][wave] = m;
+    }
+    __syncthreads();
+    tm = rest ? ent.tlse[row] : base_of(wave_max(lane < 4 ? red[0][lane] : -__builtin_inff()));
+    float S = 0.0f, R = 0.0f, tsum = 0.0f;
+    if constexpr (FROM_PARTS) {
+        m = wave_max(lane < 4 ? red[1][lane] : -__builtin_inff());
+        const float b = base_of(m);
+        for (int i = t; i < parts; i += 256) {
+            const float f = ex2((of[3 * i] - b) * c);
+            S += of[3 * i + 1] * f;
+            R += of[3 * i + 2] * f;
+        }
+    }
+    for (int i = t; i < ent.K; i += 256)
+        if (list.col[i] >= 0) tsum += rest ? ex2((list.val[i] * s - tm) * LOG2E) : ex2((list.val[i] - tm) * c);
+    tsum = wave_sum(tsum);
+    S = wave_sum(S);
+    R = wave_sum(R);
+    if (lane == 0) {
+        red[2][wave] = tsum;
+        red[3][wave] = S;
+        red[4][wave] = R;
+    }
+    marks_count(k);                      // its barrier also publishes the sums
+    __syncthreads();
+    tsum = wave_sum(four(2));
+    if constexpr (FROM_PARTS) {
+        S = wave_sum(four(3));
+        R = wave_sum(four(4));
+    } else {
+        m = stats[2 * row];
+        S = stats[2 * row + 1];
+        R = rest ? rest_sum[row] : 0.0f;
+    }
+    const bool some = any && (rest || tsum != 0.0f);
+    float pr;
+    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+    if (FROM_PARTS && p == 0) {          // uniform
+        float l = 0.0f;
+        for (int i = t; i < (some ? ent.K : 0); i += 256)
+            if (list.col[i] >= 0) l += entry_loss(ent, list.val[i], zk[row * ent.K + i], s, c, tm, tsum, m, S);
+        l = wave_sum(l);
+        if (lane == 0) red[5][wave] = l;
+        __syncthreads();
+        l = wave_sum(four(5));
+        if (t == 0) loss[row] = some ? l + rest_loss(pr, R, S) : 0.0f;
+    }
+    if (!some) {                         // uniform: no entries, no gradient
         for (int j = t; j < n; j += 256) store1<FT>(dz, to + j, 0.0f);
         return;
     }
-    marks_clear(k);
-    __syncthreads();
-    for (int i = t; i < ent.K; i += 256) {
-        const int col = entry_col(ent, row, i, V) - c0;
-        if (col >= 0 && col < n) mark(k, col);
-    }
-    __syncthreads();
-    marks_count(k);
-    __syncthreads();
-    marks_fill(k, ent, q, row, V, c0, n, s, c);
+    marks_fill(k, list, ent, q, c0, n, s, c);
     __syncthreads();
     auto x = [&](float v) { return ex2((v - q.m) * c); };
     if (n < 8) {
@@ -476,20 +537,18 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
         return;
     }
     for (int v0 = t; v0 < nvec; v0 += 256 * U) {
-        Raw8<FT> raw[U];
-        Vec8 at[U];
+        Raw8<FT> now[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = raw[u];
+        if (v0 + 256 * U < nvec) fetch(v0 + 256 * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            at[u] = vec8(v0 + 256 * u, n);
-            raw[u] = load8_any<FT>(z, from + at[u].at);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (at[u].lo == 8) continue;
+            const Vec8 at = vec8(v0 + 256 * u, n);
+            if (at.lo == 8) continue;
             float v[8];
-            widen8<FT>(raw[u], v);
-            grad8(k, q, at[u].at, v, x);
-            store8_own<FT>(dz, to, at[u], v);
+            widen8<FT>(now[u], v);
+            grad8(k, q, at.at, v, x);
+            store8_own<FT>(dz, to, at, v);
         }
     }
 }
@@ -516,6 +575,7 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
     constexpr int NW = NT / 64, ES = FT == F32 ? 4 : 2;
     __shared__ Marks<NT, NT * W / 4 + 1> k;
     __shared__ float red[6][NW], tails[8];
+    __shared__ EntryList list;
     __shared__ int any;
     const bool rest = ent.tlse != nullptr;
     // V / 8 whole vectors (absent ones read the last again), and an element more for the first V % 8 threads
@@ -546,15 +606,16 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
     if (t < 8) tails[t] = tail;          // read by the same threads
     if (t == 0) any = 0;
     marks_clear(k);
+    load_entries<NT>(list, ent, row, V);
     __syncthreads();
     float tm = -__builtin_inff();
 #pragma unroll 1
     for (int i = t; i < ent.K; i += NT) {
-        const int col = entry_col(ent, row, i, V);
+        const int col = list.col[i];
         if (col >= 0) {
             any = 1;
             mark(k, col);
-            tm = __builtin_fmaxf(tm, entry_val(ent, row, i));
+            tm = __builtin_fmaxf(tm, list.val[i]);
         }
     }
     tm = wave_max(tm);
@@ -571,8 +632,8 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
     float tsum = 0.0f;
 #pragma unroll 1
     for (int i = t; i < ent.K; i += NT)
-        if (entry_col(ent, row, i, V) >= 0) {
-            const float x = entry_val(ent, row, i);
+        if (list.col[i] >= 0) {
+            const float x = list.val[i];
             tsum += rest ? ex2((x * s - tm) * LOG2E) : ex2((x - tm) * c);
         }
 
@@ -663,12 +724,12 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
     if (!rest && tsum == 0.0f) some = false;
     float pr;
     const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
-    if (q.some) marks_fill(k, ent, q, row, V, 0, V, s, c);
+    if (q.some) marks_fill(k, list, ent, q, 0, V, s, c);
     float l = 0.0f;
 #pragma unroll 1
     for (int i = t; i < (q.some ? ent.K : 0); i += NT) {
-        const int col = entry_col(ent, row, i, V);
-        if (col >= 0) l += entry_loss(ent, entry_val(ent, row, i), load1<FT>(from, col), s, c, tm, tsum, m, S);
+        const int col = list.col[i];
+        if (col >= 0) l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S);
     }
     l = wave_sum(l);
     if ((t & 63) == 0) red[5][wave] = l;
@@ -738,33 +799,39 @@ struct Distill {
     float s, c;
 };
 
+// Workspace: the parts' statistics, then the logits at the entries.
+inline size_t distill_part_floats(int64_t rows, int64_t V) { return 3 * (size_t)rows * (size_t)cdiv(V, distill_ch(rows, V)); }
+
 template <int FT>
-static void stats_launch(const Distill& d, int ch, float* part, hipStream_t st)
+static void stats_launch(const Distill& d, float* ws, hipStream_t st)
 {
-    const int parts = (int)cdiv(d.V, ch);
+    const int ch = distill_ch(d.rows, d.V), parts = (int)cdiv(d.V, ch);
     const dim3 grid((unsigned)(d.rows * parts));
+    float* zk = ws + distill_part_floats(d.rows, d.V);
     if (d.ent.tlse)
         TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
-                                            parts, d.ent, d.c, part));
+                                            parts, d.ent, d.c, ws, zk));
     else
         TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
-                                            parts, d.ent, d.c, part));
+                                            parts, d.ent, d.c, ws, zk));
+}
+
+static void rows_launch(const Distill& d, const float* ws, float* loss, float* stats, float* rest_sum, hipStream_t st)
+{
+    hipLaunchKernelGGL(k_distill_rows, dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.rows, d.V, d.ent, d.s, d.c,
+                       ws, ws + distill_part_floats(d.rows, d.V), (int)cdiv(d.V, distill_ch(d.rows, d.V)), loss, stats,
+                       rest_sum);
 }
 
 template <int FT, bool FROM_PARTS>
-static void rows_launch(const Distill& d, int parts, const float* part, const float* dloss, float* loss, float* stats,
-                        float* rest_sum, float* coef, hipStream_t st)
+static void grad_launch(const Distill& d, const float* ws, const float* stats, const float* rest_sum,
+                        const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_distill_rows<FT, FROM_PARTS>), dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.z, d.ldz,
-                       d.rows, d.V, d.ent, d.s, d.c, part, parts, dloss, loss, stats, rest_sum, coef);
-}
-
-template <int FT>
-static void grad_launch(const Distill& d, int ch, const float* coef, void* dz, int64_t lddz, hipStream_t st)
-{
-    const int parts = (int)cdiv(d.V, ch);
-    TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV>), dim3((unsigned)(d.rows * parts)), dim3(256), 0, st,
-                                        d.z, d.ldz, d.V, parts, d.ent, d.s, d.c, coef, dz, lddz));
+    const int ch = distill_ch(d.rows, d.V), parts = (int)cdiv(d.V, ch);
+    const float* zk = FROM_PARTS ? ws + distill_part_floats(d.rows, d.V) : nullptr;
+    TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV, FROM_PARTS>), dim3((unsigned)(d.rows * parts)),
+                                        dim3(256), 0, st, d.z, d.ldz, d.V, parts, d.ent, d.s, d.c, ws, zk, stats,
+                                        rest_sum, dloss, loss, dz, lddz));
 }
 
 // The row is held from this many rows on (fewer leave CUs idle, and the
@@ -818,9 +885,9 @@ static tq_status distill_check(const void* logits, int dt, int64_t rows, int64_t
     return TQ_OK;
 }
 
-static tq_status workspace_check(const void* ws, size_t have, int64_t rows, int64_t vocab)
+static tq_status workspace_check(const void* ws, size_t have, int64_t rows, int64_t vocab, int64_t k)
 {
-    if (!ws || have < tq_topk_distill_workspace_bytes(rows, vocab)) return TQ_ERR_INVALID;
+    if (!ws || have < tq_topk_distill_workspace_bytes(rows, vocab, k)) return TQ_ERR_INVALID;
     return aligned16(ws) ? TQ_OK : TQ_ERR_ALIGN;
 }
 
@@ -830,10 +897,10 @@ using namespace tq;
 
 extern "C" {
 
-size_t tq_topk_distill_workspace_bytes(int64_t rows, int64_t vocab)
+size_t tq_topk_distill_workspace_bytes(int64_t rows, int64_t vocab, int64_t k)
 {
-    if (rows <= 0 || vocab <= 0) return 0;
-    return (size_t)rows * (DT_COEF + 3 * (size_t)cdiv(vocab, distill_ch(rows, vocab))) * sizeof(float);
+    if (rows <= 0 || vocab <= 0 || k <= 0) return 0;
+    return (distill_part_floats(rows, vocab) + (size_t)rows * (size_t)k) * sizeof(float);
 }
 
 tq_status tq_topk_distill(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
@@ -848,15 +915,11 @@ tq_status tq_topk_distill(const void* logits, int dtype, int64_t rows, int64_t v
     if (r != TQ_OK || !work) return r;
     if (!loss) return TQ_ERR_INVALID;
     if (!natural(loss, 4) || !natural(stats, 4) || !natural(rest_sum, 4)) return TQ_ERR_ALIGN;
-    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab)) != TQ_OK) return r;
-    const int ch = distill_ch(rows, vocab);
-    float* part = static_cast<float*>(workspace) + rows * DT_COEF;
+    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab, k)) != TQ_OK) return r;
+    float* ws = static_cast<float*>(workspace);
     hipStream_t st = as_stream(stream);
-    TQ_LLM_FT_SWITCH(dtype, {
-        stats_launch<FTV>(d, ch, part, st);
-        rows_launch<FTV, true>(d, (int)cdiv(vocab, ch), part, nullptr, loss, stats, teacher_lse ? rest_sum : nullptr,
-                               nullptr, st);
-    });
+    TQ_LLM_FT_SWITCH(dtype, stats_launch<FTV>(d, ws, st));
+    rows_launch(d, ws, loss, stats, teacher_lse ? rest_sum : nullptr, st);
     return launch_status();
 }
 
@@ -864,24 +927,18 @@ tq_status tq_topk_distill_backward(const void* logits, int dtype, int64_t rows, 
                                    const void* top_idx, int idx_bits, const void* top_val, int val_dtype, int64_t k,
                                    const float* teacher_lse, float temperature, const float* stats,
                                    const float* rest_sum, const float* dloss, void* dlogits, int64_t d_row_stride,
-                                   void* workspace, size_t workspace_bytes, void* stream)
+                                   void* stream)
 {
     Distill d;
     bool work;
-    tq_status r = distill_check(logits, dtype, rows, vocab, row_stride, top_idx, idx_bits, top_val, val_dtype, k,
-                                teacher_lse, temperature, &d, &work);
+    const tq_status r = distill_check(logits, dtype, rows, vocab, row_stride, top_idx, idx_bits, top_val, val_dtype, k,
+                                      teacher_lse, temperature, &d, &work);
     if (r != TQ_OK || !work) return r;
     if (!stats || (teacher_lse && !rest_sum) || !dlogits || d_row_stride < vocab) return TQ_ERR_INVALID;
     if (!natural(stats, 4) || !natural(rest_sum, 4) || !natural(dloss, 4) || !natural(dlogits, ftype_size(dtype)))
         return TQ_ERR_ALIGN;
-    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab)) != TQ_OK) return r;
-    float* coef = static_cast<float*>(workspace);
-    hipStream_t st = as_stream(stream);
-    TQ_LLM_FT_SWITCH(dtype, {
-        rows_launch<FTV, false>(d, 0, nullptr, dloss, nullptr, const_cast<float*>(stats), const_cast<float*>(rest_sum),
-                                coef, st);
-        grad_launch<FTV>(d, distill_ch(rows, vocab), coef, dlogits, d_row_stride, st);
-    });
+    TQ_LLM_FT_SWITCH(dtype, (grad_launch<FTV, false>(d, nullptr, stats, rest_sum, dloss, nullptr, dlogits, d_row_stride,
+                                                     as_stream(stream))));
     return launch_status();
 }
 
@@ -898,16 +955,13 @@ tq_status tq_topk_distill_grad(const void* logits, int dtype, int64_t rows, int6
     if (r != TQ_OK || !work) return r;
     if (!loss || !dlogits || d_row_stride < vocab) return TQ_ERR_INVALID;
     if (!natural(loss, 4) || !natural(dloss, 4) || !natural(dlogits, ftype_size(dtype))) return TQ_ERR_ALIGN;
-    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab)) != TQ_OK) return r;
-    const int ch = distill_ch(rows, vocab);
-    float* coef = static_cast<float*>(workspace);
-    float* part = coef + rows * DT_COEF;
+    if ((r = workspace_check(workspace, workspace_bytes, rows, vocab, k)) != TQ_OK) return r;
+    float* ws = static_cast<float*>(workspace);
     hipStream_t st = as_stream(stream);
     TQ_LLM_FT_SWITCH(dtype, {
         if (!held_launch<FTV>(d, dloss, loss, dlogits, d_row_stride, st)) {
-            stats_launch<FTV>(d, ch, part, st);
-            rows_launch<FTV, true>(d, (int)cdiv(vocab, ch), part, dloss, loss, nullptr, nullptr, coef, st);
-            grad_launch<FTV>(d, ch, coef, dlogits, d_row_stride, st);
+            stats_launch<FTV>(d, ws, st);
+            grad_launch<FTV, true>(d, ws, nullptr, nullptr, dloss, loss, dlogits, d_row_stride, st);
         }
     });
     return launch_status();

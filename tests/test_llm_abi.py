@@ -84,7 +84,7 @@ def test_epilogue_refusals(tq):
 
 def test_distill_refusals(tq):
     L, INV, UNS, ALIGN = tq._lib, tq.TQ_ERR_INVALID, tq.TQ_ERR_UNSUPPORTED, tq.TQ_ERR_ALIGN
-    n = tq.tq_topk_distill_workspace_bytes(4, 100)
+    n = tq.tq_topk_distill_workspace_bytes(4, 100, 5)
     ok = dict(z=A, dt=2, rows=4, V=100, ld=100, idx=A, bits=64, val=B, vdt=0, k=5, tlse=None, T=1.0, dloss=None,
               loss=C, dz=B, ldd=100, ws=A, n=n, st=None)
 
@@ -105,16 +105,16 @@ def test_distill_refusals(tq):
     f = L.tq_topk_distill
     assert f(A, 2, 4, 100, 100, A, 64, B, 0, 5, None, 1.0, None, None, None, A, n, None) == INV   # no loss
     b = L.tq_topk_distill_backward
-    assert b(A, 2, 4, 100, 100, A, 64, B, 0, 5, None, 1.0, None, None, None, B, 100, A, n, None) == INV  # no stats
-    assert b(A, 2, 4, 100, 100, A, 64, B, 0, 5, C, 1.0, C, None, None, B, 100, A, n, None) == INV        # no rest
+    assert b(A, 2, 4, 100, 100, A, 64, B, 0, 5, None, 1.0, None, None, None, B, 100, None) == INV  # no stats
+    assert b(A, 2, 4, 100, 100, A, 64, B, 0, 5, C, 1.0, C, None, None, B, 100, None) == INV        # no rest
 
 
 def test_workspaces_grow_with_what_they_hold(tq):
     assert tq.tq_layer_norm_backward_workspace_bytes(0, 64) == 0
     assert tq.tq_linear_epilogue_backward_workspace_bytes(64, 0) == 0
-    assert tq.tq_topk_distill_workspace_bytes(0, 5) == 0
+    assert tq.tq_topk_distill_workspace_bytes(0, 5, 5) == 0
     for rows in (1, 100, 10000):
         for cols in (1, 5, 4096, 40000):
             parts = tq.tq_layer_norm_backward_workspace_bytes(rows, cols) // 8
             assert parts >= (cols + 3) // 4 * 4 * min(rows, 1)
-            assert tq.tq_topk_distill_workspace_bytes(rows, cols) >= rows * 4 * 11
+            assert tq.tq_topk_distill_workspace_bytes(rows, cols, 7) >= rows * 4 * 10
