@@ -312,13 +312,12 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
 }
 
 // -------------------------------------------------------------- many tokens
-// k_epi_tile: a 128 x 128 output tile per 256-thread workgroup, wave w the
-// 64 x 64 quarter (w / 2, w % 2) as 4 x 4 tiles of 16 x 16.  Any K and any
-// alignment: a thread loads four 16-code chunks of each operand into registers
-// one 128-code block ahead and writes them to LDS (zeros past K).  The product
-// is taken as D^T, so a lane holds four consecutive columns of a row; at the
-// end each wave lays its quarter out in LDS and finishes it eight columns at a
-// time, so that stores are whole and the epilogue's code exists once.
+// Output tiles of TILE x TILE, K in blocks of 128 codes.  A row of a block is
+// 128 bytes of LDS in eight 16-byte chunks, their order turned by the row so
+// that the sixteen rows of a matrix operand meet all banks.  The product is
+// taken as D^T, so a lane holds four consecutive columns of a row; at the end
+// each wave lays its part out in LDS and finishes it eight columns at a time,
+// so that stores are whole and the epilogue's code exists once.
 constexpr int ET = 128;
 __device__ __forceinline__ int eslot(int row, int chunk) { return row * ET + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
@@ -464,72 +463,6 @@ __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0
     else finish_any<YT, NM, NN>(e, cc, m0, acc, stage);
 }
 
-template <int YT>
-__global__ __launch_bounds__(256) void k_epi_tile(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
-                                                  int64_t K, Epi e)
-{
-    __shared__ __attribute__((aligned(16))) union {
-        uint8_t in[2][2][ET * ET];
-        int out[4][Stage<4, 4>::INTS];
-    } lds;
-    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int l16 = lane & 15, g4 = lane >> 4, wm = w >> 1, wn = w & 1;
-    const int64_t m0 = (int64_t)blockIdx.y * ET, n0 = (int64_t)blockIdx.x * ET;
-    const int64_t nkb = (K + ET - 1) / ET;
-    const int fr = t >> 3, fc = t & 7;   // chunk fc of rows fr, fr + 32, + 64, + 96
-    const int8_t* pa[4];
-    const int8_t* pb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + fr + 32 * i, n = n0 + fr + 32 * i;
-        pa[i] = qx + (m < e.M ? m : e.M - 1) * K;
-        pb[i] = qw + (n < e.N ? n : e.N - 1) * K;
-    }
-    v4i ra[4], rb[4];
-    auto fetch = [&](int64_t kb) {
-        const int64_t k = kb * ET + 16 * fc;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ra[i] = codes16(pa[i], k, K);
-            rb[i] = codes16(pb[i], k, K);
-        }
-    };
-    v4i acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4i{};
-    fetch(0);
-    for (int64_t kb = 0; kb < nkb; ++kb) {
-        uint8_t* la = lds.in[kb & 1][0];
-        uint8_t* lb = lds.in[kb & 1][1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<v4i*>(&la[eslot(fr + 32 * i, fc)]) = ra[i];
-            *reinterpret_cast<v4i*>(&lb[eslot(fr + 32 * i, fc)]) = rb[i];
-        }
-        // the buffer written next was last read before this barrier
-        __syncthreads();
-        if (kb + 1 < nkb) fetch(kb + 1);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            v4i av[4], bv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                av[i] = *reinterpret_cast<const v4i*>(&la[eslot(wm * 64 + i * 16 + l16, 4 * s + g4)]);
-                bv[i] = *reinterpret_cast<const v4i*>(&lb[eslot(wn * 64 + i * 16 + l16, 4 * s + g4)]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[j], av[i], acc[i][j], 0, 0, 0);
-        }
-    }
-    __syncthreads();                     // the operands give way to the staged sums
-    finish_part<YT, 4, 4>(e, m0 + 64 * wm, n0 + 64 * wn, acc, lds.out[w]);
-}
-
 // k_epi_ring: operands whose rows start at 16-byte addresses.  A TILE x TILE
 // output tile per workgroup of WM x WN waves, a wave a TILE / WM x TILE / WN
 // part of it.  LDS is a ring of RING units, a unit one operand's [TILE x 128
@@ -611,6 +544,111 @@ __device__ __forceinline__ void tile_of(int64_t nt, int64_t mt, int slab, int64_
     const int64_t at = L % per;
     tn = first + at % wide;
     tm = at / wide;
+}
+
+// k_epi_tile: operands of any alignment and K.  Direct loads to LDS take
+// 16-byte addresses only, so the codes pass through registers: a thread loads
+// its chunks of both operands at any byte address D blocks ahead (the loop is
+// unrolled by D, each block's registers refilled as they are written out) and
+// the blocks alternate between two LDS buffers, one barrier per block.
+// Measured, 777 x 4096 x 4095 35 us (aligned operands: 20), 8192 x 11008 x
+// 4088 416 us (330): bound by the loads, whose 16 bytes per lane straddle
+// lines.  One block ahead only: 52 / 485 us.
+template <int YT, int TILE, int WM, int WN, int D, int WGS>
+__global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_tile(const int8_t* __restrict__ qx,
+                                                                              const int8_t* __restrict__ qw, int64_t K,
+                                                                              int64_t nt, int64_t mt, int slab, Epi e)
+{
+    constexpr int WAVES = WM * WN, NT = 64 * WAVES;
+    constexpr int QM = TILE / WM, QN = TILE / WN, NM = QM / 16, NN = QN / 16;   // a wave's part and its 16-wide tiles
+    constexpr int RPL = NT / 8, L = TILE / RPL;                                 // rows per load, loads per operand
+    static_assert(D % 2 == 0, "blocks alternate between two buffers");
+    __shared__ __attribute__((aligned(16))) union {
+        uint8_t in[2][2][TILE * ET];
+        int out[WAVES][Stage<NM, NN>::INTS];
+    } lds;
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int l16 = lane & 15, g4 = lane >> 4, wm = w / WN, wn = w % WN;
+    int64_t tm, tn;
+    tile_of(nt, mt, slab, tm, tn);
+    const int64_t m0 = tm * TILE, n0 = tn * TILE;
+    const int fr = t >> 3, fc = t & 7;   // chunk fc of rows fr, fr + RPL, ...
+    const int8_t* ga = qx + m0 * K;
+    const int8_t* gb = qw + n0 * K;
+    uint32_t oa[L], ob[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const int r = fr + RPL * i;
+        oa[i] = (uint32_t)(m0 + r < e.M ? r : (int)(e.M - 1 - m0)) * (uint32_t)K;
+        ob[i] = (uint32_t)(n0 + r < e.N ? r : (int)(e.N - 1 - n0)) * (uint32_t)K;
+    }
+    v4i ra[D][L], rb[D][L];
+    auto fetch = [&](int u, int kb) {    // a whole block
+        const int k = kb * ET + 16 * fc;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            ra[u][i] = codes16_whole(ga + k + oa[i]);
+            rb[u][i] = codes16_whole(gb + k + ob[i]);
+        }
+    };
+    v4i acc[NM][NN];
+#pragma unroll
+    for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int j = 0; j < NN; ++j) acc[i][j] = v4i{};
+    auto block = [&](int buf, const v4i (&a)[L], const v4i (&b)[L], auto refill) {
+        uint8_t* la = lds.in[buf][0];
+        uint8_t* lb = lds.in[buf][1];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            *reinterpret_cast<v4i*>(&la[eslot(fr + RPL * i, fc)]) = a[i];
+            *reinterpret_cast<v4i*>(&lb[eslot(fr + RPL * i, fc)]) = b[i];
+        }
+        // the buffer written next was last read before this barrier
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        refill();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            v4i av[NM], bv[NN];
+#pragma unroll
+            for (int i = 0; i < NM; ++i) av[i] = *reinterpret_cast<const v4i*>(&la[eslot(wm * QM + i * 16 + l16, 4 * s + g4)]);
+#pragma unroll
+            for (int j = 0; j < NN; ++j) bv[j] = *reinterpret_cast<const v4i*>(&lb[eslot(wn * QN + j * 16 + l16, 4 * s + g4)]);
+#pragma unroll
+            for (int i = 0; i < NM; ++i)
+#pragma unroll
+                for (int j = 0; j < NN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[j], av[i], acc[i][j], 0, 0, 0);
+        }
+    };
+    const int whole = (int)(K / ET);
+    if (whole > 0) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) fetch(u, u < whole ? u : whole - 1);
+        int kb = 0;
+        for (; kb + D <= whole; kb += D)
+#pragma unroll
+            for (int u = 0; u < D; ++u)
+                // past the end the last block again: an unconditional load leaves the waits of the others exact
+                block(u & 1, ra[u], rb[u], [&] { fetch(u, kb + u + D < whole ? kb + u + D : whole - 1); });
+#pragma unroll
+        for (int u = 0; u < D - 1; ++u)
+            if (kb + u < whole) block(u & 1, ra[u], rb[u], [] {});
+    }
+    __syncthreads();
+    if (K % ET) {                        // the rest of K, zeros past it
+        const int64_t k = (int64_t)whole * ET + 16 * fc;
+        v4i a[L], b[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            a[i] = codes16(ga + oa[i], k, K);
+            b[i] = codes16(gb + ob[i], k, K);
+        }
+        block(0, a, b, [] {});
+        __syncthreads();
+    }
+    // the operands give way to the staged sums
+    finish_part<YT, NM, NN>(e, m0 + QM * wm, n0 + QN * wn, acc, lds.out[w]);
 }
 
 template <int YT, int TILE, int RING, int WM, int WN, int WGS>
@@ -866,7 +904,12 @@ inline int64_t epi_chunk(int64_t M, int64_t N)
 // round of resident workgroups (two 64 x 64 tiles or, up to 256 of them, one
 // 128 x 128 tile per CU), so the smallest tile that needs one round is taken,
 // and the largest once it fills the chip.  128 x 128 tiles beyond one round run
-// two to a CU on shorter rings.
+// two to a CU on shorter rings.  Operands of other alignments (k_epi_tile, us;
+// 64 / 128 / 256 tile):
+//   243 x 2546 x 9000    26.7 / 51 / -      777 x 4096 x 4095     57 / 35 / 81
+//   2564 x 614 x 2708    20.5 / 21.8 / -    2048 x 4096 x 4098    87 / 58 / 75
+//   1024 x 11008 x 4088    - / 71 / 67      4096 x 4096 x 4088     - / 96 / 75
+// where the largest tile pays a little before it fills the chip.
 template <int YT>
 static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Epi& e, hipStream_t st)
 {
@@ -898,8 +941,17 @@ static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const 
 #undef TQ_RING
         return;
     }
-    const dim3 grid((unsigned)cdiv(e.N, ET), (unsigned)cdiv(e.M, ET));
-    hipLaunchKernelGGL((k_epi_tile<YT>), grid, dim3(256), 0, st, qx, qw, K, e);
+#define TQ_TILE(TILE, WM, WN, D, WGS)                                                                        \
+    do {                                                                                                     \
+        const int64_t nt = cdiv(e.N, TILE), mt = cdiv(e.M, TILE);                                            \
+        const int slab = (int)std::min<int64_t>(cdiv(nt, 8), 16);                                            \
+        hipLaunchKernelGGL((k_epi_tile<YT, TILE, WM, WN, D, WGS>), dim3((unsigned)(nt * mt)),                \
+                           dim3(64 * WM * WN), 0, st, qx, qw, K, nt, mt, slab, e);                           \
+    } while (0)
+    if (cdiv(e.M, 256) * cdiv(e.N, 256) > 160) TQ_TILE(256, 2, 4, 2, 1);
+    else if (cdiv(e.M, 64) * cdiv(e.N, 64) > 512) TQ_TILE(128, 2, 4, 2, 2);
+    else TQ_TILE(64, 2, 2, 4, 2);
+#undef TQ_TILE
 }
 
 static bool natural(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(ftype_size(dt) - 1)) == 0; }

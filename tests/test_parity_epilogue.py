@@ -68,6 +68,26 @@ def test_tiles(tq, M, N, K, ft, act):
     check(tq, M, N, K, ft, act, True, ft == "bf16")
 
 
+# operands of other alignments: every number of whole blocks in flight, every tile size
+@pytest.mark.parametrize("M,N,K", [(100, 130, k) for k in (1, 127, 129, 250, 257, 385, 513, 645, 1030)] +
+                         [(1500, 1600, 389), (1500, 1600, 650), (2900, 4110, 131), (2900, 4110, 520), (4100, 4100, 261)])
+def test_any_alignment(tq, M, N, K):
+    note("product any alignment", M, N, K)
+    check(tq, M, N, K, "bf16", "silu", True, True)
+
+
+@pytest.mark.parametrize("M", [5, 30, 70, 300])
+def test_operands_that_start_anywhere(tq, M):
+    N, K = 200, 512
+    g = torch.Generator().manual_seed(M)
+    qx = torch.randint(-128, 128, (M * K + 3,), generator=g, dtype=torch.int8)[3:].view(M, K)
+    qw = torch.randint(-128, 128, (N * K + 9,), generator=g, dtype=torch.int8)[9:].view(N, K)
+    dx, dw = (torch.empty(v.numel() + 5, dtype=torch.int8, device="cuda")[5:].view(v.shape).copy_(v) for v in (qx, qw))
+    one = torch.ones
+    y = tq.tq_w8a8_linear_epilogue(dx, one(M).cuda(), dw, one(N).cuda(), out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), qx.double() @ qw.double().T)    # sums below 2^24
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("residual", [False, True])
