@@ -834,14 +834,21 @@ static void grad_launch(const Distill& d, const float* ws, const float* stats, c
                                         rest_sum, dloss, loss, dz, lddz));
 }
 
-// The row is held from this many rows on (fewer leave CUs idle, and the
-// parts of a row spread over them instead), where a workgroup can hold it.
+// Whether the joint call holds its rows in registers.  A row in registers costs
+// one read instead of two, and spreads over no more than one workgroup: rows of
+// 64 KB (a workgroup of 256 threads) are held at any number of them; of 128 KB
+// from DT_HELD_ROWS of them on; of 256 KB, which take a CU each, where they
+// fill at least 5/8 of their rounds over the CUs.  Measured, us, held / in
+// parts:   1 row of 32000 bf16 12.1 / 14.6, 256 rows 13.0 / 17.3;   64 rows of
+// 65536 bf16 15.7 / 14.5, 128 rows 16.6 / 17.4;   rows of 131072 bf16: 128 of
+// them 26.4 / 22.4, 160 28.2 / 29.1, 300 58 / 47, 512 66 / 88, 4096 482 / 640.
 constexpr int64_t DT_HELD_ROWS = 128;
 template <int FT>
 static bool held_launch(const Distill& d, const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
 {
     constexpr int H = FT == F32 ? 2 : 1;  // binary32 rows hold half as many elements
-    if (d.rows < DT_HELD_ROWS || d.V < 8 || d.V > (FT == F32 ? 65536 : 131072)) return false;
+    if (d.V < 8 || d.V > 131072 / H) return false;
+    if (d.V > 65536 / H ? 8 * d.rows < 5 * 256 * cdiv(d.rows, 256) : d.V > 32768 / H && d.rows < DT_HELD_ROWS) return false;
     // as many workgroups as fit on the chip by their registers
 #define TQ_HELD(NT, W)                                                                                            \
     hipLaunchKernelGGL((k_distill_held<FT, NT, W>), dim3((unsigned)std::min<int64_t>(d.rows, 256 * (1024 / NT) * \

@@ -224,8 +224,9 @@ __global__ __launch_bounds__(1024) void k_ln_loop(const void* __restrict__ x, in
 // units of its BT / NT teams); each thread keeps the sums of dy h and dy of
 // its own columns in registers over all its rows, the teams add theirs in LDS
 // in a fixed order at the end, and the workgroup leaves one row of partial
-// sums.  The rows of the next step are
-// loaded before the sums of the present one are taken.
+// sums.  The rows of the next step are loaded before the sums of the present
+// one are taken.  Rows of more than 8192 columns keep the sums in LDS, each
+// thread its own, where registers would not hold them beside two rows.
 template <int FT, int NT, int W, int BT>
 __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int64_t lddy, const void* __restrict__ x,
                                                int64_t ldx, int64_t rows, int64_t cols,
@@ -234,20 +235,27 @@ __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int6
                                                void* __restrict__ dx, float* __restrict__ part, int64_t ldp)
 {
     constexpr int TEAMS = BT / NT, NW = NT / 64;
+    constexpr bool IN_LDS = 8 * NT * W > 8192;
     __shared__ float slots[2][TEAMS][NW][2];
     __shared__ float fold[TEAMS > 1 ? 8 * NT * W : 1];
+    __shared__ float4 sums[IN_LDS ? 4 * NT * W : 1];     // [w][dw 0 .. 3, 4 .. 7, db 0 .. 3, 4 .. 7][t]
     const int t = threadIdx.x % NT, team = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
 
     Vec8 at[W];
-    float ww[W][8], dw[W][8], db[W][8];
+    float ww[W][8], dw[W][8], db[W][8];           // the sums unused with IN_LDS
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         at[w] = vec8(w * NT + t, (int)cols);
         widen8_rt(load8_rt(weight, wdt, at[w].at), weight, wdt, 1.0f, ww[w]);
+        if constexpr (IN_LDS) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            dw[w][i] = 0.0f;
-            db[w][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) sums[(4 * w + i) * NT + t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dw[w][i] = 0.0f;
+                db[w][i] = 0.0f;
+            }
         }
     }
     const int64_t step = (int64_t)gridDim.x * TEAMS;
@@ -285,16 +293,31 @@ __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int6
             float h[8], d[8];
             widen8<FT>(cx[w], h);
             widen8<FT>(cy[w], d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            auto add = [&](int i, float& to_dw, float& to_db) {
                 const bool own = mine && i >= at[w].lo;
-                h[i] = (h[i] - mu) * r;
-                const float dd = own ? d[i] : 0.0f, hh = own ? h[i] : 0.0f;
+                const float dd = own ? d[i] : 0.0f, hh = own ? (h[i] - mu) * r : 0.0f;
                 const float g = dd * ww[w][i];
                 sg += g;
                 sgh = __builtin_fmaf(g, hh, sgh);
-                dw[w][i] = __builtin_fmaf(dd, hh, dw[w][i]);
-                db[w][i] += dd;
+                to_dw = __builtin_fmaf(dd, hh, to_dw);
+                to_db += dd;
+            };
+            if constexpr (IN_LDS) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float4* s = sums + (4 * w + k) * NT + t;
+                    float4 a = s[0], b = s[2 * NT];
+                    add(4 * k, a.x, b.x);
+                    add(4 * k + 1, a.y, b.y);
+                    add(4 * k + 2, a.z, b.z);
+                    add(4 * k + 3, a.w, b.w);
+                    s[0] = a;
+                    s[2 * NT] = b;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) add(i, dw[w][i], db[w][i]);
             }
         }
         sg = wave_sum(sg);
@@ -318,6 +341,11 @@ __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int6
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             float h[8], d[8];
+            if constexpr (IN_LDS) {      // nothing held from the first pass over the row
+                keep_raw<FT>(cx[w]);
+                keep_raw<FT>(cy[w]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             widen8<FT>(cx[w], h);
             widen8<FT>(cy[w], d);
 #pragma unroll
@@ -331,6 +359,19 @@ __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int6
     if (!part) return;
     // the teams' sums, added in team order, first those of dw, then of db
     float* to = part + (int64_t)blockIdx.x * 2 * ldp;
+    if constexpr (IN_LDS) {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            if (at[w].lo < 8) {
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const float4 a = sums[(4 * w + 2 * o) * NT + t], b = sums[(4 * w + 2 * o + 1) * NT + t];
+                    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    store8_own<F32>(to + o * ldp, 0, at[w], v);
+                }
+            }
+        return;
+    }
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
         if constexpr (TEAMS > 1) {
@@ -410,11 +451,12 @@ __global__ __launch_bounds__(256) void k_ln_bwd_cols(const void* __restrict__ dy
 
 // ------------------------------------------------------------- column sums
 // A workgroup takes 32 columns of one output: 8 lanes of four columns by 32
-// rows of partials at a time, four such loads under way per thread, then the
+// rows of partials at a time, U such loads under way per thread, then the
 // 32 row sums in order through LDS.
 __global__ __launch_bounds__(256) void k_colsum(const float* __restrict__ part, int64_t parts, int outs, int64_t ld,
                                                 int64_t cols, void* __restrict__ out0, void* __restrict__ out1, int dt)
 {
+    constexpr int U = 8;
     __shared__ float4 sums[32][8];
     const int o = blockIdx.y;
     void* out = o ? out1 : out0;
@@ -423,15 +465,15 @@ __global__ __launch_bounds__(256) void k_colsum(const float* __restrict__ part, 
     const int64_t col = (int64_t)blockIdx.x * 32 + 4 * c4;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (col < cols) {
-        for (int64_t p = rl; p < parts; p += 128) {
-            float4 a[4];
+        for (int64_t p = rl; p < parts; p += 32 * U) {
+            float4 a[U];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < U; ++k) {
                 const int64_t q = p + 32 * k < parts ? p + 32 * k : p;
                 a[k] = *reinterpret_cast<const float4*>(part + (q * outs + o) * ld + col);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < U; ++k)
                 if (p + 32 * k < parts) {
                     s.x += a[k].x;
                     s.y += a[k].y;
@@ -460,7 +502,7 @@ void colsum_launch(const float* part, int64_t parts, int outs, int64_t ld, int64
 
 // ---------------------------------------------------------------- launches
 constexpr int64_t LN_HELD = 16384;       // longest row that a workgroup holds in registers
-constexpr int64_t LN_BWD_HELD = 8192;    // and with the column sums beside it, in the backward pass
+constexpr int64_t LN_BWD_HELD = 16384;   // and that of dy beside it; half as many in binary32
 constexpr int64_t LN_PARTS = 256;        // workgroups of the backward pass, one row of partials each
 constexpr int64_t LN_COL_CHUNKS = 64;    // row chunks of the column kernel of long rows
 
@@ -506,7 +548,7 @@ static void ln_bwd_launch(const void* dy, int64_t lddy, const void* x, int64_t l
         hipLaunchKernelGGL((k_ln_bwd<FT, NT, W, BT>), dim3((unsigned)parts), dim3(BT), 0, st, dy, lddy, x, ldx,   \
                            rows, cols, w, wdt, mean, rstd, dx, part, ld);                                         \
     } while (0)
-    if (!ln_held(cols, LN_BWD_HELD)) {
+    if (!ln_held(cols, FT == F32 ? LN_BWD_HELD / 2 : LN_BWD_HELD)) {
         if (dx)
             hipLaunchKernelGGL((k_ln_bwd_loop<FT>), dim3((unsigned)rows), dim3(1024), 0, st, dy, lddy, x, ldx, cols, w,
                                wdt, mean, rstd, dx);
@@ -519,10 +561,11 @@ static void ln_bwd_launch(const void* dy, int64_t lddy, const void* x, int64_t l
         }
     }
     else if (cols <= 512) TQ_LNB(64, 1, 512);
-    else if (cols <= 1024) TQ_LNB(64, 2, 512);
-    else if (cols <= 2048) TQ_LNB(128, 2, 512);
+    else if (cols <= 1024) TQ_LNB(128, 1, 512);
+    else if (cols <= 2048) TQ_LNB(256, 1, 512);
     else if (cols <= 4096) TQ_LNB(256, 2, 512);
-    else TQ_LNB(512, 2, 512);
+    else if (cols <= 8192) TQ_LNB(512, 2, 512);
+    else if constexpr (FT != F32) TQ_LNB(1024, 2, 1024);
 #undef TQ_LNB
     if (part) colsum_launch(part, parts, 2, ld, cols, dw, db, wdt, st);
 }

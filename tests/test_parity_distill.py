@@ -66,9 +66,10 @@ def test_sizes(tq, rows, V, K, rest, ft):
 
 @pytest.mark.parametrize("V,ft", [(40003, "bf16"), (65536, "f16"), (70001, "bf16"), (98304, "bf16"), (131072, "bf16"),
                                   (131001, "f16"), (50001, "f32"), (65544, "f32"), (140000, "bf16")])
-def test_long_rows(tq, V, ft):
-    note("distill long", V, ft)
-    z, idx, val, tlse, dloss = draw(131, V, 40, V, ft)
+@pytest.mark.parametrize("rows", [131, 170])
+def test_long_rows(tq, rows, V, ft):
+    note("distill long", rows, V, ft)
+    z, idx, val, tlse, dloss = draw(rows, V, 40, V, ft)
     pick = [0, 1, 64, 129, 130]
     zd, id_, vd, td = z.cuda(), idx.cuda(), val.cuda(), tlse.cuda()
     loss, grad = tq.tq_topk_distill_grad(zd, id_, vd, dloss=dloss.cuda(), teacher_lse=td)
@@ -92,14 +93,15 @@ def test_temperature_types_and_padding(tq, T, rest):
         check(tq, z, idx, val.float().to(torch.float16), T, tlse if rest else None, None, "bf16")
 
 
-@pytest.mark.parametrize("rows", [8, 150])
+# held rows, and rows in parts
+@pytest.mark.parametrize("rows,V", [(8, 2000), (150, 2000), (8, 70001), (8, 140000)])
 @pytest.mark.parametrize("rest", [False, True])
-def test_masks_infinities_and_empty_rows(tq, rows, rest):
-    z, idx, val, tlse, dloss = draw(rows, 2000, 10, 3, "f32")
+def test_masks_infinities_and_empty_rows(tq, rows, V, rest):
+    z, idx, val, tlse, dloss = draw(rows, V, 10, 3, "f32")
     low = torch.finfo(torch.float32).min
     z[0, 500:] = -math.inf                              # banned tokens, some of them the teacher's
     idx[1] = -1                                         # no entries
-    idx[2, 3:] = 2000                                   # past the vocabulary: padding
+    idx[2, 3:] = V                                      # past the vocabulary: padding
     idx[2, 5] = 1 << 40                                 # far past it
     z[3] = -math.inf                                    # nothing can be drawn
     z[4, 100:] = low                                    # masked by the type's lowest value
@@ -117,9 +119,9 @@ def test_masks_infinities_and_empty_rows(tq, rows, rest):
         assert loss[7] == 0 and not grad[7].any() and not grad2[7].any()
 
 
-@pytest.mark.parametrize("rows", [4, 130])
-def test_nan_stays_in_its_row_and_empty_rows_ignore_it(tq, rows):
-    z, idx, val, tlse, dloss = draw(rows, 777, 6, 8, "f32")
+@pytest.mark.parametrize("rows,V", [(4, 777), (130, 777), (4, 70001)])
+def test_nan_stays_in_its_row_and_empty_rows_ignore_it(tq, rows, V):
+    z, idx, val, tlse, dloss = draw(rows, V, 6, 8, "f32")
     z[1, 5] = math.nan
     z[2, 9] = math.nan
     idx[2] = -1
@@ -132,10 +134,10 @@ def test_nan_stays_in_its_row_and_empty_rows_ignore_it(tq, rows):
     assert torch.isnan(loss[1]) and torch.isnan(grad[1]).all() and loss[2] == 0 and not grad[2].any()
 
 
-@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("rows,V", [(3, 300), (200, 300), (3, 70001)])
 @pytest.mark.parametrize("rest", [False, True])
-def test_repeated_columns_add_up(tq, rows, rest):
-    z, idx, val, tlse, dloss = draw(rows, 300, 9, 5, "f32")
+def test_repeated_columns_add_up(tq, rows, V, rest):
+    z, idx, val, tlse, dloss = draw(rows, V, 9, 5, "f32")
     idx[:, 4] = idx[:, 0]
     idx[:, 7] = idx[:, 0]
     idx[:, 8] = idx[:, 3]
