@@ -879,13 +879,13 @@ def tq_layer_norm(x, weight=None, bias=None, eps=1e-5):
 
 
 def tq_layer_norm_quant_per_token(x, weight=None, bias=None, eps=1e-5, stats=False):
-    """Layer norm and the symmetric per-token s8 quantizer in one pass: int8
-    codes of x's shape and one scale per row; with ``stats`` also mean and
-    rstd, for the backward pass."""
+    """Layer norm and the symmetric per-token s8 quantizer in one pass: codes
+    of x's shape (bytes, as tq_quant_per_token's) and one scale per row; with
+    ``stats`` also mean and rstd, for the backward pass."""
     xr, rows, cols, ld = _rows_of(x, "x")
     w, b, wdt = _params(x, cols, weight, bias)
     dev = x.device
-    q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    q = torch.empty(x.shape, dtype=torch.uint8, device=dev)
     scale = _f32(dev, rows)
     mean, rstd = (torch.empty_like(scale), torch.empty_like(scale)) if stats else (None, None)
     _call("tq_layer_norm_quant_per_token", xr.data_ptr(), FTYPE[x.dtype], rows, cols, ld, _ptr(w), _ptr(b), wdt, eps,

@@ -257,7 +257,9 @@ __device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, 
 // part's largest logit m, the sum of 2^((z - m) c) over all its columns and
 // over those that are no entries (only with REST), and the logits at its
 // entries, zk [rows, K] (for the loss, which may be taken after the gradient
-// has overwritten the logits).
+// has overwritten the logits).  A thread keeps its own running maximum and
+// sums, rescaled when a vector of eight exceeds it, so a part is one pass with
+// no barrier before the end.  Bound by HBM: [512, 32000] f32 12.9 us (5.1 TB/s).
 template <int FT, bool REST, int CH>
 __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ z, int64_t ldz, int V, int parts,
                                                        Entries ent, float c, float* __restrict__ part,
@@ -366,7 +368,8 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
 
 // k_distill_rows: a wave per row joins the row's parts and writes the loss and
 // the row's statistics: stats[row] = {largest logit, sum of exp(s (z - it))},
-// rest_sum[row] the same sum over the columns outside the entries.
+// rest_sum[row] the same sum over the columns outside the entries.  A launch's
+// latency (4.3 us), whatever the rows.
 __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entries ent, float s, float c,
                                                       const float* __restrict__ part, const float* __restrict__ zk,
                                                       int parts, float* __restrict__ loss, float* __restrict__ stats,
@@ -425,7 +428,10 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
 // k_distill_grad: a workgroup per row and part of the row.  Every workgroup
 // derives the row's coefficients itself, from the parts' statistics
 // (FROM_PARTS; the row's first workgroup writes the loss too) or from saved
-// ones, while its first vectors are under way.
+// ones, while its first vectors are under way: that costs a few hundred
+// operations per workgroup and saves a launch (9 rows of 131001 f16 loss and
+// gradient 15.8 us, 18.6 with one; 40 / 43 for [512, 32000] f32 forwards and
+// back).  Bound by HBM: [512, 32000] f32 23.4 us (5.6 TB/s).
 template <int FT, int CH, bool FROM_PARTS>
 __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz, int V, int parts, Entries ent,
                                                       float s, float c, const float* __restrict__ part,
@@ -566,9 +572,17 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
 //
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's
 // gradient is computed its registers take the next row's vector, so that the
-// reads go on under the gradient's arithmetic and stores.
+// reads go on under the gradient's arithmetic and stores.  Loads and stores are
+// non-temporal: a row is not met again.
+//
+// Bound by HBM and by how far reads and writes overlap with one row per CU:
+// [4096, 131072] bf16 482 us (4.45 TB/s; a large copy reaches 5.0, and the same
+// kernel without its stores takes 406).  Two passes with the parts' kernels
+// take 640, a workgroup per row without the next row's loads 516, temporal
+// stores 506 and temporal loads 496.
 template <int FT, int NT, int W>
-__global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz, uint32_t rows, int V, Entries ent, float s, float c,
+__global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz, uint32_t rows, int V, Entries ent,
+                                                     float s, float c,
                                                      const float* __restrict__ dloss, float* __restrict__ loss,
                                                      void* dz, int64_t lddz)
 {
@@ -589,191 +603,194 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
     }
     const uint32_t step = gridDim.x;
     for (uint32_t r = blockIdx.x; r < rows; r += step) {
-    // opaque, so that nothing computed from them is kept in registers over the rows
-    const int64_t row = afresh_uniform((int)r);
-    const int t = afresh((int)threadIdx.x), wave = t >> 6;
-    char* to = static_cast<char*>(dz) + row * lddz * ES;
-    from = static_cast<const char*>(z) + row * ldz * ES;
-    const bool more = r + step < rows;
-    const char* next = from + (more ? step * ldz * ES : 0);
-    // vector w of the next row (after the last row, one address of this one again)
-    auto ahead = [&](int w) {
-        const int at = afresh(afresh(t) + w * NT);
-        raw[w] = load8_off<FT, true>(next, more ? (uint32_t)(at < nvec ? at : nvec - 1) * (8 * ES) : 0u);
-    };
-    const float tail = t < ntail ? load1<FT>(from, 8 * nvec + t) : -__builtin_inff();
-    __syncthreads();                     // the row before is done with the marks
-    if (t < 8) tails[t] = tail;          // read by the same threads
-    if (t == 0) any = 0;
-    marks_clear(k);
-    load_entries<NT>(list, ent, row, V);
-    __syncthreads();
-    float tm = -__builtin_inff();
+        // opaque, so that nothing computed from them is kept in registers over the rows
+        const int64_t row = afresh_uniform((int)r);
+        const int t = afresh((int)threadIdx.x), wave = t >> 6;
+        char* to = static_cast<char*>(dz) + row * lddz * ES;
+        from = static_cast<const char*>(z) + row * ldz * ES;
+        const bool more = r + step < rows;
+        const char* next = from + (more ? step * ldz * ES : 0);
+        // vector w of the next row (after the last row, one address of this one again)
+        auto ahead = [&](int w) {
+            const int at = afresh(afresh(t) + w * NT);
+            raw[w] = load8_off<FT, true>(next, more ? (uint32_t)(at < nvec ? at : nvec - 1) * (8 * ES) : 0u);
+        };
+        const float tail = t < ntail ? load1<FT>(from, 8 * nvec + t) : -__builtin_inff();
+        __syncthreads();                     // the row before is done with the marks
+        if (t < 8) tails[t] = tail;          // read by the same threads
+        if (t == 0) any = 0;
+        marks_clear(k);
+        load_entries<NT>(list, ent, row, V);
+        __syncthreads();
+        float tm = -__builtin_inff();
 #pragma unroll 1
-    for (int i = t; i < ent.K; i += NT) {
-        const int col = list.col[i];
-        if (col >= 0) {
-            any = 1;
-            mark(k, col);
-            tm = __builtin_fmaxf(tm, list.val[i]);
+        for (int i = t; i < ent.K; i += NT) {
+            const int col = list.col[i];
+            if (col >= 0) {
+                any = 1;
+                mark(k, col);
+                tm = __builtin_fmaxf(tm, list.val[i]);
+            }
         }
-    }
-    tm = wave_max(tm);
-    if ((t & 63) == 0) red[0][wave] = tm;
-    __syncthreads();
-    bool some = any != 0;
-    marks_count(k);
-    // one value per wave, joined across the lanes
-    const int lane = t & 63;
-    auto top = [&](int i) { return wave_max(lane < NW ? red[i][lane] : -__builtin_inff()); };
-    auto total = [&](int i) { return wave_sum(lane < NW ? red[i][lane] : 0.0f); };
-    tm = top(0);
-    tm = rest ? ent.tlse[row] : base_of(tm);
-    float tsum = 0.0f;
+        tm = wave_max(tm);
+        if ((t & 63) == 0) red[0][wave] = tm;
+        __syncthreads();
+        bool some = any != 0;
+        marks_count(k);
+        // one value per wave, joined across the lanes
+        const int lane = t & 63;
+        auto top = [&](int i) { return wave_max(lane < NW ? red[i][lane] : -__builtin_inff()); };
+        auto total = [&](int i) { return wave_sum(lane < NW ? red[i][lane] : 0.0f); };
+        tm = top(0);
+        tm = rest ? ent.tlse[row] : base_of(tm);
+        float tsum = 0.0f;
 #pragma unroll 1
-    for (int i = t; i < ent.K; i += NT)
-        if (list.col[i] >= 0) {
-            const float x = list.val[i];
-            tsum += rest ? ex2((x * s - tm) * LOG2E) : ex2((x - tm) * c);
-        }
+        for (int i = t; i < ent.K; i += NT)
+            if (list.col[i] >= 0) {
+                const float x = list.val[i];
+                tsum += rest ? ex2((x * s - tm) * LOG2E) : ex2((x - tm) * c);
+            }
 
-    float m, S, R;
-    // the sums over this thread's vectors of x(z) and, in R, of those off the entries
-    auto sum = [&](auto x) {
-        S = t < ntail ? x(tails[t]) : 0.0f;
-        R = rest && t < ntail && !(marks8(k, 8 * nvec) >> t & 1) ? S : 0.0f;
+        float m, S, R;
+        // the sums over this thread's vectors of x(z) and, in R, of those off the entries
+        auto sum = [&](auto x) {
+            S = t < ntail ? x(tails[t]) : 0.0f;
+            R = rest && t < ntail && !(marks8(k, 8 * nvec) >> t & 1) ? S : 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const int at = afresh(afresh(t) + w * NT);
+                float v[8], part = 0.0f;
+                keep_raw<FT>(raw[w]);
+                widen8<FT>(raw[w], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = x(v[i]);
+                    part += v[i];
+                }
+                const bool here = at < nvec;
+                S += here ? part : 0.0f;
+                if (rest) {
+                    const uint32_t mask = here ? marks8(k, 8 * at) : 0;
+                    if (mask) {
+                        part = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) part += mask >> i & 1 ? 0.0f : v[i];
+                    }
+                    R += here ? part : 0.0f;
+                }
+                __builtin_amdgcn_sched_barrier(0);   // one vector at a time, in the order they arrive
+            }
+        };
+        {
+            float v[8];
+            widen8<FT>(raw[0], v);
+            m = v[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+            m = base_of(wave_max(m));
+            const float mc = m * c;
+            sum([&](float v) { return ex2(__builtin_fmaf(v, c, -mc)); });
+        }
+        S = wave_sum(S);
+        R = wave_sum(R);
+        tsum = wave_sum(tsum);
+        if ((t & 63) == 0) {
+            red[1][wave] = m;
+            red[2][wave] = S;
+            red[3][wave] = R;
+            red[4][wave] = tsum;
+        }
+        __syncthreads();
+        m = top(1);
+        const float f = lane < NW ? ex2((red[1][lane] - m) * c) : 0.0f;
+        S = wave_sum(lane < NW ? red[2][lane] * f : 0.0f);
+        R = wave_sum(lane < NW ? red[3][lane] * f : 0.0f);
+        tsum = total(4);
+        const bool near = S >= 0x1p-60f && S < 0x1p100f;
+        if (!near) {                         // uniform: around the row's own maximum
+            m = t < ntail ? tails[t] : -__builtin_inff();
+#pragma unroll
+            for (int w = 0; w < W; ++w) {    // repeated elements do not change a maximum
+                float v[8];
+                keep_raw<FT>(raw[w]);
+                widen8<FT>(raw[w], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+            }
+            m = wave_max(m);
+            __syncthreads();
+            if ((t & 63) == 0) red[1][wave] = m;
+            __syncthreads();
+            m = top(1);
+            const float b = base_of(m);
+            sum([&](float v) { return ex2((v - b) * c); });
+            S = wave_sum(S);
+            R = wave_sum(R);
+            __syncthreads();
+            if ((t & 63) == 0) {
+                red[2][wave] = S;
+                red[3][wave] = R;
+            }
+            __syncthreads();
+            S = total(2);
+            R = total(3);
+        }
+        if (!rest && tsum == 0.0f) some = false;
+        float pr;
+        const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+        if (q.some) marks_fill(k, list, ent, q, 0, V, s, c);
+        float l = 0.0f;
+#pragma unroll 1
+        for (int i = t; i < (q.some ? ent.K : 0); i += NT) {
+            const int col = list.col[i];
+            if (col >= 0) l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S);
+        }
+        l = wave_sum(l);
+        if ((t & 63) == 0) red[5][wave] = l;
+        __syncthreads();                     // also before the first store: dz may be z
+        if (wave == 0) {
+            l = total(5) + rest_loss(pr, R, S);
+            if (t == 0) loss[row] = q.some ? l : 0.0f;
+        }
+        // 2^(z c - m c) or 2^((z - m) c)
+        const float sub = near ? 0.0f : q.m, mc = near ? q.m * c : 0.0f;
+        auto x = [&](float v) { return ex2(__builtin_fmaf(v - sub, c, -mc)); };
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const int at = afresh(afresh(t) + w * NT);
-            float v[8], part = 0.0f;
-            keep_raw<FT>(raw[w]);
-            widen8<FT>(raw[w], v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = x(v[i]);
-                part += v[i];
-            }
-            const bool here = at < nvec;
-            S += here ? part : 0.0f;
-            if (rest) {
-                const uint32_t mask = here ? marks8(k, 8 * at) : 0;
-                if (mask) {
-                    part = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) part += mask >> i & 1 ? 0.0f : v[i];
-                }
-                R += here ? part : 0.0f;
-            }
-            __builtin_amdgcn_sched_barrier(0);   // one vector at a time, in the order they arrive
-        }
-    };
-    {
-        float v[8];
-        widen8<FT>(raw[0], v);
-        m = v[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
-        m = base_of(wave_max(m));
-        const float mc = m * c;
-        sum([&](float v) { return ex2(__builtin_fmaf(v, c, -mc)); });
-    }
-    S = wave_sum(S);
-    R = wave_sum(R);
-    tsum = wave_sum(tsum);
-    if ((t & 63) == 0) {
-        red[1][wave] = m;
-        red[2][wave] = S;
-        red[3][wave] = R;
-        red[4][wave] = tsum;
-    }
-    __syncthreads();
-    m = top(1);
-    const float f = lane < NW ? ex2((red[1][lane] - m) * c) : 0.0f;
-    S = wave_sum(lane < NW ? red[2][lane] * f : 0.0f);
-    R = wave_sum(lane < NW ? red[3][lane] * f : 0.0f);
-    tsum = total(4);
-    const bool near = S >= 0x1p-60f && S < 0x1p100f;
-    if (!near) {                         // uniform: around the row's own maximum
-        m = t < ntail ? tails[t] : -__builtin_inff();
-#pragma unroll
-        for (int w = 0; w < W; ++w) {    // repeated elements do not change a maximum
             float v[8];
             keep_raw<FT>(raw[w]);
             widen8<FT>(raw[w], v);
+            // the old vector's registers are free before the new one's load is issued: it goes into the same ones,
+            // and no copy at the loop's end waits for it
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+            for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(v[i]));
+            __builtin_amdgcn_sched_barrier(0);
+            ahead(w);
+            if (at < nvec) {
+                if (q.some) grad8(k, q, 8 * at, v, x);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+                store8_off<FT, true>(to, (uint32_t)at * (8 * ES), v);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        m = wave_max(m);
-        __syncthreads();
-        if ((t & 63) == 0) red[1][wave] = m;
-        __syncthreads();
-        m = top(1);
-        const float b = base_of(m);
-        sum([&](float v) { return ex2((v - b) * c); });
-        S = wave_sum(S);
-        R = wave_sum(R);
-        __syncthreads();
-        if ((t & 63) == 0) {
-            red[2][wave] = S;
-            red[3][wave] = R;
+        if (t < ntail) {
+            const int at = 8 * nvec + t;
+            const float e = x(tails[t]);
+            const bool entry = marks8(k, 8 * nvec) >> t & 1;
+            store1<FT>(to, at, !q.some ? 0.0f : entry ? e * q.in - k.value[rank_of(k, at)] : e * q.out);
         }
-        __syncthreads();
-        S = total(2);
-        R = total(3);
-    }
-    if (!rest && tsum == 0.0f) some = false;
-    float pr;
-    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
-    if (q.some) marks_fill(k, list, ent, q, 0, V, s, c);
-    float l = 0.0f;
-#pragma unroll 1
-    for (int i = t; i < (q.some ? ent.K : 0); i += NT) {
-        const int col = list.col[i];
-        if (col >= 0) l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S);
-    }
-    l = wave_sum(l);
-    if ((t & 63) == 0) red[5][wave] = l;
-    __syncthreads();                     // also before the first store: dz may be z
-    if (wave == 0) {
-        l = total(5) + rest_loss(pr, R, S);
-        if (t == 0) loss[row] = q.some ? l : 0.0f;
-    }
-    // 2^(z c - m c) or 2^((z - m) c)
-    const float sub = near ? 0.0f : q.m, mc = near ? q.m * c : 0.0f;
-    auto x = [&](float v) { return ex2(__builtin_fmaf(v - sub, c, -mc)); };
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const int at = afresh(afresh(t) + w * NT);
-        float v[8];
-        keep_raw<FT>(raw[w]);
-        widen8<FT>(raw[w], v);
-        // the old vector's registers are free before the new one's load is issued: it goes into the same ones, and no
-        // copy at the loop's end waits for it
-#pragma unroll
-        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(v[i]));
-        __builtin_amdgcn_sched_barrier(0);
-        ahead(w);
-        if (at < nvec) {
-            if (q.some) grad8(k, q, 8 * at, v, x);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-            store8_off<FT, 1>(to, (uint32_t)at * (8 * ES), v);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    if (t < ntail) {
-        const int at = 8 * nvec + t;
-        const float e = x(tails[t]);
-        const bool entry = marks8(k, 8 * nvec) >> t & 1;
-        store1<FT>(to, at, !q.some ? 0.0f : entry ? e * q.in - k.value[rank_of(k, at)] : e * q.out);
-    }
     }
 }
 
 // ---------------------------------------------------------------- launches
 // Columns per part: the longest of 32768, 16384, 8192 and 4096 that still
-// gives the chip DT_GROUPS workgroups.
+// gives the chip DT_GROUPS workgroups.  Measured, forwards and back, us, at 512
+// / 2048 / 8192 workgroups: [512, 32000] f32 41.5 / 38.6 / 44.3, [128, 131072]
+// bf16 28.8 / 25.6 / 30.7, [2048, 32000] bf16 94 / 94 / 86, [2048, 131072] bf16
+// 324 / 324 / 324.
 constexpr int64_t DT_GROUPS = 2048;
 constexpr int DT_CH[] = {32768, 16384, 8192, 4096};
 inline int distill_ch(int64_t rows, int64_t V)
@@ -800,7 +817,10 @@ struct Distill {
 };
 
 // Workspace: the parts' statistics, then the logits at the entries.
-inline size_t distill_part_floats(int64_t rows, int64_t V) { return 3 * (size_t)rows * (size_t)cdiv(V, distill_ch(rows, V)); }
+inline size_t distill_part_floats(int64_t rows, int64_t V)
+{
+    return 3 * (size_t)rows * (size_t)cdiv(V, distill_ch(rows, V));
+}
 
 template <int FT>
 static void stats_launch(const Distill& d, float* ws, hipStream_t st)
@@ -848,7 +868,8 @@ static bool held_launch(const Distill& d, const float* dloss, float* loss, void*
 {
     constexpr int H = FT == F32 ? 2 : 1;  // binary32 rows hold half as many elements
     if (d.V < 8 || d.V > 131072 / H) return false;
-    if (d.V > 65536 / H ? 8 * d.rows < 5 * 256 * cdiv(d.rows, 256) : d.V > 32768 / H && d.rows < DT_HELD_ROWS) return false;
+    if (d.V > 65536 / H ? 8 * d.rows < 5 * 256 * cdiv(d.rows, 256) : d.V > 32768 / H && d.rows < DT_HELD_ROWS)
+        return false;
     // as many workgroups as fit on the chip by their registers
 #define TQ_HELD(NT, W)                                                                                            \
     hipLaunchKernelGGL((k_distill_held<FT, NT, W>), dim3((unsigned)std::min<int64_t>(d.rows, 256 * (1024 / NT) * \

@@ -89,7 +89,8 @@ __device__ __forceinline__ void slope8(int act, const float z[8], float d[8])
         for (int i = 0; i < 8; ++i) {
             constexpr float A = -2.0f * LOG2E * GELU_C;
             const float zz = z[i] * z[i];
-            const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[i] * __builtin_fmaf(zz, A * GELU_A, A)));
+            const float x = z[i] * __builtin_fmaf(zz, A * GELU_A, A);
+            const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
             const float pq = __builtin_fmaf(-p, p, p);
             const float u = z[i] * __builtin_fmaf(zz, 6.0f * GELU_C * GELU_A, 2.0f * GELU_C);
             d[i] *= __builtin_fmaf(pq == 0.0f ? 0.0f : u, pq, p);
@@ -217,7 +218,12 @@ __device__ __forceinline__ v4i codes16(const int8_t* row, int64_t k, int64_t K)
 // lines; the sums meet in LDS, one thread per output.  The weights are the
 // matrix core's first operand (16 columns), the tokens its second (16 tokens,
 // rows past M repeat row M - 1), U blocks of both in flight per wave.  What an
-// output's epilogue needs is loaded before the weights are.
+// output's epilogue needs is loaded before the weights are.  Kernel times: 1 x
+// 11008 x 4096 10.2 us (4.4 TB/s of weights), 16 x 4096 x 11008 12.2 (3.7): with
+// 256 workgroups each CU has one slice of 16 columns, whose first loads and
+// last sums nothing covers.
+// Refilling each of the U slots as it is used instead of all at once: 13.3 ->
+// 12.2 us.
 template <int YT, int MT, int NWV, int U>
 __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
                                                       int64_t K, Epi e)
@@ -353,7 +359,8 @@ __device__ __forceinline__ void stage_half(int h, const v4i (&acc)[NM][NN], int*
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < NN; ++j)
-            *reinterpret_cast<v4i*>(&stage[(16 * i + l16) * Stage<NM, NN>::PITCH + 16 * j + 4 * g4]) = acc[2 * h + i][j];
+            *reinterpret_cast<v4i*>(&stage[(16 * i + l16) * Stage<NM, NN>::PITCH + 16 * j + 4 * g4]) =
+                acc[2 * h + i][j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
@@ -407,7 +414,7 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[k][i] += w[i];
                 }
-                store8_off<YT, NTS ? 1 : 0>(y, yo + k * S::RPI * ystep, v[k]);
+                store8_off<YT, NTS>(y, yo + k * S::RPI * ystep, v[k]);
             }
             yo += 2 * S::RPI * ystep;
             ro += 2 * S::RPI * rstep;
@@ -485,7 +492,15 @@ __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0
 // waves of 128 x 128 read a third less but leave each SIMD one wave, whose
 // loads (about 58 clocks of issue each) then stop its products: 326 / 346 us.
 // Of the 333 us about 45 are the epilogue, which one workgroup per CU cannot
-// lay under the products of another.
+// lay under the products of another.  The 256 x 256 tile's stores are
+// non-temporal (an output of 180 MB passes every cache): 10 us less; smaller
+// products keep plain stores, since what follows reads them.
+//
+// 128 x 128, one workgroup per CU and 9 units: 777 x 4096 x 4096 f16 with bias,
+// gelu and residual 20.3 us; 64 x 64, two per CU: 128 x 4096 x 4096 11.1 us.
+// There a block of 128 codes takes a fixed 0.48 and 0.3 us of waits for the
+// barrier, LDS and the slices in turn; longer rings change nothing, and neither
+// does sharing a block's two steps between two sets of waves (23.2 and 10.5 us).
 //
 // Where K is no multiple of 128, the block that the rest makes comes first
 // (integer sums have no order): its missing chunks come from sixteen zero
@@ -520,8 +535,8 @@ __device__ __forceinline__ void lds_load_at(const void* g, uint32_t lds)
 }
 #pragma clang diagnostic pop
 
-// c += w x, 16 x 16 x 64 codes.  The sums of one tile are next touched NT^2
-// products later, far behind the matrix core's own latency.
+// c += w x, 16 x 16 x 64 codes.  The sums of one tile are next added to after
+// every other tile of the wave, three products later or more.
 __device__ __forceinline__ void add_product(v4i& c, v4i w, v4i x)
 {
     asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(w), "v"(x));
@@ -611,9 +626,11 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_tile(co
         for (int s = 0; s < 2; ++s) {
             v4i av[NM], bv[NN];
 #pragma unroll
-            for (int i = 0; i < NM; ++i) av[i] = *reinterpret_cast<const v4i*>(&la[eslot(wm * QM + i * 16 + l16, 4 * s + g4)]);
+            for (int i = 0; i < NM; ++i)
+                av[i] = *reinterpret_cast<const v4i*>(&la[eslot(wm * QM + i * 16 + l16, 4 * s + g4)]);
 #pragma unroll
-            for (int j = 0; j < NN; ++j) bv[j] = *reinterpret_cast<const v4i*>(&lb[eslot(wn * QN + j * 16 + l16, 4 * s + g4)]);
+            for (int j = 0; j < NN; ++j)
+                bv[j] = *reinterpret_cast<const v4i*>(&lb[eslot(wn * QN + j * 16 + l16, 4 * s + g4)]);
 #pragma unroll
             for (int i = 0; i < NM; ++i)
 #pragma unroll
@@ -652,8 +669,9 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_tile(co
 }
 
 template <int YT, int TILE, int RING, int WM, int WN, int WGS>
-__global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
-                                                     int64_t K, int64_t nt, int64_t mt, int slab, Epi e)
+__global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(const int8_t* __restrict__ qx,
+                                                                              const int8_t* __restrict__ qw, int64_t K,
+                                                                              int64_t nt, int64_t mt, int slab, Epi e)
 {
     constexpr int UNIT = TILE * ET;      // bytes of a unit
     constexpr int WAVES = WM * WN;
@@ -661,7 +679,8 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
     constexpr int QM = TILE / WM, QN = TILE / WN;  // rows and columns of a wave's part
     constexpr int NM = QM / 16, NN = QN / 16;      // 16-wide tiles along its sides
     constexpr int AHEAD = (RING - 4) * U;          // loads that may be in flight behind the next block's
-    constexpr int GROUPS = NM * NN >= 32 ? 16 : NM * NN >= 8 ? 8 : 4, PER = NM * NN / GROUPS;   // products go in groups, loads between them
+    constexpr int GROUPS = NM * NN >= 32 ? 16 : NM * NN >= 8 ? 8 : 4;   // products go in groups, loads between them
+    constexpr int PER = NM * NN / GROUPS;
     static_assert(NM + NN <= 2 * GROUPS && 2 * U <= GROUPS && RING % 2 == 1 && TILE % (8 * WAVES) == 0, "schedule");
     static_assert(4 * WAVES * Stage<NM, NN>::INTS <= RING * UNIT, "staging");
     __shared__ __attribute__((aligned(16))) uint8_t ring[RING * UNIT];
@@ -726,7 +745,8 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
     };
     auto products = [&](int set, int g) {
 #pragma unroll
-        for (int x = PER * g; x < PER * (g + 1); ++x) add_product(acc[x / NN][x % NN], bv[set][x % NN], av[set][x / NN]);
+        for (int x = PER * g; x < PER * (g + 1); ++x)
+            add_product(acc[x / NN][x % NN], bv[set][x % NN], av[set][x / NN]);
         __builtin_amdgcn_sched_barrier(0);
     };
 
@@ -790,7 +810,8 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
 
 // ------------------------------------------------------ backward of epilogue
 // k_epi_bwd: dz = dy act'(z) and its column sums: 4 bytes read and 2 written
-// per bf16 element, bound by HBM.  A wave owns 512 columns, a workgroup's four
+// per bf16 element, bound by HBM: [8192, 11008] bf16 with gelu's slope 101.7 us
+// (5.3 TB/s) and 4.9 us for the column sums.  A wave owns 512 columns, a workgroup's four
 // waves take a chunk of the rows in turn, U rows in flight each; their column
 // sums meet in LDS in wave order and leave as one row of partials per chunk.
 template <int FT>
@@ -1010,7 +1031,8 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
     const dim3 grid((unsigned)cdiv(N, 512), (unsigned)chunks);
     TQ_LLM_FT_SWITCH(dtype, {
         if (N < 8)
-            hipLaunchKernelGGL((k_epi_bwd_thin<FTV>), grid, dim3(256), 0, st, dy, preact, M, N, chunk, act, dz, part, ld);
+            hipLaunchKernelGGL((k_epi_bwd_thin<FTV>), grid, dim3(256), 0, st, dy, preact, M, N, chunk, act, dz, part,
+                               ld);
         else
             hipLaunchKernelGGL((k_epi_bwd<FTV>), grid, dim3(256), 0, st, dy, preact, M, N, chunk, act, dz, part, ld);
     });

@@ -1,7 +1,7 @@
 // tq_llm.h -- device helpers of the operators around a quantized layer
 // (layer norm, the W8A8 product's epilogue, distillation): lane sums, vectors
-// of eight elements at any element alignment, the activations and their
-// slopes, and the column sums that finish a weight's or a bias's gradient.
+// of eight elements at any element alignment, parameters whose type is known
+// at run time, and the column sums that finish a weight's or a bias's gradient.
 #pragma once
 
 #include "tq_device.h"
@@ -59,14 +59,11 @@ __device__ __forceinline__ uint4 ld16_any(const void* p)
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
-// Stores as st16: NT = 0 plain, 1 non-temporal, 2 (WT) non-temporal with
-// device scope.
-template <int NT = 0>
+template <bool NT = false>
 __device__ __forceinline__ void st16_any(void* p, uint4 w)
 {
     const u32x4_any v = {w.x, w.y, w.z, w.w};
-    if constexpr (NT == WT) st16<WT>(p, w);
-    else if constexpr (NT) __builtin_nontemporal_store(v, static_cast<u32x4_any*>(p));
+    if constexpr (NT) __builtin_nontemporal_store(v, static_cast<u32x4_any*>(p));
     else *static_cast<u32x4_any*>(p) = v;
 }
 
@@ -84,7 +81,7 @@ __device__ __forceinline__ Raw8<FT> load8_any(const void* base, int64_t e)
     return r;
 }
 
-template <int FT, int NT = 0>
+template <int FT, bool NT = false>
 __device__ __forceinline__ void store8_any(void* base, int64_t e, const float v[8])
 {
     if constexpr (FT == F32) {
@@ -109,7 +106,7 @@ __device__ __forceinline__ Raw8<FT> load8_off(const void* row, uint32_t off)
     if constexpr (FT == F32) r.w[1] = ld16_any<NT>(p + 16);
     return r;
 }
-template <int FT, int NT = 0>
+template <int FT, bool NT = false>
 __device__ __forceinline__ void store8_off(void* row, uint32_t off, const float v[8])
 {
     store8_any<FT, NT>(static_cast<char*>(row) + off, 0, v);
@@ -158,7 +155,7 @@ __device__ __forceinline__ Vec8 vec8(int v, int n)
 }
 
 // Stores the vector's own elements.
-template <int FT, int NT = 0>
+template <int FT, bool NT = false>
 __device__ __forceinline__ void store8_own(void* base, int64_t row, Vec8 q, const float v[8])
 {
     if (q.lo == 0) {
@@ -167,19 +164,6 @@ __device__ __forceinline__ void store8_own(void* base, int64_t row, Vec8 q, cons
 #pragma unroll
         for (int i = 1; i < 8; ++i)
             if (i >= q.lo) store1<FT>(base, row + q.at + i, v[i]);
-    }
-}
-
-template <int FT, int NT = 0>
-__device__ __forceinline__ void store8_own_off(void* row, Vec8 q, const float v[8])
-{
-    const uint32_t off = (uint32_t)q.at * (FT == F32 ? 4 : 2);
-    if (q.lo == 0) {
-        store8_off<FT, NT>(row, off, v);
-    } else {
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            if (i >= q.lo) store1<FT>(static_cast<char*>(row) + off, i, v[i]);
     }
 }
 
