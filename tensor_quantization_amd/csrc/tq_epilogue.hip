@@ -484,7 +484,7 @@ __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0
 // still be on their way: the wait counts loads, it does not drain them).
 //
 // 256 x 256 with 2 x 4 waves of 128 x 64: on [8192, 4096] x [11008, 4096] 314
-// us without and 333 us with bias and gelu (2350 / 2220 TOP/s; the platform
+// us without and 333 us with bias and gelu_tanh (2350 / 2220 TOP/s; the platform
 // library's plain int8 product of that size 400 us, its best size 2336 TOP/s),
 // 2560 TOP/s at 8192^3.  Bound by the matrix cores at the clock that the chip
 // holds under them, and by LDS: per block 192 KB of operand reads and 64 KB of
@@ -497,7 +497,7 @@ __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0
 // products keep plain stores, since what follows reads them.
 //
 // 128 x 128, one workgroup per CU and 9 units: 777 x 4096 x 4096 f16 with bias,
-// gelu and residual 20.3 us; 64 x 64, two per CU: 128 x 4096 x 4096 11.1 us.
+// silu and residual 20.3 us; 64 x 64, two per CU: 128 x 4096 x 4096 11.1 us.
 // There a block of 128 codes takes a fixed 0.48 and 0.3 us of waits for the
 // barrier, LDS and the slices in turn; longer rings change nothing, and neither
 // does sharing a block's two steps between two sets of waves (23.2 and 10.5 us).
@@ -810,7 +810,7 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
 
 // ------------------------------------------------------ backward of epilogue
 // k_epi_bwd: dz = dy act'(z) and its column sums: 4 bytes read and 2 written
-// per bf16 element, bound by HBM: [8192, 11008] bf16 with gelu's slope 101.7 us
+// per bf16 element, bound by HBM: [8192, 11008] bf16 with gelu_tanh 101.7 us
 // (5.3 TB/s) and 4.9 us for the column sums.  A wave owns 512 columns, a workgroup's four
 // waves take a chunk of the rows in turn, U rows in flight each; their column
 // sums meet in LDS in wave order and leave as one row of partials per chunk.
