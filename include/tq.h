@@ -622,7 +622,8 @@ tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_
  * dtype) and dbias[n] = sum_m of the dz before its rounding (binary32 [N], may
  * be NULL; zeros when M is 0).  The residual's gradient is dy.  dz may be dy or
  * preact itself.  relu's slope at 0 is 0.  `workspace` (needed for dbias):
- * tq_linear_epilogue_backward_workspace_bytes(M, N) bytes, 16-byte aligned. */
+ * tq_linear_epilogue_backward_workspace_bytes(M, N) bytes, 16-byte aligned (0
+ * bytes, and null, for few rows). */
 size_t tq_linear_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
 tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dtype, int64_t M, int64_t N, int act,
                                       void* dz, float* dbias, void* workspace, size_t workspace_bytes, void* stream);

@@ -908,8 +908,11 @@ __global__ __launch_bounds__(256) void k_epi_bwd_thin(const void* __restrict__ d
 // rows, in about EPI_GROUPS workgroups over the slabs of 512 columns (measured on
 // [8192, 11008] bf16: 1400 workgroups 115 us, 4096 109, 8192 106).
 constexpr int64_t EPI_GROUPS = 8192;
+// Up to EPI_ONE rows are one chunk, whose sums are dbias itself: one launch.
+constexpr int64_t EPI_ONE = 64;
 inline int64_t epi_chunk(int64_t M, int64_t N)
 {
+    if (M <= EPI_ONE) return EPI_ONE;
     const int64_t chunks = std::max<int64_t>(1, EPI_GROUPS / cdiv(N, 512));
     return cdiv(cdiv(M, chunks), 16) * 16;
 }
@@ -1004,7 +1007,7 @@ tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_
 
 size_t tq_linear_epilogue_backward_workspace_bytes(int64_t M, int64_t N)
 {
-    if (M <= 0 || N <= 0) return 0;
+    if (M <= EPI_ONE || N <= 0) return 0;
     return (size_t)cdiv(M, epi_chunk(M, N)) * (size_t)colsum_ld(N) * sizeof(float);
 }
 
@@ -1022,12 +1025,12 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
     if (!dy || !preact || !dz) return TQ_ERR_INVALID;
     if (!natural(dy, dtype) || !natural(preact, dtype) || !natural(dz, dtype)) return TQ_ERR_ALIGN;
     if (cdiv(N, 512) > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
-    if (dbias) {
+    if (dbias && M > EPI_ONE) {
         if (!workspace || workspace_bytes < tq_linear_epilogue_backward_workspace_bytes(M, N)) return TQ_ERR_INVALID;
         if (!aligned16(workspace)) return TQ_ERR_ALIGN;
     }
-    float* part = dbias ? static_cast<float*>(workspace) : nullptr;
     const int64_t chunk = epi_chunk(M, N), chunks = cdiv(M, chunk), ld = colsum_ld(N);
+    float* part = dbias && chunks > 1 ? static_cast<float*>(workspace) : dbias;
     const dim3 grid((unsigned)cdiv(N, 512), (unsigned)chunks);
     TQ_LLM_FT_SWITCH(dtype, {
         if (N < 8)
@@ -1036,7 +1039,7 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
         else
             hipLaunchKernelGGL((k_epi_bwd<FTV>), grid, dim3(256), 0, st, dy, preact, M, N, chunk, act, dz, part, ld);
     });
-    if (dbias) colsum_launch(part, chunks, 1, ld, N, dbias, nullptr, TQ_F32, st);
+    if (dbias && chunks > 1) colsum_launch(part, chunks, 1, ld, N, dbias, nullptr, TQ_F32, st);
     return launch_status();
 }
 
