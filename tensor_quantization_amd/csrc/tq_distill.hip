@@ -458,13 +458,28 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     };
     if (n >= 8) fetch(t);
 
+    // everything from memory is asked for ahead of the first barrier
     if (t == 0) any = 0;
     marks_clear(k);
     load_entries<256>(list, ent, row, V);
-    float m = -__builtin_inff();
-    const float* of = part + row * parts * 3;
-    if constexpr (FROM_PARTS)
-        for (int i = t; i < parts; i += 256) m = __builtin_fmaxf(m, of[3 * i]);
+    const float lse = rest ? ent.tlse[row] : 0.0f, g = dloss ? dloss[row] : 1.0f;
+    float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
+    if constexpr (FROM_PARTS) {
+        const float* of = part + row * parts * 3;
+        for (int i = t; i < parts; i += 256) {   // this thread's parts, relative to their largest logit
+            const float pm = of[3 * i], ps = of[3 * i + 1], pr = of[3 * i + 2];
+            const float top = __builtin_fmaxf(m, pm), b = base_of(top);
+            const float f = ex2((m - b) * c), pf = ex2((pm - b) * c);
+            S = S * f + ps * pf;
+            R = R * f + pr * pf;
+            m = top;
+        }
+    } else {
+        m = stats[2 * row];
+        S = stats[2 * row + 1];
+        R = rest ? rest_sum[row] : 0.0f;
+    }
+    const float zk0 = FROM_PARTS && p == 0 && t < ent.K ? zk[row * ent.K + t] : 0.0f;
     __syncthreads();
     float tm = -__builtin_inff();
     for (int i = t; i < ent.K; i += 256) {
@@ -476,28 +491,24 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     }
     auto four = [&](int i) { return lane < 4 ? red[i][lane] : 0.0f; };
     tm = wave_max(tm);
-    m = wave_max(m);
+    const float mt = m;
+    if constexpr (FROM_PARTS) m = wave_max(m);
     if (lane == 0) {
         red[0][wave] = tm;
         red[1][wave] = m;
     }
     __syncthreads();
-    tm = rest ? ent.tlse[row] : base_of(wave_max(lane < 4 ? red[0][lane] : -__builtin_inff()));
-    float S = 0.0f, R = 0.0f, tsum = 0.0f;
+    tm = rest ? lse : base_of(wave_max(lane < 4 ? red[0][lane] : -__builtin_inff()));
+    float tsum = 0.0f;
     if constexpr (FROM_PARTS) {
         m = wave_max(lane < 4 ? red[1][lane] : -__builtin_inff());
-        const float b = base_of(m);
-        for (int i = t; i < parts; i += 256) {
-            const float f = ex2((of[3 * i] - b) * c);
-            S += of[3 * i + 1] * f;
-            R += of[3 * i + 2] * f;
-        }
+        const float f = ex2((mt - base_of(m)) * c);
+        S = wave_sum(S * f);
+        R = wave_sum(R * f);
     }
     for (int i = t; i < ent.K; i += 256)
         if (list.col[i] >= 0) tsum += rest ? ex2((list.val[i] * s - tm) * LOG2E) : ex2((list.val[i] - tm) * c);
     tsum = wave_sum(tsum);
-    S = wave_sum(S);
-    R = wave_sum(R);
     if (lane == 0) {
         red[2][wave] = tsum;
         red[3][wave] = S;
@@ -509,18 +520,15 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     if constexpr (FROM_PARTS) {
         S = wave_sum(four(3));
         R = wave_sum(four(4));
-    } else {
-        m = stats[2 * row];
-        S = stats[2 * row + 1];
-        R = rest ? rest_sum[row] : 0.0f;
     }
     const bool some = any && (rest || tsum != 0.0f);
     float pr;
-    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, g, &pr);
     if (FROM_PARTS && p == 0) {          // uniform
         float l = 0.0f;
         for (int i = t; i < (some ? ent.K : 0); i += 256)
-            if (list.col[i] >= 0) l += entry_loss(ent, list.val[i], zk[row * ent.K + i], s, c, tm, tsum, m, S);
+            if (list.col[i] >= 0)
+                l += entry_loss(ent, list.val[i], i < 256 ? zk0 : zk[row * ent.K + i], s, c, tm, tsum, m, S);
         l = wave_sum(l);
         if (lane == 0) red[5][wave] = l;
         __syncthreads();
