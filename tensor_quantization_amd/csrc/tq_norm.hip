@@ -84,6 +84,23 @@ __device__ __forceinline__ float s8_code(float v, const S8Row& r)
     return int_code_f(q, 0.0f, MAGIC - 127.0f, MAGIC + 127.0f);
 }
 
+// Stores the codes of the vector's own elements, v as x's type holds them.
+template <int FT>
+__device__ __forceinline__ void store_codes(uint8_t* q, Vec8 at, const float v[8], const S8Row& p)
+{
+    float c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = s8_code<FT>(v[i], p);
+    if (at.lo == 0) {
+        const u32x2_any o = {pack_bytes4(c[0], c[1], c[2], c[3]), pack_bytes4(c[4], c[5], c[6], c[7])};
+        *reinterpret_cast<u32x2_any*>(q + at.at) = o;
+    } else {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (i >= at.lo) q[at.at + i] = (uint8_t)as_u(c[i]);
+    }
+}
+
 // k_ln_rows: NT threads per row, W vectors of eight elements per thread, the
 // row held in registers (8 <= cols <= 8 * NT * W): one read of x, the two sums
 // in turn from the registers, one write.  NT = 64 puts four rows in a workgroup
@@ -165,62 +182,127 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_rows(
         uint8_t* q = static_cast<uint8_t*>(y) + row * cols;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            if (at[w].lo == 8) continue;
-            float c[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = s8_code<FT>(v[w][i], p);
-            if (at[w].lo == 0) {
-                const u32x2_any o = {pack_bytes4(c[0], c[1], c[2], c[3]), pack_bytes4(c[4], c[5], c[6], c[7])};
-                *reinterpret_cast<u32x2_any*>(q + at[w].at) = o;
-            } else {
-#pragma unroll
-                for (int i = 1; i < 8; ++i)
-                    if (i >= at[w].lo) q[at[w].at + i] = (uint8_t)as_u(c[i]);
-            }
+            if (at[w].lo < 8) store_codes<FT>(q, at[w], v[w], p);
         }
     }
 }
 
-// k_ln_loop: rows of any length (below 8 elements, or longer than a workgroup
-// holds): a workgroup per row reads it once for the mean, once around the
-// mean and once for the output (the later reads meet the caches), and once
-// more for the codes.  An element at a time: [4096, 16384] bf16 takes 188 us
-// here and 66 held.
+// k_ln_long: rows longer than a workgroup holds: a workgroup per row reads it
+// once for the mean, once around the mean and once for the output (the later
+// reads meet the caches), and once more for the codes.  [4096, 20000] bf16 84 us
+// (3.9 TB/s of what it must read and write); an element per load took 245.
+constexpr int LN_LT = 1024;              // threads per long row
 template <int FT, int OUT>
-__global__ __launch_bounds__(1024) void k_ln_loop(const void* __restrict__ x, int64_t ldx, int64_t cols,
-                                                  const void* __restrict__ weight, const void* __restrict__ bias,
-                                                  int wdt, float eps, void* __restrict__ y, float* __restrict__ scale,
-                                                  float* __restrict__ mean, float* __restrict__ rstd)
+__global__ __launch_bounds__(LN_LT) void k_ln_long(const void* __restrict__ x, int64_t ldx, int cols,
+                                                   const void* __restrict__ weight, const void* __restrict__ bias,
+                                                   int wdt, float eps, void* __restrict__ y, float* __restrict__ scale,
+                                                   float* __restrict__ mean, float* __restrict__ rstd)
 {
-    __shared__ float slots[3][16];
-    const int t = threadIdx.x;
+    __shared__ float slots[3][LN_LT / 64];
+    const int t = threadIdx.x, nvec = (cols + 7) / 8;
     const int64_t row = blockIdx.x, base = row * ldx;
+    // f(a vector's eight elements, which of them are its own)
+    auto each = [&](auto f) {
+        for (int k = t; k < nvec; k += LN_LT) {
+            const Vec8 at = vec8(k, cols);
+            float v[8];
+            widen8<FT>(load8_any<FT>(x, base + at.at), v);
+            f(v, at);
+        }
+    };
     float s = 0.0f;
-    for (int64_t j = t; j < cols; j += 1024) s += load1<FT>(x, base + j);
-    const float mu = row_sum<1024>(s, slots[0]) / (float)cols;
+    each([&](const float v[8], Vec8 at) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += i >= at.lo ? v[i] : 0.0f;
+    });
+    const float mu = row_sum<LN_LT>(s, slots[0]) / (float)cols;
     s = 0.0f;
-    for (int64_t j = t; j < cols; j += 1024) {
-        const float d = load1<FT>(x, base + j) - mu;
-        s = __builtin_fmaf(d, d, s);
-    }
-    const float r = 1.0f / __builtin_sqrtf(row_sum<1024>(s, slots[1]) / (float)cols + eps);
+    each([&](const float v[8], Vec8 at) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = i >= at.lo ? v[i] - mu : 0.0f;
+            s = __builtin_fmaf(d, d, s);
+        }
+    });
+    const float r = 1.0f / __builtin_sqrtf(row_sum<LN_LT>(s, slots[1]) / (float)cols + eps);
     if (t == 0) {
         if (mean) mean[row] = mu;
         if (rstd) rstd[row] = r;
     }
-    auto value = [&](int64_t j) {
-        return __builtin_fmaf((load1<FT>(x, base + j) - mu) * r, load1_rt(weight, wdt, j, 1.0f),
-                              load1_rt(bias, wdt, j, 0.0f));
+    auto values = [&](float v[8], Vec8 at) {
+        float w[8], b[8];
+        widen8_rt(load8_rt(weight, wdt, at.at), weight, wdt, 1.0f, w);
+        widen8_rt(load8_rt(bias, wdt, at.at), bias, wdt, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf((v[i] - mu) * r, w[i], b[i]);
     };
     if constexpr (OUT == OUT_Y) {
-        for (int64_t j = t; j < cols; j += 1024) store1<FT>(y, row * cols + j, value(j));
+        each([&](float v[8], Vec8 at) {
+            values(v, at);
+            store8_own<FT>(y, row * cols, at, v);
+        });
     } else {
         float amax = 0.0f;
-        for (int64_t j = t; j < cols; j += 1024) amax = __builtin_fmaxf(amax, __builtin_fabsf(as_stored<FT>(value(j))));
-        const S8Row p = s8_row(row_max<1024>(amax, slots[2]));
+        each([&](float v[8], Vec8 at) {
+            values(v, at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                amax = __builtin_fmaxf(amax, i >= at.lo ? __builtin_fabsf(as_stored<FT>(v[i])) : 0.0f);
+        });
+        const S8Row p = s8_row(row_max<LN_LT>(amax, slots[2]));
         if (t == 0) scale[row] = p.s;
-        for (int64_t j = t; j < cols; j += 1024)
-            static_cast<uint8_t*>(y)[row * cols + j] = (uint8_t)as_u(s8_code<FT>(as_stored<FT>(value(j)), p));
+        each([&](float v[8], Vec8 at) {
+            values(v, at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = as_stored<FT>(v[i]);
+            store_codes<FT>(static_cast<uint8_t*>(y) + row * cols, at, v, p);
+        });
+    }
+}
+
+// k_ln_thin: rows of fewer than 8 elements, a thread each: [1000000, 7] bf16
+// 16.8 us (a workgroup per row: 3130).
+template <int FT, int OUT>
+__global__ __launch_bounds__(256) void k_ln_thin(const void* __restrict__ x, int64_t ldx, int64_t rows, int cols,
+                                                 const void* __restrict__ weight, const void* __restrict__ bias,
+                                                 int wdt, float eps, void* __restrict__ y, float* __restrict__ scale,
+                                                 float* __restrict__ mean, float* __restrict__ rstd)
+{
+    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (row >= rows) return;
+    float v[7], s = 0.0f, amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        v[j] = j < cols ? load1<FT>(x, row * ldx + j) : 0.0f;
+        s += v[j];
+    }
+    const float mu = s / (float)cols;
+    s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        v[j] = j < cols ? v[j] - mu : 0.0f;
+        s = __builtin_fmaf(v[j], v[j], s);
+    }
+    const float r = 1.0f / __builtin_sqrtf(s / (float)cols + eps);
+    if (mean) mean[row] = mu;
+    if (rstd) rstd[row] = r;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        if (j >= cols) break;
+        v[j] = __builtin_fmaf(v[j] * r, load1_rt(weight, wdt, j, 1.0f), load1_rt(bias, wdt, j, 0.0f));
+        if constexpr (OUT == OUT_Y) {
+            store1<FT>(y, row * cols + j, v[j]);
+        } else {
+            v[j] = as_stored<FT>(v[j]);
+            amax = __builtin_fmaxf(amax, __builtin_fabsf(v[j]));
+        }
+    }
+    if constexpr (OUT == OUT_S8) {
+        const S8Row p = s8_row(amax);
+        scale[row] = p.s;
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < cols) static_cast<uint8_t*>(y)[row * cols + j] = (uint8_t)as_u(s8_code<FT>(v[j], p));
     }
 }
 
@@ -410,54 +492,171 @@ __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int6
     }
 }
 
-// Rows of any length: a workgroup per row for dx (two reads), and a second
-// kernel for the column sums, a workgroup per 256 columns and chunk of rows
-// (two more): [4096, 16384] bf16 takes 262 us in these two and 92 held.
+// Rows longer than that: a workgroup per row for dx (two reads), and a second
+// kernel for the column sums (one more): a wave owns 512 columns, a workgroup's
+// four waves take a chunk of the rows in turn, U rows in flight each, and their
+// sums meet in LDS in wave order.  [4096, 20000] bf16 190 us (2.6 TB/s: x and dy
+// cross three times); an element per load took 328.
 template <int FT>
-__global__ __launch_bounds__(1024) void k_ln_bwd_loop(const void* __restrict__ dy, int64_t lddy,
-                                                      const void* __restrict__ x, int64_t ldx, int64_t cols,
-                                                      const void* __restrict__ weight, int wdt,
-                                                      const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                      void* __restrict__ dx)
+__global__ __launch_bounds__(LN_LT) void k_ln_bwd_long(const void* __restrict__ dy, int64_t lddy,
+                                                       const void* __restrict__ x, int64_t ldx, int cols,
+                                                       const void* __restrict__ weight, int wdt,
+                                                       const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                       void* __restrict__ dx)
 {
-    __shared__ float slots[2][16];
-    const int t = threadIdx.x;
+    __shared__ float slots[2][LN_LT / 64];
+    const int t = threadIdx.x, nvec = (cols + 7) / 8;
     const int64_t row = blockIdx.x;
     const float mu = mean[row], r = rstd[row];
+    // f(h, g, which of the eight are the vector's own)
+    auto each = [&](auto f) {
+        for (int k = t; k < nvec; k += LN_LT) {
+            const Vec8 at = vec8(k, cols);
+            const Raw8<FT> a = load8_any<FT>(x, row * ldx + at.at), b = load8_any<FT>(dy, row * lddy + at.at);
+            float h[8], g[8], w[8];
+            widen8_rt(load8_rt(weight, wdt, at.at), weight, wdt, 1.0f, w);
+            widen8<FT>(a, h);
+            widen8<FT>(b, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] = (h[i] - mu) * r;
+                g[i] *= w[i];
+            }
+            f(h, g, at);
+        }
+    };
     float sg = 0.0f, sgh = 0.0f;
-    for (int64_t j = t; j < cols; j += 1024) {
-        const float h = (load1<FT>(x, row * ldx + j) - mu) * r;
-        const float g = load1<FT>(dy, row * lddy + j) * load1_rt(weight, wdt, j, 1.0f);
-        sg += g;
-        sgh = __builtin_fmaf(g, h, sgh);
-    }
-    const float c1 = row_sum<1024>(sg, slots[0]) / (float)cols, c2 = row_sum<1024>(sgh, slots[1]) / (float)cols;
-    for (int64_t j = t; j < cols; j += 1024) {
-        const float h = (load1<FT>(x, row * ldx + j) - mu) * r;
-        const float g = load1<FT>(dy, row * lddy + j) * load1_rt(weight, wdt, j, 1.0f);
-        store1<FT>(dx, row * cols + j, (g - c1 - h * c2) * r);
-    }
+    each([&](const float h[8], const float g[8], Vec8 at) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float gg = i >= at.lo ? g[i] : 0.0f;
+            sg += gg;
+            sgh = __builtin_fmaf(gg, i >= at.lo ? h[i] : 0.0f, sgh);
+        }
+    });
+    const float c1 = row_sum<LN_LT>(sg, slots[0]) / (float)cols, c2 = row_sum<LN_LT>(sgh, slots[1]) / (float)cols;
+    each([&](const float h[8], float g[8], Vec8 at) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = (g[i] - c1 - h[i] * c2) * r;
+        store8_own<FT>(dx, row * cols, at, g);
+    });
 }
 
 template <int FT>
 __global__ __launch_bounds__(256) void k_ln_bwd_cols(const void* __restrict__ dy, int64_t lddy,
-                                                     const void* __restrict__ x, int64_t ldx, int64_t rows,
-                                                     int64_t cols, int64_t chunk, const float* __restrict__ mean,
+                                                     const void* __restrict__ x, int64_t ldx, int64_t rows, int cols,
+                                                     int64_t chunk, const float* __restrict__ mean,
                                                      const float* __restrict__ rstd, float* __restrict__ part,
                                                      int64_t ldp)
 {
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (j >= cols) return;
+    constexpr int U = 4;
+    __shared__ float fold[3][2][8][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Vec8 at = vec8((int)blockIdx.x * 64 + lane, cols);
     const int64_t r0 = blockIdx.y * chunk, r1 = r0 + chunk < rows ? r0 + chunk : rows;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        const float d = load1<FT>(dy, r * lddy + j);
-        dw = __builtin_fmaf(d, (load1<FT>(x, r * ldx + j) - mean[r]) * rstd[r], dw);
-        db += d;
+    float dw[8], db[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        dw[i] = 0.0f;
+        db[i] = 0.0f;
     }
-    float* to = part + (int64_t)blockIdx.y * 2 * ldp + j;
-    to[0] = dw;
-    to[ldp] = db;
+    for (int64_t r = r0 + w; r < r1; r += 4 * U) {
+        Raw8<FT> a[U], b[U];
+        float mu[U], rs[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = r + 4 * u < r1 ? r + 4 * u : r1 - 1;
+            mu[u] = mean[row];
+            rs[u] = rstd[row];
+            a[u] = load8_any<FT>(x, row * ldx + at.at);
+            b[u] = load8_any<FT>(dy, row * lddy + at.at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + 4 * u >= r1) break;
+            float h[8], d[8];
+            widen8<FT>(a[u], h);
+            widen8<FT>(b[u], d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dw[i] = __builtin_fmaf(d[i], (h[i] - mu[u]) * rs[u], dw[i]);
+                db[i] += d[i];
+            }
+        }
+    }
+    if (w > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            fold[w - 1][0][i][lane] = dw[i];
+            fold[w - 1][1][i][lane] = db[i];
+        }
+    }
+    __syncthreads();
+    if (w > 0 || at.lo == 8) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dw[i] += fold[k][0][i][lane];
+            db[i] += fold[k][1][i][lane];
+        }
+    float* to = part + (int64_t)blockIdx.y * 2 * ldp;
+    store8_own<F32>(to, 0, at, dw);
+    store8_own<F32>(to + ldp, 0, at, db);
+}
+
+// Rows of fewer than 8 elements: a thread per row and step, [1000000, 7] bf16
+// 45.5 us (a workgroup per row and column sums by single elements: 4640).
+template <int FT>
+__global__ __launch_bounds__(256) void k_ln_bwd_thin(const void* __restrict__ dy, int64_t lddy,
+                                                     const void* __restrict__ x, int64_t ldx, int64_t rows, int cols,
+                                                     int64_t chunk, const void* __restrict__ weight, int wdt,
+                                                     const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                     void* __restrict__ dx, float* __restrict__ part, int64_t ldp)
+{
+    __shared__ float fold[4][2][7];
+    const int t = threadIdx.x;
+    const int64_t r0 = (int64_t)blockIdx.x * chunk, r1 = r0 + chunk < rows ? r0 + chunk : rows;
+    float ww[7], dw[7], db[7];
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        ww[j] = j < cols ? load1_rt(weight, wdt, j, 1.0f) : 0.0f;
+        dw[j] = 0.0f;
+        db[j] = 0.0f;
+    }
+    for (int64_t r = r0 + t; r < r1; r += 256) {
+        const float mu = mean[r], rs = rstd[r];
+        float h[7], d[7], sg = 0.0f, sgh = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 7; ++j) {
+            h[j] = j < cols ? (load1<FT>(x, r * ldx + j) - mu) * rs : 0.0f;
+            d[j] = j < cols ? load1<FT>(dy, r * lddy + j) : 0.0f;
+            dw[j] = __builtin_fmaf(d[j], h[j], dw[j]);
+            db[j] += d[j];
+            sg = __builtin_fmaf(d[j], ww[j], sg);
+            sgh = __builtin_fmaf(d[j] * ww[j], h[j], sgh);
+        }
+        const float c1 = sg / (float)cols, c2 = sgh / (float)cols;
+        if (dx) {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < cols) store1<FT>(dx, r * cols + j, (d[j] * ww[j] - c1 - h[j] * c2) * rs);
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        const float a = wave_sum(dw[j]), b = wave_sum(db[j]);
+        if ((t & 63) == 0) {
+            fold[t >> 6][0][j] = a;
+            fold[t >> 6][1][j] = b;
+        }
+    }
+    __syncthreads();
+    if (t >= cols) return;
+    float* to = part + (int64_t)blockIdx.x * 2 * ldp + t;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) to[o * ldp] = fold[0][o][t] + fold[1][o][t] + fold[2][o][t] + fold[3][o][t];
 }
 
 // ------------------------------------------------------------- column sums
@@ -517,9 +716,7 @@ void colsum_launch(const float* part, int64_t parts, int outs, int64_t ld, int64
 constexpr int64_t LN_HELD = 16384;       // longest row that a workgroup holds in registers
 constexpr int64_t LN_BWD_HELD = 16384;   // and that of dy beside it; half as many in binary32
 constexpr int64_t LN_PARTS = 256;        // workgroups of the backward pass, one row of partials each
-constexpr int64_t LN_COL_CHUNKS = 64;    // row chunks of the column kernel of long rows
-
-inline bool ln_held(int64_t cols, int64_t most) { return cols >= 8 && cols <= most; }
+constexpr int64_t LN_COL_CHUNKS = 64;    // row chunks of the column kernel of longer rows
 
 // Threads and vectors per row, measured on 8192 rows (us, taken / next best):
 //   1024 bf16  64 x 2  11.0 / 13.3 (256 x 1)     4096 bf16  256 x 2  23.5 / 25.5 (512 x 1)
@@ -534,9 +731,12 @@ static void ln_launch(const void* x, int64_t ldx, int64_t rows, int64_t cols, co
 #define TQ_LN(NT, W)                                                                                              \
     hipLaunchKernelGGL((k_ln_rows<FT, NT, W, OUT>), dim3((unsigned)cdiv(rows, NT < 256 ? 256 / NT : 1)),          \
                        dim3(NT < 256 ? 256 : NT), 0, st, x, ldx, rows, cols, w, b, wdt, eps, y, scale, mean, rstd)
-    if (!ln_held(cols, LN_HELD))
-        hipLaunchKernelGGL((k_ln_loop<FT, OUT>), dim3((unsigned)rows), dim3(1024), 0, st, x, ldx, cols, w, b, wdt, eps,
-                           y, scale, mean, rstd);
+    if (cols < 8)
+        hipLaunchKernelGGL((k_ln_thin<FT, OUT>), dim3((unsigned)cdiv(rows, 256)), dim3(256), 0, st, x, ldx, rows,
+                           (int)cols, w, b, wdt, eps, y, scale, mean, rstd);
+    else if (cols > LN_HELD)
+        hipLaunchKernelGGL((k_ln_long<FT, OUT>), dim3((unsigned)rows), dim3(LN_LT), 0, st, x, ldx, (int)cols, w, b, wdt,
+                           eps, y, scale, mean, rstd);
     else if (cols <= 512) TQ_LN(64, 1);
     else if (cols <= 1024) TQ_LN(64, 2);
     else if (cols <= 2048) TQ_LN(256, 1);
@@ -570,17 +770,21 @@ static void ln_bwd_launch(const void* dy, int64_t lddy, const void* x, int64_t l
         hipLaunchKernelGGL((k_ln_bwd<FT, NT, W, BT>), dim3((unsigned)parts), dim3(BT), 0, st, dy, lddy, x, ldx,   \
                            rows, cols, w, wdt, mean, rstd, dx, part, ld);                                         \
     } while (0)
-    if (!ln_held(cols, FT == F32 ? LN_BWD_HELD / 2 : LN_BWD_HELD)) {
-        if (dx)
-            hipLaunchKernelGGL((k_ln_bwd_loop<FT>), dim3((unsigned)rows), dim3(1024), 0, st, dy, lddy, x, ldx, cols, w,
-                               wdt, mean, rstd, dx);
+    if (cols < 8) {
+        const int64_t chunk = cdiv(cdiv(rows, LN_PARTS), 256) * 256;
+        parts = cdiv(rows, chunk);
+        hipLaunchKernelGGL((k_ln_bwd_thin<FT>), dim3((unsigned)parts), dim3(256), 0, st, dy, lddy, x, ldx, rows,
+                           (int)cols, chunk, w, wdt, mean, rstd, dx, part, ld);
+    } else if (cols > (FT == F32 ? LN_BWD_HELD / 2 : LN_BWD_HELD)) {
         if (part) {
-            parts = rows < LN_COL_CHUNKS ? rows : LN_COL_CHUNKS;
-            const int64_t chunk = cdiv(rows, parts);
+            const int64_t chunk = cdiv(cdiv(rows, LN_COL_CHUNKS), 16) * 16;
             parts = cdiv(rows, chunk);
-            hipLaunchKernelGGL((k_ln_bwd_cols<FT>), dim3((unsigned)cdiv(cols, 256), (unsigned)parts), dim3(256), 0, st,
-                               dy, lddy, x, ldx, rows, cols, chunk, mean, rstd, part, ld);
+            hipLaunchKernelGGL((k_ln_bwd_cols<FT>), dim3((unsigned)cdiv(cols, 512), (unsigned)parts), dim3(256), 0, st,
+                               dy, lddy, x, ldx, rows, (int)cols, chunk, mean, rstd, part, ld);
         }
+        if (dx)
+            hipLaunchKernelGGL((k_ln_bwd_long<FT>), dim3((unsigned)rows), dim3(LN_LT), 0, st, dy, lddy, x, ldx,
+                               (int)cols, w, wdt, mean, rstd, dx);
     }
     else if (cols <= 512) TQ_LNB(64, 1, 512);
     else if (cols <= 1024) TQ_LNB(128, 1, 512);
@@ -605,10 +809,10 @@ void zero_vec_launch(void* p, int dt, int64_t n, hipStream_t st)
 
 static bool natural(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(ftype_size(dt) - 1)) == 0; }
 
-// A workgroup per row, and columns counted in 32 bits.
+// A workgroup per row, and columns counted in 32 bits, a slab past their end.
 static bool ln_fits(int64_t rows, int64_t cols)
 {
-    return rows <= 0x7fffffff && cols <= 0x7fffffff;
+    return rows <= 0x7fffffff && cols <= 0x7fffffff - 1024;
 }
 
 static tq_status ln_check(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void* w,
@@ -658,7 +862,7 @@ tq_status tq_layer_norm_quant_per_token(const void* x, int x_dtype, int64_t rows
 size_t tq_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (rows <= 0 || cols <= 0) return 0;
-    const int64_t parts = ln_held(cols, LN_BWD_HELD) ? LN_PARTS : LN_COL_CHUNKS;
+    const int64_t parts = cols > LN_BWD_HELD ? LN_COL_CHUNKS : LN_PARTS;
     return (size_t)(rows < parts ? rows : parts) * 2 * (size_t)colsum_ld(cols) * sizeof(float);
 }
 

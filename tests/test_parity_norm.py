@@ -36,7 +36,17 @@ WIDTHS = [1, 7, 8, 9, 64, 511, 512, 520, 1000, 1024, 1025, 2048, 2056, 4095, 409
 @pytest.mark.parametrize("ft", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("cols", WIDTHS)
 def test_forward_and_backward(tq, ft, cols):
-    rows = 5 if cols > 1024 else 37
+    forward_and_backward(tq, ft, 5 if cols > 1024 else 37, cols)
+
+
+# rows of a few elements, and rows that no workgroup holds, over several chunks of rows
+@pytest.mark.parametrize("ft", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(70000, 2), (700, 3), (257, 7), (1100, 8209), (1030, 16400), (70, 20001)])
+def test_short_and_long_rows(tq, ft, rows, cols):
+    forward_and_backward(tq, ft, rows, cols)
+
+
+def forward_and_backward(tq, ft, rows, cols):
     wt = "f32" if cols % 2 else ft
     note("norm", ft, wt, rows, cols)
     x, dy = draw((rows, cols), ft, cols), draw((rows, cols), ft, cols + 1, mean=0.1)
@@ -59,7 +69,7 @@ def test_forward_and_backward(tq, ft, cols):
 
 @pytest.mark.parametrize("ft", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(1, 4096), (3, 8), (2, 5), (33, 1000), (17, 2056), (4, 4095), (9, 8192),
-                                       (2, 16384), (2, 20001)])
+                                       (2, 16384), (2, 20001), (600, 3), (300, 7)])
 def test_fused_quantizer_is_the_two_calls(tq, ft, rows, cols):
     """Codes and scales are bit for bit those of the norm followed by the
     per-token quantizer, zero rows and rows of one value included."""
