@@ -212,66 +212,81 @@ __device__ __forceinline__ v4i codes16(const int8_t* row, int64_t k, int64_t K)
 }
 
 // ------------------------------------------------------------- a few tokens
-// k_epi_few (M <= 16 MT): bound by the weights, which are read once.  A
-// workgroup of NWV waves owns 16 output columns; the waves take the K axis in
-// turn, 128 codes at a time, so that a wave's two loads use whole 128-byte
+// k_epi_few: a few tokens, bound by the weights, which are read once; or an
+// output of few elements.  A workgroup of NWV waves owns 16 CT output columns of
+// 16 MT tokens; the waves take the K axis in turn, 128 codes at a time, so that a wave's two loads use whole 128-byte
 // lines; the sums meet in LDS, one thread per output.  The weights are the
-// matrix core's first operand (16 columns), the tokens its second (16 tokens,
-// rows past M repeat row M - 1), U blocks of both in flight per wave.  What an
+// matrix core's first operand (16 columns), the tokens its second (16 tokens;
+// rows past the end repeat the last), U blocks of both in flight per wave.  What an
 // output's epilogue needs is loaded before the weights are.  Kernel times: 1 x
 // 11008 x 4096 10.2 us (4.4 TB/s of weights), 16 x 4096 x 11008 12.2 (3.7): with
 // 256 workgroups each CU has one slice of 16 columns, whose first loads and
-// last sums nothing covers.
-// Refilling each of the U slots as it is used instead of all at once: 13.3 ->
-// 12.2 us.
-template <int YT, int MT, int NWV, int U>
+// last sums nothing covers.  Refilling each of the U slots as it is used instead
+// of all at once: 13.3 -> 12.2 us.
+template <int YT, int MT, int CT, int NWV, int U>
 __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
                                                       int64_t K, Epi e)
 {
-    constexpr int NT = 64 * NWV, PER = MT * 256 > NT ? MT * 256 / NT : 1;   // outputs per thread
-    __shared__ int sums[NWV][MT * 16][20];   // rows of 16 sums, 20 apart (16-byte steps that spread over the banks)
+    constexpr int NT = 64 * NWV, COLS = 16 * CT, STEP = NT / COLS;           // rows of outputs per step of all threads
+    constexpr int PER = 16 * MT > STEP ? 16 * MT / STEP : 1;                 // outputs per thread
+    // rows 4 apart beyond their sums: 16-byte steps that spread over the banks
+    __shared__ int sums[NWV][MT * 16][COLS + 4];
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l16 = lane & 15, g4 = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = (int64_t)blockIdx.x * COLS, m0 = (int64_t)blockIdx.y * (16 * MT);
 
-    // thread t finishes column t % 16 of tokens t / 16, + NT / 16, ...
-    const int64_t on = n0 + (t & 15);
+    // thread t finishes column t % COLS of tokens t / COLS, + STEP, ...
+    const int64_t on = n0 + t % COLS;
     float osx[PER], ores[PER], osw = 0.0f, ob = 0.0f;
     bool mine[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int m = t / 16 + i * (NT / 16);
-        mine[i] = m < 16 * MT && m < e.M && on < e.N;
-        osx[i] = mine[i] ? e.sx[m] : 0.0f;
-        ores[i] = mine[i] && e.res ? load1<YT>(e.res, m * e.ldr + on) : 0.0f;
+        const int m = t / COLS + i * STEP;
+        mine[i] = m < 16 * MT && m0 + m < e.M && on < e.N;
+        osx[i] = mine[i] ? e.sx[m0 + m] : 0.0f;
+        ores[i] = mine[i] && e.res ? load1<YT>(e.res, (m0 + m) * e.ldr + on) : 0.0f;
     }
     if (mine[0]) {
         osw = e.sw[on];
         ob = load1_rt(e.bias, e.bias_dt, on, 0.0f);
     }
 
-    const int64_t n = n0 + l16 < e.N ? n0 + l16 : e.N - 1;
-    const int8_t* pw = qw + n * K;
+    const int8_t* pw[CT];
     const int8_t* px[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = 16 * i + l16 < e.M ? 16 * i + l16 : e.M - 1;
-        px[i] = qx + m * K;
+    for (int j = 0; j < CT; ++j) {
+        const int64_t n = n0 + 16 * j + l16;
+        pw[j] = qw + (n < e.N ? n : e.N - 1) * K;
     }
-    v4i acc[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = v4i{};
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + 16 * i + l16;
+        px[i] = qx + (m < e.M ? m : e.M - 1) * K;
+    }
+    v4i acc[MT][CT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = v4i{};
     // this wave's whole blocks are w, w + NWV, ...: U of them under way, each slot refilled as it is used
     const int nkb = (int)((K + 127) / 128), whole = (int)(K / 128);
-    v4i a[U][2], b[U][2][MT];
+    v4i a[U][2][CT], b[U][2][MT];
     auto fetch = [&](int u, int kb) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int k = kb * 128 + 64 * s + 16 * g4;
-            a[u][s] = codes16_whole(pw + k);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) a[u][s][j] = codes16_whole(pw[j] + k);
 #pragma unroll
             for (int i = 0; i < MT; ++i) b[u][s][i] = codes16_whole(px[i] + k);
         }
+    };
+    auto products = [&](const v4i (&x)[CT], const v4i (&y)[MT]) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[j], y[i], acc[i][j], 0, 0, 0);
     };
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -281,35 +296,36 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
         for (int u = 0; u < U; ++u) {
             if (kb + u * NWV >= whole) break;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][s], b[u][s][i], acc[i], 0, 0, 0);
+            for (int s = 0; s < 2; ++s) products(a[u][s], b[u][s]);
             if (kb + (u + U) * NWV < whole) fetch(u, kb + (u + U) * NWV);
         }
     if (whole < nkb && whole % NWV == w)     // the rest of K
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int64_t k = (int64_t)whole * 128 + 64 * s + 16 * g4;
-            const v4i r = codes16(pw, k, K);
+            v4i x[CT], y[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(r, codes16(px[i], k, K), acc[i], 0, 0, 0);
+            for (int j = 0; j < CT; ++j) x[j] = codes16(pw[j], k, K);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) y[i] = codes16(px[i], k, K);
+            products(x, y);
         }
     // lane l holds columns 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<v4i*>(&sums[w][16 * i + l16][4 * g4]) = acc[i];
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) *reinterpret_cast<v4i*>(&sums[w][16 * i + l16][16 * j + 4 * g4]) = acc[i][j];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int m = t / 16 + i * (NT / 16);
+        const int m = t / COLS + i * STEP;
         if (!mine[i]) continue;
         int s = 0;
 #pragma unroll
-        for (int v = 0; v < NWV; ++v) s += sums[v][m][t & 15];
+        for (int v = 0; v < NWV; ++v) s += sums[v][m][t % COLS];
         float v = (float)s * osx[i] * osw;
         if (e.bias) v += ob;
-        const int64_t at = m * e.N + on;
+        const int64_t at = (m0 + m) * e.N + on;
         if (e.z) store1<YT>(e.z, at, v);
         with_act(e.act, [&](auto a) { v = act1<decltype(a)::value>(v); });
         if (e.res) v += ores[i];
@@ -928,8 +944,14 @@ inline int64_t epi_chunk(int64_t M, int64_t N)
 // round of resident workgroups (two 64 x 64 tiles or, up to 256 of them, one
 // 128 x 128 tile per CU), so the smallest tile that needs one round is taken,
 // and the largest once it fills the chip.  128 x 128 tiles beyond one round run
-// two to a CU on shorter rings.  Operands of other alignments (k_epi_tile, us;
-// 64 / 128 / 256 tile):
+// two to a CU on shorter rings.  Where the output is so small that tiles leave
+// most CUs idle, its 32 x 16 or 32 x 32 pieces, each with the K axis split over
+// eight waves, do not (tiles / 32 x 16 / 32 x 32):
+//   220 x 507 x 10256   27 / 13.4 / 17.1     40 x 1024 x 8192     17.8 / 12.9 / 16.6
+//   64 x 4096 x 4096  11.1 / 13.3 / 9.9      1260 x 140 x 10688   23.4 / 26 / 17.2
+//   128 x 4096 x 4096 11.2 / 24 / 16.9       220 x 507 x 10250    34 / 42 / 55
+// (the last with rows at odd addresses, whose loads cost these kernels more).
+// Operands of other alignments (k_epi_tile, us; 64 / 128 / 256 tile):
 //   243 x 2546 x 9000    26.7 / 51 / -      777 x 4096 x 4095     57 / 35 / 81
 //   2564 x 614 x 2708    20.5 / 21.8 / -    2048 x 4096 x 4098    87 / 58 / 75
 //   1024 x 11008 x 4088    - / 71 / 67      4096 x 4096 x 4088     - / 96 / 75
@@ -938,16 +960,16 @@ template <int YT>
 static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Epi& e, hipStream_t st)
 {
     const bool rows16 = K >= ET && K % 16 == 0 && aligned16(qx) && aligned16(qw);
-#define TQ_FEW(MT, NWV, U)                                                                                 \
-    hipLaunchKernelGGL((k_epi_few<YT, MT, NWV, U>), dim3((unsigned)cdiv(e.N, 16)), dim3(64 * NWV), 0, st, qx, qw, K, e)
-    if (e.M <= 16) {
-        TQ_FEW(1, 8, 4);
-        return;
-    }
-    if (e.M <= 32 && (e.N <= 6144 || !rows16)) {
-        TQ_FEW(2, 8, 2);
-        return;
-    }
+#define TQ_FEW(MT, CT, NWV, U)                                                                              \
+    do {                                                                                                    \
+        const dim3 grid((unsigned)cdiv(e.N, 16 * CT), (unsigned)cdiv(e.M, 16 * MT));                        \
+        hipLaunchKernelGGL((k_epi_few<YT, MT, CT, NWV, U>), grid, dim3(64 * NWV), 0, st, qx, qw, K, e);     \
+        return;                                                                                             \
+    } while (0)
+    if (e.M <= 16) TQ_FEW(1, 1, 8, 4);
+    if ((e.M <= 32 && (e.N <= 6144 || !rows16)) || (rows16 && cdiv(e.M, 32) * cdiv(e.N, 16) <= 256))
+        TQ_FEW(2, 1, 8, 2);
+    if (rows16 && cdiv(e.M, 32) * cdiv(e.N, 32) <= 256) TQ_FEW(2, 2, 8, 2);
 #undef TQ_FEW
     if (rows16) {
 #define TQ_RING(TILE, RING, WM, WN, WGS)                                                                     \

@@ -61,7 +61,8 @@ def test_sizes(tq, M, N, K, ft):
 
 # every tile size, with tiles that stick out on both sides and a K that ends inside a block
 @pytest.mark.parametrize("M,N,K", [(1000, 1100, 272), (1500, 1600, 528), (2100, 2200, 144), (4100, 4110, 400),
-                                   (4096, 4096, 2048), (40, 6200, 1040), (30, 7000, 208)])
+                                   (4096, 4096, 2048), (40, 6200, 1040), (30, 7000, 208), (64, 4000, 1040),
+                                   (250, 1000, 400), (1201, 140, 1552), (220, 507, 2064), (40, 1001, 1168)])
 @pytest.mark.parametrize("ft,act", [("bf16", "silu"), ("f32", "none")])
 def test_tiles(tq, M, N, K, ft, act):
     note("product tiles", M, N, K, ft)
