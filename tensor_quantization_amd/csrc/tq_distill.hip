@@ -253,16 +253,16 @@ __device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, 
 }
 
 // --------------------------------------------------------------- statistics
-// k_distill_stats: a workgroup per row and part of the row (CH columns): the
-// part's largest logit m, the sum of 2^((z - m) c) over all its columns and
-// over those that are no entries (only with REST), and the logits at its
-// entries, zk [rows, K] (for the loss, which may be taken after the gradient
+// k_distill_stats: a workgroup per row and part of the row (`len` columns, at
+// most CH): the part's largest logit m, the sum of 2^((z - m) c) over all its
+// columns and over those that are no entries (only with REST), and the logits
+// at its entries, zk [rows, K] (for the loss, which may be taken after the gradient
 // has overwritten the logits).  A thread keeps its own running maximum and
 // sums, rescaled when a vector of eight exceeds it, so a part is one pass with
 // no barrier before the end.  Bound by HBM: [512, 32000] f32 12.9 us (5.1 TB/s).
 template <int FT, bool REST, int CH>
 __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ z, int64_t ldz, int V, int parts,
-                                                       Entries ent, float c, float* __restrict__ part,
+                                                       int len, Entries ent, float c, float* __restrict__ part,
                                                        float* __restrict__ zk)
 {
     constexpr int U = 4;
@@ -270,8 +270,8 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
     __shared__ float red[4][3];
     const int t = threadIdx.x;
     const int64_t row = blockIdx.x / (unsigned)parts;
-    const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * CH;
-    const int n = V - c0 < CH ? V - c0 : CH, nvec = (n + 7) / 8;
+    const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * len;
+    const int n = V - c0 < len ? V - c0 : len, nvec = (n + 7) / 8;
     const int64_t base = row * ldz + c0;
     if constexpr (REST) {
         for (int i = t; i < CH / 32 + 1; i += 256) bits[i] = 0;
@@ -433,8 +433,8 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
 // gradient 15.8 us, 18.6 with one; 40 / 43 for [512, 32000] f32 forwards and
 // back).  Bound by HBM: [512, 32000] f32 23.4 us (5.6 TB/s).
 template <int FT, int CH, bool FROM_PARTS>
-__global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz, int V, int parts, Entries ent,
-                                                      float s, float c, const float* __restrict__ part,
+__global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz, int V, int parts, int len,
+                                                      Entries ent, float s, float c, const float* __restrict__ part,
                                                       const float* __restrict__ zk, const float* __restrict__ stats,
                                                       const float* __restrict__ rest_sum,
                                                       const float* __restrict__ dloss, float* __restrict__ loss,
@@ -447,8 +447,8 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     __shared__ int any;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int64_t row = blockIdx.x / (unsigned)parts;
-    const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * CH;
-    const int n = V - c0 < CH ? V - c0 : CH, nvec = (n + 7) / 8;
+    const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * len;
+    const int n = V - c0 < len ? V - c0 : len, nvec = (n + 7) / 8;
     const int64_t from = row * ldz + c0, to = row * lddz + c0;
     const bool rest = ent.tlse != nullptr;
     Raw8<FT> raw[U];
@@ -794,26 +794,29 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
 }
 
 // ---------------------------------------------------------------- launches
-// Columns per part: the longest of 32768, 16384, 8192 and 4096 that still
-// gives the chip DT_GROUPS workgroups.  Measured, forwards and back, us, at 512
-// / 2048 / 8192 workgroups: [512, 32000] f32 41.5 / 38.6 / 44.3, [128, 131072]
-// bf16 28.8 / 25.6 / 30.7, [2048, 32000] bf16 94 / 94 / 86, [2048, 131072] bf16
-// 324 / 324 / 324.
+// Most columns per part: 8192, or 4096 where that would not give the chip
+// DT_GROUPS workgroups.  Measured, forwards and back, us, parts of 4096 / 8192 /
+// longer: [512, 32000] f32 44 / 37.7 / 41.5, [128, 131072] bf16 30.9 / 25.4 /
+// 28.8, [2048, 32000] bf16 - / 84 / 92, [2048, 131072] bf16 - / 297 / 324.
 constexpr int64_t DT_GROUPS = 2048;
-constexpr int DT_CH[] = {32768, 16384, 8192, 4096};
-inline int distill_ch(int64_t rows, int64_t V)
+// The parts of a row have one length, a multiple of 8 (the last may be shorter):
+// [1700, 41410] f32 234 -> 187 us against full parts and a rest.
+struct Split {
+    int ch, len, parts;
+};
+inline Split distill_split(int64_t rows, int64_t V)
 {
-    for (int ch : DT_CH)
-        if (rows * cdiv(V, ch) >= DT_GROUPS) return ch;
-    return DT_CH[3];
+    Split q;
+    q.ch = rows * cdiv(V, 8192) >= DT_GROUPS ? 8192 : 4096;
+    q.len = (int)cdiv(cdiv(V, cdiv(V, q.ch)), 8) * 8;
+    q.parts = (int)cdiv(V, q.len);
+    return q;
 }
 
-#define TQ_CH_SWITCH(ch, ...)                                                                \
-    do {                                                                                     \
-        if ((ch) == 32768) { constexpr int CHV = 32768; __VA_ARGS__; }                       \
-        else if ((ch) == 16384) { constexpr int CHV = 16384; __VA_ARGS__; }                  \
-        else if ((ch) == 8192) { constexpr int CHV = 8192; __VA_ARGS__; }                    \
-        else { constexpr int CHV = 4096; __VA_ARGS__; }                                      \
+#define TQ_CH_SWITCH(ch, ...)                                    \
+    do {                                                         \
+        if ((ch) == 8192) { constexpr int CHV = 8192; __VA_ARGS__; } \
+        else { constexpr int CHV = 4096; __VA_ARGS__; }          \
     } while (0)
 
 struct Distill {
@@ -827,27 +830,27 @@ struct Distill {
 // Workspace: the parts' statistics, then the logits at the entries.
 inline size_t distill_part_floats(int64_t rows, int64_t V)
 {
-    return 3 * (size_t)rows * (size_t)cdiv(V, distill_ch(rows, V));
+    return 3 * (size_t)rows * (size_t)distill_split(rows, V).parts;
 }
 
 template <int FT>
 static void stats_launch(const Distill& d, float* ws, hipStream_t st)
 {
-    const int ch = distill_ch(d.rows, d.V), parts = (int)cdiv(d.V, ch);
-    const dim3 grid((unsigned)(d.rows * parts));
+    const Split q = distill_split(d.rows, d.V);
+    const dim3 grid((unsigned)(d.rows * q.parts));
     float* zk = ws + distill_part_floats(d.rows, d.V);
     if (d.ent.tlse)
-        TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
-                                            parts, d.ent, d.c, ws, zk));
+        TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
+                                            q.parts, q.len, d.ent, d.c, ws, zk));
     else
-        TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
-                                            parts, d.ent, d.c, ws, zk));
+        TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz,
+                                            d.V, q.parts, q.len, d.ent, d.c, ws, zk));
 }
 
 static void rows_launch(const Distill& d, const float* ws, float* loss, float* stats, float* rest_sum, hipStream_t st)
 {
     hipLaunchKernelGGL(k_distill_rows, dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.rows, d.V, d.ent, d.s, d.c,
-                       ws, ws + distill_part_floats(d.rows, d.V), (int)cdiv(d.V, distill_ch(d.rows, d.V)), loss, stats,
+                       ws, ws + distill_part_floats(d.rows, d.V), distill_split(d.rows, d.V).parts, loss, stats,
                        rest_sum);
 }
 
@@ -855,29 +858,35 @@ template <int FT, bool FROM_PARTS>
 static void grad_launch(const Distill& d, const float* ws, const float* stats, const float* rest_sum,
                         const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
 {
-    const int ch = distill_ch(d.rows, d.V), parts = (int)cdiv(d.V, ch);
+    const Split q = distill_split(d.rows, d.V);
     const float* zk = FROM_PARTS ? ws + distill_part_floats(d.rows, d.V) : nullptr;
-    TQ_CH_SWITCH(ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV, FROM_PARTS>), dim3((unsigned)(d.rows * parts)),
-                                        dim3(256), 0, st, d.z, d.ldz, d.V, parts, d.ent, d.s, d.c, ws, zk, stats,
-                                        rest_sum, dloss, loss, dz, lddz));
+    TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV, FROM_PARTS>), dim3((unsigned)(d.rows * q.parts)),
+                                        dim3(256), 0, st, d.z, d.ldz, d.V, q.parts, q.len, d.ent, d.s, d.c, ws, zk,
+                                        stats, rest_sum, dloss, loss, dz, lddz));
 }
 
 // Whether the joint call holds its rows in registers.  A row in registers costs
 // one read instead of two, and spreads over no more than one workgroup: rows of
 // 64 KB (a workgroup of 256 threads) are held at any number of them; of 128 KB
 // from DT_HELD_ROWS of them on; of 256 KB, which take a CU each, where they
-// fill at least 5/8 of their rounds over the CUs.  Measured, us, held / in
-// parts:   1 row of 32000 bf16 12.1 / 14.6, 256 rows 13.0 / 17.3;   64 rows of
-// 65536 bf16 15.7 / 14.5, 128 rows 16.6 / 17.4;   rows of 131072 bf16: 128 of
-// them 26.4 / 22.4, 160 28.2 / 29.1, 300 58 / 47, 512 66 / 88, 4096 482 / 640.
+// fill at least 5/8 of their rounds over the CUs (binary32, which takes more
+// instructions per byte, 7/8 of at least two rounds).  Measured, us, held / in
+// parts:   1 row of 32000 bf16 12.1 / 14.7, 256 rows 13.0 / 17.8, 2048 rows 56 /
+// 83;   64 rows of 65536 bf16 15.6 / 14.6, 128 rows 15.8 / 17.8;   rows of
+// 131072 bf16: 128 of them 26.4 / 22.7, 160 28.2 / 29.3, 300 57 / 48, 512 66 /
+// 80, 4096 482 / 643;   of 65536 f32: 256 43 / 36, 512 76 / 79, 2048 278 / 306.
 constexpr int64_t DT_HELD_ROWS = 128;
 template <int FT>
 static bool held_launch(const Distill& d, const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
 {
     constexpr int H = FT == F32 ? 2 : 1;  // binary32 rows hold half as many elements
     if (d.V < 8 || d.V > 131072 / H) return false;
-    if (d.V > 65536 / H ? 8 * d.rows < 5 * 256 * cdiv(d.rows, 256) : d.V > 32768 / H && d.rows < DT_HELD_ROWS)
+    if (d.V > 65536 / H) {
+        const int64_t rounds = std::max<int64_t>(H, cdiv(d.rows, 256));
+        if (8 * d.rows < (H == 2 ? 7 : 5) * 256 * rounds) return false;
+    } else if (d.V > 32768 / H && d.rows < DT_HELD_ROWS) {
         return false;
+    }
     // as many workgroups as fit on the chip by their registers
 #define TQ_HELD(NT, W)                                                                                            \
     hipLaunchKernelGGL((k_distill_held<FT, NT, W>), dim3((unsigned)std::min<int64_t>(d.rows, 256 * (1024 / NT) * \
@@ -905,7 +914,7 @@ static tq_status distill_check(const void* logits, int dt, int64_t rows, int64_t
     if (!(temperature > 0.0f) || temperature > 3.0e38f) return TQ_ERR_INVALID;
     if (rows == 0) return TQ_OK;
     if (vocab == 0 || !logits || ldz < vocab || !idx || !val) return TQ_ERR_INVALID;
-    if (K > DT_K || vocab > 0x7fffff00 || rows > 0x7fffffff || rows * cdiv(vocab, DT_CH[3]) > 0x7fffffff)
+    if (K > DT_K || vocab > 0x7fffff00 || rows > 0x7fffffff || rows * cdiv(vocab, 4096) > 0x7fffffff)
         return TQ_ERR_UNSUPPORTED;
     if (!natural(logits, ftype_size(dt)) || !natural(idx, idx_bits / 8) || !natural(val, ftype_size(val_dt)) ||
         !natural(teacher_lse, 4))

@@ -64,10 +64,18 @@ def test_sizes(tq, rows, V, K, rest, ft):
     check(tq, z, idx, val, 1.0, tlse if rest else None, dloss, ft)
 
 
+@pytest.mark.parametrize("rows", [131, 170])
 @pytest.mark.parametrize("V,ft", [(40003, "bf16"), (65536, "f16"), (70001, "bf16"), (98304, "bf16"), (131072, "bf16"),
                                   (131001, "f16"), (50001, "f32"), (65544, "f32"), (140000, "bf16")])
-@pytest.mark.parametrize("rows", [131, 170])
 def test_long_rows(tq, rows, V, ft):
+    long_rows(tq, rows, V, ft)
+
+
+def test_long_binary32_rows_of_two_rounds(tq):
+    long_rows(tq, 450, 40003, "f32")
+
+
+def long_rows(tq, rows, V, ft):
     note("distill long", rows, V, ft)
     z, idx, val, tlse, dloss = draw(rows, V, 40, V, ft)
     pick = [0, 1, 64, 129, 130]
