@@ -110,15 +110,15 @@ __device__ __forceinline__ Coef make_coef(bool rest, bool some, float m, float S
     return q;
 }
 
-// Entry k's part of the loss.
+// Entry k's part of the loss; lgS is log2 of the student's sum relative to m.
 __device__ __forceinline__ float entry_loss(const Entries& e, float t, float z, float s, float c, float tm, float tsum,
-                                            float m, float S)
+                                            float m, float S, float lgS)
 {
     const float logp = e.tlse ? (t * s - tm) : ((t - tm) * s - lg2(tsum) * LN2);
     const float p = e.tlse ? ex2(logp * LOG2E) : ex2((t - tm) * c) / tsum;
     if (p == 0.0f) return 0.0f;
     if (S == 0.0f) return __builtin_inff();
-    return p * (logp - ((z - base_of(m)) * s - lg2(S) * LN2));
+    return p * (logp - ((z - base_of(m)) * s - lgS * LN2));
 }
 __device__ __forceinline__ float rest_loss(float pr, float R, float S)
 {
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
     if (some)
         for (int k = lane; k < ent.K; k += 64)
             if (entry_col(ent, row, k, V) >= 0)
-                l += entry_loss(ent, entry_val(ent, row, k), zk[row * ent.K + k], s, c, tm, tsum, m, S);
+                l += entry_loss(ent, entry_val(ent, row, k), zk[row * ent.K + k], s, c, tm, tsum, m, S, lg2(S));
     l = wave_sum(l);
     if (lane != 0) return;
     float pr;
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
         float l = 0.0f;
         for (int i = t; i < (some ? ent.K : 0); i += 256)
             if (list.col[i] >= 0)
-                l += entry_loss(ent, list.val[i], i < 256 ? zk0 : zk[row * ent.K + i], s, c, tm, tsum, m, S);
+                l += entry_loss(ent, list.val[i], i < 256 ? zk0 : zk[row * ent.K + i], s, c, tm, tsum, m, S, lg2(S));
         l = wave_sum(l);
         if (lane == 0) red[5][wave] = l;
         __syncthreads();
@@ -572,11 +572,14 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
 // while the loads are under way, and every vector's exponentials are summed as
 // it arrives, so that only the gradient's own arithmetic follows the last load.
 // For that a wave takes its exponentials relative to the largest logit m of its
-// first vector instead of the row's, as 2^(z c - m c) with one rounding: a sum
-// in floating point loses nothing by it unless it overflows (a logit more than
-// 88 / s above m) or m c does; then S is no positive finite number, and the row
-// is summed again around its true maximum, the products taken after the
-// difference.
+// first vector instead of the row's, as 2^(z c - mc) with one rounding, where mc
+// is m c rounded.  That rounding grows with |m| and differs from wave to wave,
+// so whatever meets these sums knows it: the waves are joined by 2^(mc - mc'),
+// the gradient's exponentials take the same mc, and the loss, which needs log2 S
+// relative to m itself, subtracts m c - mc.  Such a sum loses nothing unless it
+// overflows (a logit more than 88 / s above m) or m c does; then S is no
+// positive finite number, and the row is summed again around its true maximum,
+// the products taken after the difference.
 //
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's
 // gradient is computed its registers take the next row's vector, so that the
@@ -710,11 +713,12 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
         }
         __syncthreads();
         m = top(1);
-        const float f = lane < NW ? ex2((red[1][lane] - m) * c) : 0.0f;
+        const float f = lane < NW ? ex2(red[1][lane] * c - m * c) : 0.0f;   // products rounded as the waves' own
         S = wave_sum(lane < NW ? red[2][lane] * f : 0.0f);
         R = wave_sum(lane < NW ? red[3][lane] * f : 0.0f);
         tsum = total(4);
         const bool near = S >= 0x1p-60f && S < 0x1p100f;
+        const float off = near ? __builtin_fmaf(m, c, -(m * c)) : 0.0f;
         if (!near) {                         // uniform: around the row's own maximum
             m = t < ntail ? tails[t] : -__builtin_inff();
 #pragma unroll
@@ -751,7 +755,7 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
 #pragma unroll 1
         for (int i = t; i < (q.some ? ent.K : 0); i += NT) {
             const int col = list.col[i];
-            if (col >= 0) l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S);
+            if (col >= 0) l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S, lg2(S) - off);
         }
         l = wave_sum(l);
         if ((t & 63) == 0) red[5][wave] = l;
