@@ -654,8 +654,9 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
  *
  * tq_topk_distill writes the loss and what the backward pass needs: stats
  * [rows, 2] = the row's largest logit and the sum of exp(s (z - it)), rest_sum
- * [rows] the same sum outside the entries (only with teacher_lse); both may be
- * NULL.  tq_topk_distill_backward turns dloss [rows] (NULL: ones) into dlogits
+ * [rows, 2] the same pair over the columns outside the entries (only with
+ * teacher_lse; relative to their own largest, so that q_r of a confident student
+ * or of a masked vocabulary does not vanish); both may be NULL.  tq_topk_distill_backward turns dloss [rows] (NULL: ones) into dlogits
  * (logits' type, row stride d_row_stride).  tq_topk_distill_grad does both in
  * one call, for a program that knows dloss beforehand: where a workgroup can
  * hold a row, the logits are read once.  dlogits may be the logits themselves

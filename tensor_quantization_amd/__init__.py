@@ -1015,7 +1015,7 @@ def tq_topk_distill(logits, top_idx, top_val, temperature=1.0, teacher_lse=None)
     head, kept, rows, vocab, dev = _distill_args(logits, top_idx, top_val, teacher_lse)
     ws, nws = _distill_workspace(dev, rows, vocab, head[9])
     loss, stats = _f32(dev, rows), _f32(dev, rows, 2)
-    rest = torch.empty_like(loss) if teacher_lse is not None else None
+    rest = torch.empty_like(stats) if teacher_lse is not None else None
     _call("tq_topk_distill", *head, temperature, loss.data_ptr(), stats.data_ptr(), _ptr(rest), _ptr(ws), nws,
           _stream(dev))
     return loss, stats, rest
@@ -1030,8 +1030,11 @@ def tq_topk_distill_backward(logits, top_idx, top_val, stats, dloss=None, temper
         raise ValueError("stats must be tq_topk_distill's [rows, 2]")
     if (teacher_lse is None) != (rest_sum is None):
         raise ValueError("rest_sum goes with teacher_lse")
+    if rest_sum is not None and (rest_sum.shape != (rows, 2) or rest_sum.dtype != torch.float32
+                                 or rest_sum.device != dev):
+        raise ValueError("rest_sum must be tq_topk_distill's [rows, 2]")
     stats = stats.contiguous()
-    rest_sum = None if rest_sum is None else _row_vector(rest_sum, rows, logits, "rest_sum")
+    rest_sum = None if rest_sum is None else rest_sum.contiguous()
     dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
     dz = torch.empty_like(kept[0], memory_format=torch.contiguous_format)
     _call("tq_topk_distill_backward", *head, temperature, stats.data_ptr(), _ptr(rest_sum), _ptr(dloss),

@@ -12,13 +12,20 @@
 //   A row without entries has loss 0 and gradient 0.
 //
 // q_r is summed over the entries' complement, not taken as 1 - sum q, which
-// would lose it where the student agrees with the teacher.  To know which
+// would lose it where the student agrees with the teacher, and relative to the
+// complement's own largest logit m_r: relative to the row's it would vanish
+// where every other logit lies 87 T below an entry's (a confident student, a
+// mask of large finite values).  So the row's sum S, relative to its largest
+// logit m, is joined from the complement's R and the entries' own, and
+//   log q_r = s (m_r - m) + log R - log S,
+//   dL/dz_j = s e_j (Z 2^((m_r - m) c) / S - p_r / R), e_j = 2^((z_j - m_r) c)
+// outside the entries (c = s log2 e).  To know which
 // columns are entries, a workgroup keeps one bit per column of its part of the
 // row in LDS; the gradient finds an entry's probability by the rank of its bit
 // (a prefix count per 32-column word, then the bits below it), so each element
 // is written once, in order, with no scatter afterwards.
 //
-// All sums are binary32, relative to the row's largest logit.  Every kernel is
+// All sums are binary32, relative to the largest of what they add.  Every kernel is
 // bound by HBM: the loss reads the logits once, the gradient reads them and
 // writes as much; in one call the row is held in registers between the two.
 #include "tq_llm.h"
@@ -64,17 +71,19 @@ __device__ __forceinline__ void load_entries(EntryList& l, const Entries& e, int
 }
 
 // 2^x by the exponential unit (x of a probability, at most 0 up to rounding;
-// results below 2^-126 are flushed, far under any sum they join).
+// results below 2^-126 are flushed, far under any sum they join: each sum's
+// largest term is about 1).
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
 // The logit that a row's exponentials are taken relative to.
 __device__ __forceinline__ float base_of(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
-// What a row's gradient needs: dL/dz_j = e_j (in or out) - sg p_j with
-// e_j = 2^((z_j - m) c), the sums' reciprocals folded into `in` and `out`.
+// What a row's gradient needs: dL/dz_j = e_j in - sg p_j at entries, e_j out
+// elsewhere, e_j the exponential relative to the row's and to the complement's
+// base; the sums' reciprocals are folded into `in` and `out`.
 struct Coef {
-    float m, in, out, sg, tm, ti;
+    float in, out, sg, tm, ti;
     bool some;
 };
 
@@ -83,14 +92,14 @@ __device__ __forceinline__ float entry_p(const Entries& e, const Coef& q, float 
     return e.tlse ? ex2((t * s - q.tm) * LOG2E) : ex2((t - q.tm) * c) * q.ti;
 }
 
-// The coefficients from the student's sums S, R (relative to m), the
-// teacher's base tm and sum (`tsum`: of 2^((t - tm) c) without, of p with the
-// normaliser) and whether the row has entries at all.
-__device__ __forceinline__ Coef make_coef(bool rest, bool some, float m, float S, float R, float tm, float tsum,
+// The coefficients from the student's sums S and R, the ratio of their bases
+// up = 2^((m_r - m) c) (without the normaliser 1, and R unused), the teacher's base
+// tm and sum (`tsum`: of 2^((t - tm) c) without, of p with the normaliser) and
+// whether the row has entries at all.
+__device__ __forceinline__ Coef make_coef(bool rest, bool some, float S, float R, float up, float tm, float tsum,
                                           float s, float g, float* p_rest)
 {
     Coef q;
-    q.m = base_of(m);
     q.some = some;
     q.sg = s * g;
     q.tm = tm;
@@ -99,9 +108,7 @@ __device__ __forceinline__ Coef make_coef(bool rest, bool some, float m, float S
     const float Z = rest ? tsum + pr : 1.0f;
     const float is = S == 0.0f ? 0.0f : 1.0f / S;    // a row of -inf logits has no gradient
     q.in = q.sg * Z * is;
-    q.out = pr > 0.0f && R > 0.0f ? q.sg * (Z * is - pr / R) : q.in;
-    // it multiplies exponentials that may be 0
-    if (__builtin_isinf(q.out)) q.out = __builtin_copysignf(3.4028234664e38f, q.out);
+    q.out = rest ? q.sg * (Z * is * up - (R == 0.0f ? 0.0f : pr / R)) : q.in;    // R = 0: no such exponential
     if (S == 0.0f) {
         q.out = 0.0f;
         q.sg = 0.0f;
@@ -120,10 +127,30 @@ __device__ __forceinline__ float entry_loss(const Entries& e, float t, float z, 
     if (S == 0.0f) return __builtin_inff();
     return p * (logp - ((z - base_of(m)) * s - lgS * LN2));
 }
-__device__ __forceinline__ float rest_loss(float pr, float R, float S)
+// The rest's, `above` = s (m_r - m).
+__device__ __forceinline__ float rest_loss(float pr, float R, float S, float above)
 {
     if (pr == 0.0f) return 0.0f;
-    return S == 0.0f ? __builtin_inff() : pr * LN2 * (lg2(pr) - (lg2(R) - lg2(S)));
+    return S == 0.0f ? __builtin_inff() : pr * ((lg2(pr) - (lg2(R) - lg2(S))) * LN2 - above);
+}
+
+// The sum R relative to its largest term's logit m, and b's joined to it.
+struct Part {
+    float m, sum;
+};
+__device__ __forceinline__ float part_at(const Part& a, float base, float c)
+{
+    return a.sum * ex2((a.m - base) * c);    // m = -inf: 0
+}
+__device__ __forceinline__ Part join(const Part& a, const Part& b, float c)
+{
+    const float m = __builtin_fmaxf(a.m, b.m), base = base_of(m);
+    return Part{m, part_at(a, base, c) + part_at(b, base, c)};
+}
+__device__ __forceinline__ Part wave_join(const Part& a, float c)
+{
+    const float m = wave_max(a.m);
+    return Part{m, wave_sum(part_at(a, base_of(m), c))};
 }
 
 // ------------------------------------------------------------ entry columns
@@ -227,26 +254,27 @@ __device__ __forceinline__ void marks_fill(Marks<NT, WORDS>& k, const EntryList&
     }
 }
 
-// The gradient of eight elements, x(z) the exponential.  Entries are few: the
-// loop over their bits is rolled, and picks its element by selects.
-template <int NT, int WORDS, class X>
-__device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, int at, float v[8], X x)
+// The gradient of eight elements, out(z) and in(z) the exponentials outside and
+// at entries.  Entries are few: the loop over their bits is rolled, and picks its
+// element by selects.
+template <int NT, int WORDS, class X, class Y>
+__device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, int at, float v[8], X out, Y in)
 {
     uint32_t m = marks8(k, at);
-    float e[8];
+    float z[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        e[i] = x(v[i]);
-        v[i] = e[i] * q.out;
+        z[i] = v[i];
+        v[i] = out(v[i]) * q.out;
     }
 #pragma unroll 1
     while (m) {
         const int b = __ffs(m) - 1;
         m &= m - 1;
-        float g = e[0];
+        float g = z[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) g = b == i ? e[i] : g;
-        g = g * q.in - k.value[rank_of(k, at + b)];
+        for (int i = 1; i < 8; ++i) g = b == i ? z[i] : g;
+        g = in(g) * q.in - k.value[rank_of(k, at + b)];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = b == i ? g : v[i];
     }
@@ -254,20 +282,22 @@ __device__ __forceinline__ void grad8(const Marks<NT, WORDS>& k, const Coef& q, 
 
 // --------------------------------------------------------------- statistics
 // k_distill_stats: a workgroup per row and part of the row (`len` columns, at
-// most CH): the part's largest logit m, the sum of 2^((z - m) c) over all its
-// columns and over those that are no entries (only with REST), and the logits
-// at its entries, zk [rows, K] (for the loss, which may be taken after the gradient
-// has overwritten the logits).  A thread keeps its own running maximum and
-// sums, rescaled when a vector of eight exceeds it, so a part is one pass with
-// no barrier before the end.  Bound by HBM: [512, 32000] f32 12.9 us (5.1 TB/s).
+// most CH): the largest logit m of the part's columns and the sum of 2^((z - m) c)
+// over them, with REST one pair over the columns that are no entries and one over
+// those that are, and the logits at its entries, zk [rows, K] (for the loss,
+// which may be taken after the gradient has overwritten the logits).  A thread
+// keeps its own running maximum and sum, rescaled when a vector of eight exceeds
+// it, so a part is one pass with no barrier before the end; the entries' pair
+// comes from zk.  Bound by HBM: [512, 32000] f32 12.9 us (5.1 TB/s).
 template <int FT, bool REST, int CH>
 __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ z, int64_t ldz, int V, int parts,
-                                                       int len, Entries ent, float c, float* __restrict__ part,
+                                                       int len, Entries ent, float c, float4* __restrict__ part,
                                                        float* __restrict__ zk)
 {
     constexpr int U = 4;
     __shared__ uint32_t bits[REST ? CH / 32 + 1 : 1];
-    __shared__ float red[4][3];
+    __shared__ Part red[4][2];
+    __shared__ int twice;
     const int t = threadIdx.x;
     const int64_t row = blockIdx.x / (unsigned)parts;
     const int p = (int)(blockIdx.x % (unsigned)parts), c0 = p * len;
@@ -275,37 +305,47 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
     const int64_t base = row * ldz + c0;
     if constexpr (REST) {
         for (int i = t; i < CH / 32 + 1; i += 256) bits[i] = 0;
+        if (t == 0) twice = 0;
         __syncthreads();
     }
-    for (int k = t; k < ent.K; k += 256) {
+    constexpr int KT = DT_K / 256;
+    float ze[KT];                        // the logits at this thread's entries t, t + 256, ...
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+        ze[i] = -__builtin_inff();
+        const int k = t + 256 * i;
+        if (k >= ent.K) continue;
         const int all = entry_col(ent, row, k, V), col = all - c0;
         if (all >= 0 && col >= 0 && col < n) {
-            zk[row * ent.K + k] = load1<FT>(z, base + col);
-            if constexpr (REST) atomicOr(&bits[col >> 5], 1u << (col & 31));
+            ze[i] = load1<FT>(z, base + col);
+            zk[row * ent.K + k] = ze[i];
+            if constexpr (REST)
+                if (atomicOr(&bits[col >> 5], 1u << (col & 31)) >> (col & 31) & 1) twice = 1;
         }
     }
     if constexpr (REST) __syncthreads();
-    float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
+    Part out = {-__builtin_inff(), 0.0f}, in = out;
+    // adds a vector's own elements, with REST those that are no entries
     auto add = [&](float v[8], int lo, uint32_t mask) {
+        if constexpr (REST) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = mask >> i & 1 ? -__builtin_inff() : v[i];
+        }
         float top = v[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, v[i]);
-        if (top > m) {
-            const float f = ex2((m - top) * c);   // m = -inf: 0
-            S *= f;
-            R *= f;
-            m = top;
+        if (top > out.m) {
+            out.sum *= ex2((out.m - top) * c);    // m = -inf: 0
+            out.m = top;
         }
-        const float b = base_of(m);
-        float sum = 0.0f, in = 0.0f;
+        const float b = base_of(out.m);
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = ex2((v[i] - b) * c), y = i >= lo ? x : 0.0f;
-            sum += y;
-            if constexpr (REST) in += mask >> i & 1 ? 0.0f : y;
+            const float x = ex2((v[i] - b) * c);
+            sum += i >= lo ? x : 0.0f;
         }
-        S += sum;
-        if constexpr (REST) R += in;
+        out.sum += sum;
     };
     if (n >= 8) {
         for (int v0 = t; v0 < nvec; v0 += 256 * U) {
@@ -325,7 +365,7 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
                 if constexpr (REST) {
                     const uint8_t* b = reinterpret_cast<const uint8_t*>(bits);
                     mask = b[at[u].at >> 3];
-                    if (at[u].at & 7) mask = (mask | (uint32_t)b[(at[u].at >> 3) + 1] << 8) >> (at[u].at & 7);
+                    if (at[u].at & 7) mask = (mask | (uint32_t)b[(at[u].at >> 3) + 1] << 8) >> (at[u].at & 7) & 0xffu;
                 }
                 add(v, at[u].lo, mask);
             }
@@ -338,40 +378,43 @@ __global__ __launch_bounds__(256) void k_distill_stats(const void* __restrict__ 
         // the seven other places hold nothing: their exponentials are zeros
         add(v, 0, REST ? bits[0] >> t & 1 : 0);
     }
-    const float mw = wave_max(m);
-    {
-        const float f = ex2((m - base_of(mw)) * c);
-        S = wave_sum(S * f);             // f = 0 where the lane met nothing above -inf
-        R = wave_sum(R * f);
+    if constexpr (REST) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const int k = t + 256 * i;
+            bool count = k < ent.K;
+            if (twice && count)          // a column counts once, by the first of its entries
+                for (int j = 0; j < k; ++j) count = count && entry_col(ent, row, j, V) != entry_col(ent, row, k, V);
+            if (count) in = join(in, Part{ze[i], 1.0f}, c);
+        }
+        in = wave_join(in, c);
     }
+    out = wave_join(out, c);
     if ((t & 63) == 0) {
-        red[t >> 6][0] = mw;
-        red[t >> 6][1] = S;
-        red[t >> 6][2] = R;
+        red[t >> 6][0] = out;
+        red[t >> 6][1] = in;
     }
     __syncthreads();
     if (t != 0) return;
-    m = __builtin_fmaxf(__builtin_fmaxf(red[0][0], red[1][0]), __builtin_fmaxf(red[2][0], red[3][0]));
-    S = 0.0f;
-    R = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = ex2((red[w][0] - base_of(m)) * c);
-        S += red[w][1] * f;
-        R += red[w][2] * f;
+    for (int o = 0; o < 2; ++o) {
+        if (o && !REST) continue;
+        Part& all = o ? in : out;
+        const float m = __builtin_fmaxf(__builtin_fmaxf(red[0][o].m, red[1][o].m),
+                                        __builtin_fmaxf(red[2][o].m, red[3][o].m));
+        all = Part{m, 0.0f};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) all.sum += part_at(red[w][o], base_of(m), c);
     }
-    float* to = part + ((int64_t)row * parts + p) * 3;
-    to[0] = m;
-    to[1] = S;
-    to[2] = R;
+    part[row * parts + p] = make_float4(out.m, out.sum, in.m, in.sum);
 }
 
 // k_distill_rows: a wave per row joins the row's parts and writes the loss and
 // the row's statistics: stats[row] = {largest logit, sum of exp(s (z - it))},
-// rest_sum[row] the same sum over the columns outside the entries.  A launch's
+// rest_sum[row] the same pair over the columns outside the entries.  A launch's
 // latency (4.3 us), whatever the rows.
 __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entries ent, float s, float c,
-                                                      const float* __restrict__ part, const float* __restrict__ zk,
+                                                      const float4* __restrict__ part, const float* __restrict__ zk,
                                                       int parts, float* __restrict__ loss, float* __restrict__ stats,
                                                       float* __restrict__ rest_sum)
 {
@@ -379,9 +422,12 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
     const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (row >= rows) return;
     const bool rest = ent.tlse != nullptr;
-    float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
-    const float* from = part + row * parts * 3;
-    for (int i = lane; i < parts; i += 64) m = __builtin_fmaxf(m, from[3 * i]);
+    Part out = {-__builtin_inff(), 0.0f}, in = out;
+    for (int i = lane; i < parts; i += 64) {
+        const float4 of = part[row * parts + i];
+        out = join(out, Part{of.x, of.y}, c);
+        in = join(in, Part{of.z, of.w}, c);
+    }
     // the teacher
     float tm = -__builtin_inff(), tsum = 0.0f;
     bool some = false;
@@ -390,15 +436,10 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
             some = true;
             tm = __builtin_fmaxf(tm, entry_val(ent, row, k));
         }
-    m = wave_max(m);
-    const float b = base_of(m);
-    for (int i = lane; i < parts; i += 64) {
-        const float f = ex2((from[3 * i] - b) * c);
-        S += from[3 * i + 1] * f;
-        R += from[3 * i + 2] * f;
-    }
-    S = wave_sum(S);
-    R = wave_sum(R);
+    out = wave_join(out, c);
+    in = wave_join(in, c);
+    const Part all = join(out, in, c);
+    const float m = all.m, S = all.sum, R = out.sum;
     some = __any(some);
     tm = rest ? ent.tlse[row] : base_of(wave_max(tm));
     for (int k = lane; k < ent.K; k += 64)
@@ -416,13 +457,16 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
     l = wave_sum(l);
     if (lane != 0) return;
     float pr;
-    make_coef(rest, some, m, S, R, tm, tsum, s, 1.0f, &pr);
-    loss[row] = some ? l + rest_loss(pr, R, S) : 0.0f;
+    make_coef(rest, some, S, R, 1.0f, tm, tsum, s, 1.0f, &pr);
+    loss[row] = some ? l + rest_loss(pr, R, S, (out.m - base_of(m)) * s) : 0.0f;
     if (stats) {
         stats[2 * row] = m;
         stats[2 * row + 1] = S;
     }
-    if (rest_sum) rest_sum[row] = R;
+    if (rest_sum) {
+        rest_sum[2 * row] = out.m;
+        rest_sum[2 * row + 1] = R;
+    }
 }
 
 // k_distill_grad: a workgroup per row and part of the row.  Every workgroup
@@ -434,7 +478,7 @@ __global__ __launch_bounds__(256) void k_distill_rows(int64_t rows, int V, Entri
 // back).  Bound by HBM: [512, 32000] f32 23.4 us (5.6 TB/s).
 template <int FT, int CH, bool FROM_PARTS>
 __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz, int V, int parts, int len,
-                                                      Entries ent, float s, float c, const float* __restrict__ part,
+                                                      Entries ent, float s, float c, const float4* __restrict__ part,
                                                       const float* __restrict__ zk, const float* __restrict__ stats,
                                                       const float* __restrict__ rest_sum,
                                                       const float* __restrict__ dloss, float* __restrict__ loss,
@@ -443,7 +487,7 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     constexpr int U = 2;
     __shared__ Marks<256, CH / 32 + 1> k;
     __shared__ EntryList list;
-    __shared__ float red[6][4];
+    __shared__ float red[7][4];
     __shared__ int any;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int64_t row = blockIdx.x / (unsigned)parts;
@@ -463,21 +507,16 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     marks_clear(k);
     load_entries<256>(list, ent, row, V);
     const float lse = rest ? ent.tlse[row] : 0.0f, g = dloss ? dloss[row] : 1.0f;
-    float m = -__builtin_inff(), S = 0.0f, R = 0.0f;
+    Part out = {-__builtin_inff(), 0.0f}, in = out, all = out;   // columns outside the entries, entries, the row
     if constexpr (FROM_PARTS) {
-        const float* of = part + row * parts * 3;
-        for (int i = t; i < parts; i += 256) {   // this thread's parts, relative to their largest logit
-            const float pm = of[3 * i], ps = of[3 * i + 1], pr = of[3 * i + 2];
-            const float top = __builtin_fmaxf(m, pm), b = base_of(top);
-            const float f = ex2((m - b) * c), pf = ex2((pm - b) * c);
-            S = S * f + ps * pf;
-            R = R * f + pr * pf;
-            m = top;
+        for (int i = t; i < parts; i += 256) {
+            const float4 of = part[row * parts + i];
+            out = join(out, Part{of.x, of.y}, c);
+            in = join(in, Part{of.z, of.w}, c);
         }
     } else {
-        m = stats[2 * row];
-        S = stats[2 * row + 1];
-        R = rest ? rest_sum[row] : 0.0f;
+        all = Part{stats[2 * row], stats[2 * row + 1]};
+        out = rest ? Part{rest_sum[2 * row], rest_sum[2 * row + 1]} : all;
     }
     const float zk0 = FROM_PARTS && p == 0 && t < ent.K ? zk[row * ent.K + t] : 0.0f;
     __syncthreads();
@@ -490,50 +529,54 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
         if (col >= 0 && col < n) mark(k, col);
     }
     auto four = [&](int i) { return lane < 4 ? red[i][lane] : 0.0f; };
+    auto top = [&](int i) { return wave_max(lane < 4 ? red[i][lane] : -__builtin_inff()); };
     tm = wave_max(tm);
-    const float mt = m;
-    if constexpr (FROM_PARTS) m = wave_max(m);
-    if (lane == 0) {
-        red[0][wave] = tm;
-        red[1][wave] = m;
+    if constexpr (FROM_PARTS) {
+        const float mo = wave_max(out.m), mi = wave_max(in.m);
+        if (lane == 0) {
+            red[1][wave] = mo;
+            red[6][wave] = mi;
+        }
     }
+    if (lane == 0) red[0][wave] = tm;
     __syncthreads();
-    tm = rest ? lse : base_of(wave_max(lane < 4 ? red[0][lane] : -__builtin_inff()));
+    tm = rest ? lse : base_of(top(0));
     float tsum = 0.0f;
     if constexpr (FROM_PARTS) {
-        m = wave_max(lane < 4 ? red[1][lane] : -__builtin_inff());
-        const float f = ex2((mt - base_of(m)) * c);
-        S = wave_sum(S * f);
-        R = wave_sum(R * f);
+        const float mo = top(1), mi = top(6);
+        out = Part{mo, wave_sum(part_at(out, base_of(mo), c))};
+        in = Part{mi, wave_sum(part_at(in, base_of(mi), c))};
     }
     for (int i = t; i < ent.K; i += 256)
         if (list.col[i] >= 0) tsum += rest ? ex2((list.val[i] * s - tm) * LOG2E) : ex2((list.val[i] - tm) * c);
     tsum = wave_sum(tsum);
     if (lane == 0) {
         red[2][wave] = tsum;
-        red[3][wave] = S;
-        red[4][wave] = R;
+        red[3][wave] = out.sum;
+        red[4][wave] = in.sum;
     }
     marks_count(k);                      // its barrier also publishes the sums
     __syncthreads();
     tsum = wave_sum(four(2));
     if constexpr (FROM_PARTS) {
-        S = wave_sum(four(3));
-        R = wave_sum(four(4));
+        out.sum = wave_sum(four(3));
+        in.sum = wave_sum(four(4));
+        all = join(out, in, c);
     }
+    const float S = all.sum, R = out.sum, mi = base_of(all.m), mo = base_of(out.m);
     const bool some = any && (rest || tsum != 0.0f);
     float pr;
-    const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, g, &pr);
+    const Coef q = make_coef(rest, some, S, R, rest ? ex2((out.m - mi) * c) : 1.0f, tm, tsum, s, g, &pr);
     if (FROM_PARTS && p == 0) {          // uniform
         float l = 0.0f;
         for (int i = t; i < (some ? ent.K : 0); i += 256)
             if (list.col[i] >= 0)
-                l += entry_loss(ent, list.val[i], i < 256 ? zk0 : zk[row * ent.K + i], s, c, tm, tsum, m, S, lg2(S));
+                l += entry_loss(ent, list.val[i], i < 256 ? zk0 : zk[row * ent.K + i], s, c, tm, tsum, all.m, S, lg2(S));
         l = wave_sum(l);
         if (lane == 0) red[5][wave] = l;
         __syncthreads();
         l = wave_sum(four(5));
-        if (t == 0) loss[row] = some ? l + rest_loss(pr, R, S) : 0.0f;
+        if (t == 0) loss[row] = some ? l + rest_loss(pr, R, S, (out.m - mi) * s) : 0.0f;
     }
     if (!some) {                         // uniform: no entries, no gradient
         for (int j = t; j < n; j += 256) store1<FT>(dz, to + j, 0.0f);
@@ -541,11 +584,12 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
     }
     marks_fill(k, list, ent, q, c0, n, s, c);
     __syncthreads();
-    auto x = [&](float v) { return ex2((v - q.m) * c); };
+    auto xo = [&](float v) { return ex2((v - mo) * c); };
+    auto xi = [&](float v) { return ex2((v - mi) * c); };
     if (n < 8) {
         if (t < n) {
             float v[8] = {load1<FT>(z, from + t), 0, 0, 0, 0, 0, 0, 0};
-            grad8(k, q, t, v, x);
+            grad8(k, q, t, v, xo, xi);
             store1<FT>(dz, to + t, v[0]);
         }
         return;
@@ -561,7 +605,7 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
             if (at.lo == 8) continue;
             float v[8];
             widen8<FT>(now[u], v);
-            grad8(k, q, at.at, v, x);
+            grad8(k, q, at.at, v, xo, xi);
             store8_own<FT>(dz, to, at, v);
         }
     }
@@ -571,15 +615,16 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
 // row (8 <= V <= 8 NT W) in registers in its own type.  The entries are marked
 // while the loads are under way, and every vector's exponentials are summed as
 // it arrives, so that only the gradient's own arithmetic follows the last load.
-// For that a wave takes its exponentials relative to the largest logit m of its
-// first vector instead of the row's, as 2^(z c - mc) with one rounding, where mc
-// is m c rounded.  That rounding grows with |m| and differs from wave to wave,
-// so whatever meets these sums knows it: the waves are joined by 2^(mc - mc'),
-// the gradient's exponentials take the same mc, and the loss, which needs log2 S
-// relative to m itself, subtracts m c - mc.  Such a sum loses nothing unless it
-// overflows (a logit more than 88 / s above m) or m c does; then S is no
-// positive finite number, and the row is summed again around its true maximum,
-// the products taken after the difference.
+// For that a wave takes its exponentials relative to the largest logit m outside
+// the entries in its first vector instead of the row's, as 2^(z c - mc) with one
+// rounding, where mc is m c rounded.  That rounding grows with |m| and differs
+// from wave to wave, so whatever meets these sums knows it: the waves are joined
+// by 2^(mc - mc'), the gradient's exponentials take the same mc, and the loss,
+// which needs log2 S relative to m itself, subtracts m c - mc.  Such sums lose
+// nothing unless they overflow (a logit more than 69 / s above m), m c does, or
+// the complement's comes out below its largest term's 1 (no logit above -inf where
+// a wave looks first); then the complement and the entries are each summed again
+// around their own maximum, the products taken after the difference.
 //
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's
 // gradient is computed its registers take the next row's vector, so that the
@@ -591,15 +636,18 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
 // kernel without its stores takes 406).  Two passes with the parts' kernels
 // take 640, a workgroup per row without the next row's loads 516, temporal
 // stores 506 and temporal loads 496.
+//
+// 16-bit rows of up to 8192 stand eight to a CU, as the launch counts on, where
+// the registers are held to eight waves per SIMD (4096 rows of 8000 42.4 -> 38.8).
 template <int FT, int NT, int W>
-__global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz, uint32_t rows, int V, Entries ent,
+__global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_distill_held(const void* z, int64_t ldz, uint32_t rows, int V, Entries ent,
                                                      float s, float c,
                                                      const float* __restrict__ dloss, float* __restrict__ loss,
                                                      void* dz, int64_t lddz)
 {
     constexpr int NW = NT / 64, ES = FT == F32 ? 4 : 2;
     __shared__ Marks<NT, NT * W / 4 + 1> k;
-    __shared__ float red[6][NW], tails[8];
+    __shared__ float red[7][NW], tails[8];
     __shared__ EntryList list;
     __shared__ int any;
     const bool rest = ent.tlse != nullptr;
@@ -662,11 +710,14 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
                 tsum += rest ? ex2((x * s - tm) * LOG2E) : ex2((x - tm) * c);
             }
 
+        // the entries among the eight columns of vector v (or the last); none without the normaliser
+        auto entries8 = [&](int v) { return rest ? marks8(k, 8 * (v < nvec ? v : nvec - 1)) : 0u; };
+        const bool tail_in = rest && t < ntail && (marks8(k, 8 * nvec) >> t & 1);
         float m, S, R;
-        // the sums over this thread's vectors of x(z) and, in R, of those off the entries
+        // over this thread's vectors x(z) added up in S and, with the normaliser, what lies outside the entries in R
         auto sum = [&](auto x) {
             S = t < ntail ? x(tails[t]) : 0.0f;
-            R = rest && t < ntail && !(marks8(k, 8 * nvec) >> t & 1) ? S : 0.0f;
+            R = rest && !tail_in ? S : 0.0f;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const int at = afresh(afresh(t) + w * NT);
@@ -695,9 +746,10 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
         {
             float v[8];
             widen8<FT>(raw[0], v);
-            m = v[0];
+            const uint32_t mask = entries8(t);
+            m = -__builtin_inff();
 #pragma unroll
-            for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+            for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, mask >> i & 1 ? -__builtin_inff() : v[i]);
             m = base_of(wave_max(m));
             const float mc = m * c;
             sum([&](float v) { return ex2(__builtin_fmaf(v, c, -mc)); });
@@ -717,56 +769,90 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
         S = wave_sum(lane < NW ? red[2][lane] * f : 0.0f);
         R = wave_sum(lane < NW ? red[3][lane] * f : 0.0f);
         tsum = total(4);
-        const bool near = S >= 0x1p-60f && S < 0x1p100f;
+        const bool near = (rest ? R : S) >= 0.5f && S < 0x1p100f;
         const float off = near ? __builtin_fmaf(m, c, -(m * c)) : 0.0f;
-        if (!near) {                         // uniform: around the row's own maximum
-            m = t < ntail ? tails[t] : -__builtin_inff();
+        float mr = m;                        // the complement's base
+        if (!near) {                         // uniform: the complement and the entries around their own maxima
+            // f(logit) for this thread's entries, a column by the first of its entries
+            auto columns = [&](auto f) {
+#pragma unroll 1
+                for (int i = t; i < (rest ? ent.K : 0); i += NT) {
+                    bool first = list.col[i] >= 0;
+                    if (k.twice)
+#pragma unroll 1
+                        for (int j = 0; j < i; ++j) first = first && list.col[j] != list.col[i];
+                    if (first) f(load1<FT>(from, list.col[i]));
+                }
+            };
+            float me = -__builtin_inff(), E = 0.0f;
+            columns([&](float z) { me = __builtin_fmaxf(me, z); });
+            mr = t < ntail && !tail_in ? tails[t] : -__builtin_inff();
 #pragma unroll
             for (int w = 0; w < W; ++w) {    // repeated elements do not change a maximum
-                float v[8];
+                const uint32_t mask = entries8(afresh(afresh(t) + w * NT));
+                float v[8], most = -__builtin_inff();
                 keep_raw<FT>(raw[w]);
                 widen8<FT>(raw[w], v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, v[i]);
+                for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, v[i]);
+                if (mask) {
+                    most = -__builtin_inff();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) most = __builtin_fmaxf(most, mask >> i & 1 ? -__builtin_inff() : v[i]);
+                }
+                mr = __builtin_fmaxf(mr, most);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            m = wave_max(m);
-            __syncthreads();
-            if ((t & 63) == 0) red[1][wave] = m;
-            __syncthreads();
-            m = top(1);
-            const float b = base_of(m);
-            sum([&](float v) { return ex2((v - b) * c); });
-            S = wave_sum(S);
-            R = wave_sum(R);
+            mr = wave_max(mr);
+            me = wave_max(me);
             __syncthreads();
             if ((t & 63) == 0) {
-                red[2][wave] = S;
-                red[3][wave] = R;
+                red[1][wave] = mr;
+                red[6][wave] = me;
             }
             __syncthreads();
-            S = total(2);
-            R = total(3);
+            mr = top(1);
+            me = top(6);
+            const float br = base_of(mr), be = base_of(me);
+            sum([&](float v) { return ex2((v - br) * c); });
+            R = rest ? R : S;
+            columns([&](float z) { E += ex2((z - be) * c); });
+            R = wave_sum(R);
+            E = wave_sum(E);
+            __syncthreads();
+            if ((t & 63) == 0) {
+                red[2][wave] = R;
+                red[3][wave] = E;
+            }
+            __syncthreads();
+            R = total(2);
+            const Part all = join(Part{mr, R}, Part{me, total(3)}, c);
+            m = all.m;
+            S = all.sum;
         }
         if (!rest && tsum == 0.0f) some = false;
         float pr;
-        const Coef q = make_coef(rest, some, m, S, R, tm, tsum, s, dloss ? dloss[row] : 1.0f, &pr);
+        const Coef q = make_coef(rest, some, S, R, rest && !near ? ex2((mr - base_of(m)) * c) : 1.0f, tm, tsum, s,
+                                 dloss ? dloss[row] : 1.0f, &pr);
         if (q.some) marks_fill(k, list, ent, q, 0, V, s, c);
         float l = 0.0f;
 #pragma unroll 1
         for (int i = t; i < (q.some ? ent.K : 0); i += NT) {
             const int col = list.col[i];
-            if (col >= 0) l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S, lg2(S) - off);
+            if (col >= 0)
+                l += entry_loss(ent, list.val[i], load1<FT>(from, col), s, c, tm, tsum, m, S, lg2(S) - off);
         }
         l = wave_sum(l);
         if ((t & 63) == 0) red[5][wave] = l;
         __syncthreads();                     // also before the first store: dz may be z
         if (wave == 0) {
-            l = total(5) + rest_loss(pr, R, S);
+            l = total(5) + rest_loss(pr, R, S, (mr - base_of(m)) * s);
             if (t == 0) loss[row] = q.some ? l : 0.0f;
         }
-        // 2^(z c - m c) or 2^((z - m) c)
-        const float sub = near ? 0.0f : q.m, mc = near ? q.m * c : 0.0f;
-        auto x = [&](float v) { return ex2(__builtin_fmaf(v - sub, c, -mc)); };
+        // 2^(z c - mc) or 2^((z - m) c), outside the entries (z - m_r)
+        const float si = near ? 0.0f : base_of(m), so = near ? 0.0f : base_of(mr), mc = near ? m * c : 0.0f;
+        auto xo = [&](float v) { return ex2(__builtin_fmaf(v - so, c, -mc)); };
+        auto xi = [&](float v) { return ex2(__builtin_fmaf(v - si, c, -mc)); };
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const int at = afresh(afresh(t) + w * NT);
@@ -780,7 +866,7 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
             __builtin_amdgcn_sched_barrier(0);
             ahead(w);
             if (at < nvec) {
-                if (q.some) grad8(k, q, 8 * at, v, x);
+                if (q.some) grad8(k, q, 8 * at, v, xo, xi);
                 else
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
@@ -790,9 +876,9 @@ __global__ __launch_bounds__(NT) void k_distill_held(const void* z, int64_t ldz,
         }
         if (t < ntail) {
             const int at = 8 * nvec + t;
-            const float e = x(tails[t]);
             const bool entry = marks8(k, 8 * nvec) >> t & 1;
-            store1<FT>(to, at, !q.some ? 0.0f : entry ? e * q.in - k.value[rank_of(k, at)] : e * q.out);
+            store1<FT>(to, at, !q.some ? 0.0f : entry ? xi(tails[t]) * q.in - k.value[rank_of(k, at)]
+                                                      : xo(tails[t]) * q.out);
         }
     }
 }
@@ -834,7 +920,7 @@ struct Distill {
 // Workspace: the parts' statistics, then the logits at the entries.
 inline size_t distill_part_floats(int64_t rows, int64_t V)
 {
-    return 3 * (size_t)rows * (size_t)distill_split(rows, V).parts;
+    return 4 * (size_t)rows * (size_t)distill_split(rows, V).parts;
 }
 
 template <int FT>
@@ -842,20 +928,21 @@ static void stats_launch(const Distill& d, float* ws, hipStream_t st)
 {
     const Split q = distill_split(d.rows, d.V);
     const dim3 grid((unsigned)(d.rows * q.parts));
+    float4* part = reinterpret_cast<float4*>(ws);
     float* zk = ws + distill_part_floats(d.rows, d.V);
     if (d.ent.tlse)
         TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
-                                            q.parts, q.len, d.ent, d.c, ws, zk));
+                                            q.parts, q.len, d.ent, d.c, part, zk));
     else
         TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz,
-                                            d.V, q.parts, q.len, d.ent, d.c, ws, zk));
+                                            d.V, q.parts, q.len, d.ent, d.c, part, zk));
 }
 
 static void rows_launch(const Distill& d, const float* ws, float* loss, float* stats, float* rest_sum, hipStream_t st)
 {
     hipLaunchKernelGGL(k_distill_rows, dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.rows, d.V, d.ent, d.s, d.c,
-                       ws, ws + distill_part_floats(d.rows, d.V), distill_split(d.rows, d.V).parts, loss, stats,
-                       rest_sum);
+                       reinterpret_cast<const float4*>(ws), ws + distill_part_floats(d.rows, d.V),
+                       distill_split(d.rows, d.V).parts, loss, stats, rest_sum);
 }
 
 template <int FT, bool FROM_PARTS>
@@ -865,8 +952,8 @@ static void grad_launch(const Distill& d, const float* ws, const float* stats, c
     const Split q = distill_split(d.rows, d.V);
     const float* zk = FROM_PARTS ? ws + distill_part_floats(d.rows, d.V) : nullptr;
     TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV, FROM_PARTS>), dim3((unsigned)(d.rows * q.parts)),
-                                        dim3(256), 0, st, d.z, d.ldz, d.V, q.parts, q.len, d.ent, d.s, d.c, ws, zk,
-                                        stats, rest_sum, dloss, loss, dz, lddz));
+                                        dim3(256), 0, st, d.z, d.ldz, d.V, q.parts, q.len, d.ent, d.s, d.c,
+                                        reinterpret_cast<const float4*>(ws), zk, stats, rest_sum, dloss, loss, dz, lddz));
 }
 
 // Whether the joint call holds its rows in registers.  A row in registers costs
