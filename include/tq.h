@@ -602,8 +602,9 @@ tq_status tq_layer_norm_backward(const void* dy, const void* x, int x_dtype, int
                                  const float* mean, const float* rstd, void* dx, void* dweight, void* dbias,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
-/* The W8A8 product with an epilogue, for any M (single tokens included), N
- * and K <= 131071.  qx, sx, qw, sw as in tq_w8a8_linear:
+/* The W8A8 product with an epilogue, from M = 1 (single tokens) to 65535 * 128,
+ * N up to 2^27 - 16, K up to 131071, and outputs of fewer than 2^23 tiles of 256 x
+ * 256 (TQ_ERR_UNSUPPORTED beyond).  qx, sx, qw, sw as in tq_w8a8_linear:
  *   z[m][n] = ((float)sum_k qx[m][k] * qw[n][k] * sx[m]) * sw[n] + bias[n]
  *   y[m][n] = act(z[m][n]) + residual[m][n]
  * in binary32, in that order, y rounded once to y_dtype; without bias, act and
@@ -621,7 +622,8 @@ tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_
 
 /* Backward of that epilogue: dz = dy * act'(preact) (dense [M, N], all in
  * dtype) and dbias[n] = sum_m of the dz before its rounding (binary32 [N], may
- * be NULL; zeros when M is 0).  The residual's gradient is dy.  dz may be dy or
+ * be NULL; zeros when M is 0).  N up to 2^33 - 512 (TQ_ERR_UNSUPPORTED beyond).
+ * The residual's gradient is dy.  dz may be dy or
  * preact itself.  relu's slope at 0 is 0.  `workspace` (needed for dbias):
  * tq_linear_epilogue_backward_workspace_bytes(M, N) bytes, 16-byte aligned (0
  * bytes, and null, for few rows). */
@@ -630,9 +632,9 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
                                       void* dz, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Distillation against a teacher's top logits.  Student logits [rows, vocab]
- * (row stride row_stride); top_idx [rows, k] (32- or 64-bit integers:
- * idx_bits) and top_val [rows, k] (val_dtype) are the teacher's k largest
- * logits of each row, k <= 1024.  An index outside [0, vocab) (-1, say) is a
+ * (row stride row_stride), rows up to 2^31 - 1 and vocab up to 2^31 - 256;
+ * top_idx [rows, k] (32- or 64-bit integers: idx_bits) and top_val [rows, k]
+ * (val_dtype) are the teacher's k largest logits of each row, 1 <= k <= 1024.  An index outside [0, vocab) (-1, say) is a
  * padding entry and counts nowhere; a row without entries has loss 0 and
  * gradient 0, whatever its logits hold.  With s = 1 / temperature:
  *   log q_j = s z_j - log sum_i exp(s z_i)

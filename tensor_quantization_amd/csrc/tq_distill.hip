@@ -917,6 +917,22 @@ struct Distill {
     float s, c;
 };
 
+// Most workgroups per launch: a grid holds fewer than 2^32 threads.  Further rows
+// are further launches.
+constexpr int64_t DT_LAUNCH = 1 << 23;
+
+// The same for the rows from `first` on, at most `most` of them.
+static Distill rows_from(const Distill& d, int FT, int64_t first, int64_t most)
+{
+    Distill r = d;
+    r.z = forward_by(d.z, first * d.ldz * ftype_size(FT));
+    r.ent.idx = forward_by(d.ent.idx, first * d.ent.K * (d.ent.idx64 ? 8 : 4));
+    r.ent.val = forward_by(d.ent.val, first * d.ent.K * ftype_size(d.ent.val_dt));
+    r.ent.tlse = forward_by(d.ent.tlse, 4 * first);
+    r.rows = std::min(d.rows - first, most);
+    return r;
+}
+
 // Workspace: the parts' statistics, then the logits at the entries.
 inline size_t distill_part_floats(int64_t rows, int64_t V)
 {
@@ -924,36 +940,57 @@ inline size_t distill_part_floats(int64_t rows, int64_t V)
 }
 
 template <int FT>
-static void stats_launch(const Distill& d, float* ws, hipStream_t st)
+static void stats_launch(const Distill& all, float* ws, hipStream_t st)
 {
-    const Split q = distill_split(d.rows, d.V);
-    const dim3 grid((unsigned)(d.rows * q.parts));
+    const Split q = distill_split(all.rows, all.V);
     float4* part = reinterpret_cast<float4*>(ws);
-    float* zk = ws + distill_part_floats(d.rows, d.V);
-    if (d.ent.tlse)
-        TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz, d.V,
-                                            q.parts, q.len, d.ent, d.c, part, zk));
-    else
-        TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz,
-                                            d.V, q.parts, q.len, d.ent, d.c, part, zk));
+    float* zk = ws + distill_part_floats(all.rows, all.V);
+    const int64_t most = std::max<int64_t>(1, DT_LAUNCH / q.parts);
+    for (int64_t r = 0; r < all.rows; r += most) {
+        const Distill d = rows_from(all, FT, r, most);
+        const dim3 grid((unsigned)(d.rows * q.parts));
+        if (d.ent.tlse)
+            TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, true, CHV>), grid, dim3(256), 0, st, d.z, d.ldz,
+                                                d.V, q.parts, q.len, d.ent, d.c, part + r * q.parts,
+                                                zk + r * d.ent.K));
+        else
+            TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_stats<FT, false, CHV>), grid, dim3(256), 0, st, d.z, d.ldz,
+                                                d.V, q.parts, q.len, d.ent, d.c, part + r * q.parts,
+                                                zk + r * d.ent.K));
+    }
 }
 
-static void rows_launch(const Distill& d, const float* ws, float* loss, float* stats, float* rest_sum, hipStream_t st)
+static void rows_launch(const Distill& all, const float* ws, float* loss, float* stats, float* rest_sum,
+                        hipStream_t st)
 {
-    hipLaunchKernelGGL(k_distill_rows, dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.rows, d.V, d.ent, d.s, d.c,
-                       reinterpret_cast<const float4*>(ws), ws + distill_part_floats(d.rows, d.V),
-                       distill_split(d.rows, d.V).parts, loss, stats, rest_sum);
+    const int parts = distill_split(all.rows, all.V).parts;
+    const float4* part = reinterpret_cast<const float4*>(ws);
+    const float* zk = ws + distill_part_floats(all.rows, all.V);
+    for (int64_t r = 0; r < all.rows; r += DT_LAUNCH) {
+        const Distill d = rows_from(all, TQ_F32, r, DT_LAUNCH);       // the logits are not read
+        hipLaunchKernelGGL(k_distill_rows, dim3((unsigned)cdiv(d.rows, 4)), dim3(256), 0, st, d.rows, d.V, d.ent, d.s,
+                           d.c, part + r * parts, zk + r * d.ent.K, parts, loss + r, forward_by(stats, 8 * r),
+                           forward_by(rest_sum, 8 * r));
+    }
 }
 
 template <int FT, bool FROM_PARTS>
-static void grad_launch(const Distill& d, const float* ws, const float* stats, const float* rest_sum,
+static void grad_launch(const Distill& all, const float* ws, const float* stats, const float* rest_sum,
                         const float* dloss, float* loss, void* dz, int64_t lddz, hipStream_t st)
 {
-    const Split q = distill_split(d.rows, d.V);
-    const float* zk = FROM_PARTS ? ws + distill_part_floats(d.rows, d.V) : nullptr;
-    TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV, FROM_PARTS>), dim3((unsigned)(d.rows * q.parts)),
-                                        dim3(256), 0, st, d.z, d.ldz, d.V, q.parts, q.len, d.ent, d.s, d.c,
-                                        reinterpret_cast<const float4*>(ws), zk, stats, rest_sum, dloss, loss, dz, lddz));
+    const Split q = distill_split(all.rows, all.V);
+    const float4* part = reinterpret_cast<const float4*>(ws);
+    const float* zk = FROM_PARTS ? ws + distill_part_floats(all.rows, all.V) : nullptr;
+    const int64_t most = std::max<int64_t>(1, DT_LAUNCH / q.parts);
+    for (int64_t r = 0; r < all.rows; r += most) {
+        const Distill d = rows_from(all, FT, r, most);
+        TQ_CH_SWITCH(q.ch, hipLaunchKernelGGL((k_distill_grad<FT, CHV, FROM_PARTS>),
+                                            dim3((unsigned)(d.rows * q.parts)), dim3(256), 0, st, d.z, d.ldz, d.V,
+                                            q.parts, q.len, d.ent, d.s, d.c, forward_by(part, 16 * r * q.parts),
+                                            forward_by(zk, 4 * r * d.ent.K), forward_by(stats, 8 * r),
+                                            forward_by(rest_sum, 8 * r), forward_by(dloss, 4 * r),
+                                            forward_by(loss, 4 * r), forward_by(dz, r * lddz * ftype_size(FT)), lddz));
+    }
 }
 
 // Whether the joint call holds its rows in registers.  A row in registers costs
@@ -1005,8 +1042,7 @@ static tq_status distill_check(const void* logits, int dt, int64_t rows, int64_t
     if (!(temperature > 0.0f) || temperature > 3.0e38f) return TQ_ERR_INVALID;
     if (rows == 0) return TQ_OK;
     if (vocab == 0 || !logits || ldz < vocab || !idx || !val) return TQ_ERR_INVALID;
-    if (K > DT_K || vocab > 0x7fffff00 || rows > 0x7fffffff || rows * cdiv(vocab, 4096) > 0x7fffffff)
-        return TQ_ERR_UNSUPPORTED;
+    if (K > DT_K || vocab > 0x7fffff00 || rows > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
     if (!natural(logits, ftype_size(dt)) || !natural(idx, idx_bits / 8) || !natural(val, ftype_size(val_dt)) ||
         !natural(teacher_lse, 4))
         return TQ_ERR_ALIGN;

@@ -9,8 +9,6 @@
 // order of operations, and y (and z, where it is asked for) is rounded once.
 #include "tq_llm.h"
 
-#include <type_traits>
-
 namespace tq {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -1018,7 +1016,9 @@ tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_
     if (bias && !valid_ftype(bias_dtype)) return TQ_ERR_INVALID;
     if (M == 0 || N == 0) return TQ_OK;
     if (!y || !sx || !sw || (K > 0 && (!qx || !qw)) || (residual && residual_row_stride < N)) return TQ_ERR_INVALID;
-    if (K > 131071 || cdiv(M, ET) > 65535 || cdiv(N, 16) > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+    // a grid holds fewer than 2^32 threads: 512 per slice of 16 columns or per 256 x 256 tile
+    if (K > 131071 || cdiv(M, ET) > 65535 || cdiv(N, 16) > 0x7fffff || cdiv(M, 256) * cdiv(N, 256) > 0x7fffff)
+        return TQ_ERR_UNSUPPORTED;
     if (!natural(sx, TQ_F32) || !natural(sw, TQ_F32) || (bias && !natural(bias, bias_dtype)) ||
         !natural(residual, y_dtype) || !natural(y, y_dtype) || !natural(preact, y_dtype))
         return TQ_ERR_ALIGN;
@@ -1046,7 +1046,7 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
     }
     if (!dy || !preact || !dz) return TQ_ERR_INVALID;
     if (!natural(dy, dtype) || !natural(preact, dtype) || !natural(dz, dtype)) return TQ_ERR_ALIGN;
-    if (cdiv(N, 512) > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+    if (cdiv(N, 512) > 0xffffff) return TQ_ERR_UNSUPPORTED;     // 256 threads each, fewer than 2^32 in a grid
     if (dbias && M > EPI_ONE) {
         if (!workspace || workspace_bytes < tq_linear_epilogue_backward_workspace_bytes(M, N)) return TQ_ERR_INVALID;
         if (!aligned16(workspace)) return TQ_ERR_ALIGN;

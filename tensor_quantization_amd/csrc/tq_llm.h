@@ -4,6 +4,8 @@
 // at run time, and the column sums that finish a weight's or a bias's gradient.
 #pragma once
 
+#include <type_traits>
+
 #include "tq_device.h"
 #include "tq_host.h"
 
@@ -232,6 +234,14 @@ void colsum_launch(const float* part, int64_t parts, int outs, int64_t ld, int64
 // Zeros of a vector of n elements of type dt (null: nothing).
 void zero_vec_launch(void* p, int dt, int64_t n, hipStream_t st);
 inline int64_t colsum_ld(int64_t cols) { return (cols + 3) / 4 * 4; }
+
+// The address `bytes` further on; null stays null.
+template <class T>
+inline T* forward_by(T* p, int64_t bytes)
+{
+    typedef std::conditional_t<std::is_const_v<T>, const char, char> byte;
+    return p ? reinterpret_cast<T*>(reinterpret_cast<byte*>(p) + bytes) : p;
+}
 
 #define TQ_LLM_FT_SWITCH(ft, ...)                              \
     do {                                                       \

@@ -708,8 +708,13 @@ __global__ __launch_bounds__(256) void k_colsum(const float* __restrict__ part, 
 void colsum_launch(const float* part, int64_t parts, int outs, int64_t ld, int64_t cols, void* out0, void* out1,
                    int dt, hipStream_t st)
 {
-    const dim3 grid((unsigned)cdiv(cols, 32), out1 ? 2u : 1u);
-    hipLaunchKernelGGL(k_colsum, grid, dim3(256), 0, st, part, parts, outs, ld, cols, out0, out1, dt);
+    constexpr int64_t MOST = 1 << 28;    // columns per launch: 2^31 threads
+    for (int64_t c = 0; c < cols; c += MOST) {
+        const int64_t n = std::min(cols - c, MOST);
+        const dim3 grid((unsigned)cdiv(n, 32), out1 ? 2u : 1u);
+        hipLaunchKernelGGL(k_colsum, grid, dim3(256), 0, st, part + c, parts, outs, ld, n,
+                           forward_by(out0, c * ftype_size(dt)), forward_by(out1, c * ftype_size(dt)), dt);
+    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -717,6 +722,9 @@ constexpr int64_t LN_HELD = 16384;       // longest row that a workgroup holds i
 constexpr int64_t LN_BWD_HELD = 16384;   // and that of dy beside it; half as many in binary32
 constexpr int64_t LN_PARTS = 256;        // workgroups of the backward pass, one row of partials each
 constexpr int64_t LN_COL_CHUNKS = 64;    // row chunks of the column kernel of longer rows
+// Most rows per launch of the kernels that give every row its own threads, up to
+// 1024: a grid holds fewer than 2^32 threads.  Further rows are further launches.
+constexpr int64_t LN_LAUNCH = 1 << 21;
 
 // Threads and vectors per row, measured on 8192 rows (us, taken / next best):
 //   1024 bf16  64 x 2  11.0 / 13.3 (256 x 1)     4096 bf16  256 x 2  23.5 / 25.5 (512 x 1)
@@ -728,6 +736,14 @@ template <int FT, int OUT>
 static void ln_launch(const void* x, int64_t ldx, int64_t rows, int64_t cols, const void* w, const void* b, int wdt,
                       float eps, void* y, float* scale, float* mean, float* rstd, hipStream_t st)
 {
+    for (; rows > LN_LAUNCH; rows -= LN_LAUNCH) {
+        ln_launch<FT, OUT>(x, ldx, LN_LAUNCH, cols, w, b, wdt, eps, y, scale, mean, rstd, st);
+        x = forward_by(x, LN_LAUNCH * ldx * ftype_size(FT));
+        y = forward_by(y, LN_LAUNCH * cols * (OUT == OUT_Y ? ftype_size(FT) : 1));
+        scale = forward_by(scale, 4 * LN_LAUNCH);
+        mean = forward_by(mean, 4 * LN_LAUNCH);
+        rstd = forward_by(rstd, 4 * LN_LAUNCH);
+    }
 #define TQ_LN(NT, W)                                                                                              \
     hipLaunchKernelGGL((k_ln_rows<FT, NT, W, OUT>), dim3((unsigned)cdiv(rows, NT < 256 ? 256 / NT : 1)),          \
                        dim3(NT < 256 ? 256 : NT), 0, st, x, ldx, rows, cols, w, b, wdt, eps, y, scale, mean, rstd)
@@ -782,9 +798,11 @@ static void ln_bwd_launch(const void* dy, int64_t lddy, const void* x, int64_t l
             hipLaunchKernelGGL((k_ln_bwd_cols<FT>), dim3((unsigned)cdiv(cols, 512), (unsigned)parts), dim3(256), 0, st,
                                dy, lddy, x, ldx, rows, (int)cols, chunk, mean, rstd, part, ld);
         }
-        if (dx)
-            hipLaunchKernelGGL((k_ln_bwd_long<FT>), dim3((unsigned)rows), dim3(LN_LT), 0, st, dy, lddy, x, ldx,
-                               (int)cols, w, wdt, mean, rstd, dx);
+        for (int64_t r = 0; dx && r < rows; r += LN_LAUNCH)
+            hipLaunchKernelGGL((k_ln_bwd_long<FT>), dim3((unsigned)std::min(rows - r, LN_LAUNCH)), dim3(LN_LT), 0, st,
+                               forward_by(dy, r * lddy * ftype_size(FT)), lddy,
+                               forward_by(x, r * ldx * ftype_size(FT)), ldx, (int)cols, w, wdt, mean + r, rstd + r,
+                               forward_by(dx, r * cols * ftype_size(FT)));
     }
     else if (cols <= 512) TQ_LNB(64, 1, 512);
     else if (cols <= 1024) TQ_LNB(128, 1, 512);
@@ -798,18 +816,18 @@ static void ln_bwd_launch(const void* dy, int64_t lddy, const void* x, int64_t l
 
 __global__ __launch_bounds__(256) void k_zero_vec(void* __restrict__ p, int dt, int64_t n)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) store1_rt(p, dt, i, 0.0f);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += 256 * (int64_t)gridDim.x)
+        store1_rt(p, dt, i, 0.0f);
 }
 
 void zero_vec_launch(void* p, int dt, int64_t n, hipStream_t st)
 {
-    if (p && n > 0) hipLaunchKernelGGL(k_zero_vec, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, st, p, dt, n);
+    if (p && n > 0) hipLaunchKernelGGL(k_zero_vec, dim3(grid_for(n, 256)), dim3(256), 0, st, p, dt, n);
 }
 
 static bool natural(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(ftype_size(dt) - 1)) == 0; }
 
-// A workgroup per row, and columns counted in 32 bits, a slab past their end.
+// Columns are counted in 32 bits, a slab past their end.
 static bool ln_fits(int64_t rows, int64_t cols)
 {
     return rows <= 0x7fffffff && cols <= 0x7fffffff - 1024;
