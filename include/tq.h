@@ -583,7 +583,8 @@ tq_status tq_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t cols, 
 
 /* Layer norm and the per-token s8 quantizer in one pass: q [rows, cols] and
  * scale [rows] are, bit for bit, those of tq_quant_per_token (TQ_S8,
- * [-127, 127], symmetric) on tq_layer_norm's y. */
+ * [-127, 127], symmetric) on tq_layer_norm's y.  A row whose y holds a NaN gets
+ * the scale NaN, so that whatever is computed from it is NaN too. */
 tq_status tq_layer_norm_quant_per_token(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t x_row_stride,
                                         const void* weight, const void* bias, int w_dtype, float eps, int8_t* q,
                                         float* scale, float* mean, float* rstd, void* stream);

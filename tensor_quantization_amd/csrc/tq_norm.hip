@@ -38,17 +38,21 @@ __device__ __forceinline__ float row_sum(float v, float* slot)
     }
     return v;
 }
+// The largest magnitude.  Magnitudes are compared as bit patterns: a NaN's lies
+// above an infinity's, so a row that holds one has it for its maximum (a float
+// maximum would drop it).
+__device__ __forceinline__ float larger(float a, float b) { return as_f(max(as_u(a), as_u(b))); }
 template <int NT>
 __device__ __forceinline__ float row_max(float v, float* slot)
 {
-    v = wave_max(v);
+    v = team_max<64>(v);
     if constexpr (NT > 64) {
         const int t = threadIdx.x;
         if ((t & 63) == 0) slot[t >> 6] = v;
         __syncthreads();
         v = slot[0];
 #pragma unroll
-        for (int k = 1; k < NT / 64; ++k) v = __builtin_fmaxf(v, slot[k]);
+        for (int k = 1; k < NT / 64; ++k) v = larger(v, slot[k]);
     }
     return v;
 }
@@ -63,7 +67,8 @@ __device__ __forceinline__ float as_stored(float v)
 }
 
 // Symmetric s8 codes of a row: scale = amax / 127 (1 if that is 0), code =
-// clamp(rne(v / scale)), both divisions correctly rounded.
+// clamp(rne(v / scale)), both divisions correctly rounded.  A row with a NaN has
+// the scale NaN, whose codes say nothing.
 struct S8Row {
     float s, y;
     bool fast;
@@ -171,7 +176,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_rows(
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[w][i] = as_stored<FT>(v[w][i]);
-                amax = __builtin_fmaxf(amax, i >= at[w].lo ? __builtin_fabsf(v[w][i]) : 0.0f);
+                amax = larger(amax, i >= at[w].lo ? __builtin_fabsf(v[w][i]) : 0.0f);
             }
         }
     }
@@ -247,7 +252,7 @@ __global__ __launch_bounds__(LN_LT) void k_ln_long(const void* __restrict__ x, i
             values(v, at);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                amax = __builtin_fmaxf(amax, i >= at.lo ? __builtin_fabsf(as_stored<FT>(v[i])) : 0.0f);
+                amax = larger(amax, i >= at.lo ? __builtin_fabsf(as_stored<FT>(v[i])) : 0.0f);
         });
         const S8Row p = s8_row(row_max<LN_LT>(amax, slots[2]));
         if (t == 0) scale[row] = p.s;
@@ -294,7 +299,7 @@ __global__ __launch_bounds__(256) void k_ln_thin(const void* __restrict__ x, int
             store1<FT>(y, row * cols + j, v[j]);
         } else {
             v[j] = as_stored<FT>(v[j]);
-            amax = __builtin_fmaxf(amax, __builtin_fabsf(v[j]));
+            amax = larger(amax, __builtin_fabsf(v[j]));
         }
     }
     if constexpr (OUT == OUT_S8) {
