@@ -624,8 +624,9 @@ tq_status tq_w8a8_linear_epilogue(const int8_t* qx, const float* sx, const int8_
 /* Backward of that epilogue: dz = dy * act'(preact) (dense [M, N], all in
  * dtype) and dbias[n] = sum_m of the dz before its rounding (binary32 [N], may
  * be NULL; zeros when M is 0).  N up to 2^33 - 512 (TQ_ERR_UNSUPPORTED beyond).
- * The residual's gradient is dy.  dz may be dy or
- * preact itself.  relu's slope at 0 is 0.  `workspace` (needed for dbias):
+ * The residual's gradient is dy.  dz may be dy or preact itself.  relu's slope at
+ * 0 is 0, and where it is 0 so is dz, whatever dy holds; a NaN in preact gives
+ * NaN (act none does not use preact's values).  `workspace` (needed for dbias):
  * tq_linear_epilogue_backward_workspace_bytes(M, N) bytes, 16-byte aligned (0
  * bytes, and null, for few rows). */
 size_t tq_linear_epilogue_backward_workspace_bytes(int64_t M, int64_t N);

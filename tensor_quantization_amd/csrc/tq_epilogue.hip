@@ -66,7 +66,7 @@ __device__ __forceinline__ void slope8(int act, const float z[8], float d[8])
     switch (act) {
     case TQ_ACT_RELU:
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = z[i] > 0.0f ? d[i] : 0.0f;
+        for (int i = 0; i < 8; ++i) d[i] = z[i] > 0.0f ? d[i] : z[i] <= 0.0f ? 0.0f : z[i];    // a NaN stays
         break;
     case TQ_ACT_SILU:
 #pragma unroll

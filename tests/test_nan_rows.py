@@ -41,3 +41,26 @@ def test_fused_codes_of_a_nan(tq, cols, ft):
     qw = torch.randint(-127, 128, (40, cols), generator=g, dtype=torch.int64).to(torch.int8).cuda()
     y = tq.tq_w8a8_linear_epilogue(q, s, qw, torch.ones(40, device="cuda"), act="relu")
     assert torch.isnan(y[bad]).all() and torch.isfinite(y[good]).all()
+
+
+# one launch, chunks of rows, fewer than eight columns
+@pytest.mark.parametrize("M,N", [(3, 24), (200, 520), (200, 5)])
+@pytest.mark.parametrize("ft", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_slope_at_a_nan(tq, M, N, ft, act):
+    note("nan through an activation's slope", M, N, ft, act)
+    g = torch.Generator().manual_seed(M + N)
+    dy, z = (torch.randn((M, N), generator=g).to(ref.TORCH[ft]).cuda() for _ in range(2))
+    clean, _ = tq.tq_linear_epilogue_backward(dy, z, act)
+    z[1, 2] = math.nan
+    dz, db = tq.tq_linear_epilogue_backward(dy, z, act)
+    at = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    at[1, 2] = act != "none"
+    assert torch.isnan(dz[at]).all() and torch.equal(dz[~at], clean[~at])
+    assert torch.equal(torch.isnan(db), at.any(0))
+    z[1, 2], dy[1, 2] = 1.0, math.nan        # a gradient's NaN, where the slope is not 0
+    dz, db = tq.tq_linear_epilogue_backward(dy, z, act)
+    assert bool(torch.isnan(dz[1, 2])) and bool(torch.isnan(db[2]))
+    z[1, 2] = -1.0
+    dz, _ = tq.tq_linear_epilogue_backward(dy, z, act)
+    assert bool(dz[1, 2] == 0) if act == "relu" else bool(torch.isnan(dz[1, 2]))
