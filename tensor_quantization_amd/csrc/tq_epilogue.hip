@@ -827,11 +827,13 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
 // per bf16 element, bound by HBM: [8192, 11008] bf16 with gelu_tanh 101.7 us
 // (5.3 TB/s) and 4.9 us for the column sums.  A wave owns 512 columns, a workgroup's four
 // waves take a chunk of the rows in turn, U rows in flight each; their column
-// sums meet in LDS in wave order and leave as one row of partials per chunk.
+// sums meet in LDS in wave order and leave as one row of partials per chunk.  dz
+// may be dy or z: an element's output depends on that element alone and is stored
+// by the lane that owns it after its load; what a moved-back vector or a chunk's
+// last rows read besides may be new already, and is not used.
 template <int FT>
-__global__ __launch_bounds__(256) void k_epi_bwd(const void* __restrict__ dy, const void* __restrict__ z, int64_t M,
-                                                 int64_t N, int64_t chunk, int act, void* __restrict__ dz,
-                                                 float* __restrict__ part, int64_t ldp)
+__global__ __launch_bounds__(256) void k_epi_bwd(const void* dy, const void* z, int64_t M, int64_t N, int64_t chunk,
+                                                 int act, void* dz, float* __restrict__ part, int64_t ldp)
 {
     constexpr int U = 4;
     __shared__ float fold[3][8][64];
@@ -883,9 +885,9 @@ __global__ __launch_bounds__(256) void k_epi_bwd(const void* __restrict__ dy, co
 
 // Fewer than 8 columns: a thread per row and step, the columns in turn.
 template <int FT>
-__global__ __launch_bounds__(256) void k_epi_bwd_thin(const void* __restrict__ dy, const void* __restrict__ z,
-                                                      int64_t M, int64_t N, int64_t chunk, int act,
-                                                      void* __restrict__ dz, float* __restrict__ part, int64_t ldp)
+__global__ __launch_bounds__(256) void k_epi_bwd_thin(const void* dy, const void* z, int64_t M, int64_t N,
+                                                      int64_t chunk, int act, void* dz, float* __restrict__ part,
+                                                      int64_t ldp)
 {
     __shared__ float fold[4][8];
     const int t = threadIdx.x;
