@@ -1,5 +1,6 @@
 """GPU: a NaN is not lost on its way through the fused norm and quantizer, the
 product and the slope of an activation, and stays in its row."""
+
 import math
 
 import pytest
