@@ -576,7 +576,7 @@ tq_status tq_fp4_predequant_to_fp8(const uint8_t* packed, const uint8_t* block_s
  * ones, zeros) have type w_dtype; y is dense in x's type; mean and rstd
  * [rows] (binary32, each may be NULL) are what the backward pass needs.
  * eps >= 0.  rows up to 2^31 - 1, cols up to 2^31 - 1025 (TQ_ERR_UNSUPPORTED
- * beyond). */
+ * beyond).  Without rows or columns nothing is written. */
 tq_status tq_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t x_row_stride,
                         const void* weight, const void* bias, int w_dtype, float eps, void* y, float* mean,
                         float* rstd, void* stream);

@@ -813,14 +813,16 @@ def tq_fp4_linear(x, packed, block_scale, global_scale, kind="nvfp4", out_dtype=
 # ------------------------------------------------------------------ layer norm
 def _rows_of(t, name):
     """(t, rows, cols, row stride) of t viewed as [rows, cols], its leading
-    dimensions flattened; copies t only where they do not flatten."""
+    dimensions flattened; copies t only where they do not flatten.  Without
+    columns there are no rows either, as for tq_quant_per_token: no value of a
+    row's would be written."""
     if t.dtype not in FTYPE:
         raise TypeError("unsupported float dtype %s" % t.dtype)
     if not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     shape = t.shape
     if len(shape) == 2:
-        rows, cols = shape
+        rows, cols = shape if shape[1] else (0, 0)
         if t.is_contiguous():
             return t, rows, cols, cols
         if t.stride(1) == 1 and (rows <= 1 or t.stride(0) >= cols):
