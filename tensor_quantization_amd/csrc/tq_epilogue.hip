@@ -436,8 +436,9 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
     }
 }
 
-// Any part: bounds, and the value before the activation where it is asked
-// for.
+// Any part: bounds, and the value before the activation where it is asked for
+// (8192 x 11008 x 4096 with gelu_tanh and that value 366 us, 327 without: the 180 MB
+// more take 36 at a large copy's rate).
 template <int YT, int NM, int NN>
 __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, const v4i (&acc)[NM][NN],
                                            int* stage)
@@ -497,24 +498,28 @@ __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0
 // units RING ahead, and the next block's units have landed (those after it may
 // still be on their way: the wait counts loads, it does not drain them).
 //
-// 256 x 256 with 2 x 4 waves of 128 x 64: on [8192, 4096] x [11008, 4096] 314
-// us without and 333 us with bias and gelu_tanh (2350 / 2220 TOP/s; the platform
+// 256 x 256 with 2 x 4 waves of 128 x 64: on [8192, 4096] x [11008, 4096] 308-319
+// us without and 327-340 us with bias and gelu_tanh, by the card and its clock (the
+// first 20 ms of matrix work run at 350-450; 2350 / 2220 TOP/s; the platform
 // library's plain int8 product of that size 400 us, its best size 2336 TOP/s),
 // 2560 TOP/s at 8192^3.  Bound by the matrix cores at the clock that the chip
-// holds under them, and by LDS: per block 192 KB of operand reads and 64 KB of
-// arriving slices at 128 bytes a clock take as long as the products.  Four
-// waves of 128 x 128 read a third less but leave each SIMD one wave, whose
-// loads (about 58 clocks of issue each) then stop its products: 326 / 346 us.
-// Of the 333 us about 45 are the epilogue, which one workgroup per CU cannot
-// lay under the products of another.  The 256 x 256 tile's stores are
+// holds under them, and by what stands between them: per block a SIMD's products
+// take 2048 clocks, its two waves' sixteen direct loads 928 of issue (about 58
+// each), the CU's operand reads 917 of LDS (counted).  Four waves of 128 x 128
+// read a third less but leave each SIMD one wave, whose loads then stop its
+// products: 326 / 346 us.  About 45 us are the epilogue, which one workgroup per
+// CU cannot lay under the products of another.  The 256 x 256 tile's stores are
 // non-temporal (an output of 180 MB passes every cache): 10 us less; smaller
 // products keep plain stores, since what follows reads them.
 //
 // 128 x 128, one workgroup per CU and 9 units: 777 x 4096 x 4096 f16 with bias,
-// silu and residual 20.3 us; 64 x 64, two per CU: 128 x 4096 x 4096 11.1 us.
-// There a block of 128 codes takes a fixed 0.48 and 0.3 us of waits for the
-// barrier, LDS and the slices in turn; longer rings change nothing, and neither
-// does sharing a block's two steps between two sets of waves (23.2 and 10.5 us).
+// silu and residual 20-21 us; 64 x 64, two per CU: 128 x 4096 x 4096 11.2 us.
+// There a block of 128 codes takes 0.48 and 0.3 us.  For the 128 tile that is some
+// 1100 clocks, of which a SIMD's products need 512, its two waves' eight direct
+// loads 464 of issue, and the CU's operand reads 420 of LDS (counted): with two waves
+// to a SIMD they run side by side only in part.  Longer rings change nothing, and
+// neither does sharing a block's two steps between two sets of waves (23.2 and 10.5
+// us).
 //
 // Where K is no multiple of 128, the block that the rest makes comes first
 // (integer sums have no order): its missing chunks come from sixteen zero

@@ -112,8 +112,9 @@ __device__ __forceinline__ void store_codes(uint8_t* q, Vec8 at, const float v[8
 // and needs no barrier.  The parameters are loaded between the two sums: later
 // (24.9 us instead of 25.6 at the size below) a single token waits for them.
 // Bound by HBM: [8192, 4096] bf16 24.9 us (5.4 TB/s; a large copy
-// reaches 5.0), one row of 4096 3.2 us, latency.  Stores are plain: what follows reads y, and non-temporal loads,
-// which skip the last-level cache that x comes from, take 32 us.
+// reaches 5.0), its codes 28 (two calls 43), one row of 4096 3.2 us, latency.  Stores
+// are plain: what follows reads y, and non-temporal loads, which skip the last-level
+// cache that x comes from, take 32 us.
 template <int FT, int NT, int W, int OUT>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_rows(
     const void* __restrict__ x, int64_t ldx, int64_t rows, int64_t cols, const void* __restrict__ weight,
@@ -194,8 +195,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_rows(
 
 // k_ln_long: rows longer than a workgroup holds: a workgroup per row reads it
 // once for the mean, once around the mean and once for the output (the later
-// reads meet the caches), and once more for the codes.  [4096, 20000] bf16 84 us
-// (3.9 TB/s of what it must read and write); an element per load took 245.
+// reads meet the caches), and once more for the codes.  [4096, 20000] bf16 84-95 us
+// (3.4-3.9 TB/s of what it must read and write); an element per load took 245.
 constexpr int LN_LT = 1024;              // threads per long row
 template <int FT, int OUT>
 __global__ __launch_bounds__(LN_LT) void k_ln_long(const void* __restrict__ x, int64_t ldx, int cols,
@@ -500,8 +501,8 @@ __global__ __launch_bounds__(BT) void k_ln_bwd(const void* __restrict__ dy, int6
 // Rows longer than that: a workgroup per row for dx (two reads), and a second
 // kernel for the column sums (one more): a wave owns 512 columns, a workgroup's
 // four waves take a chunk of the rows in turn, U rows in flight each, and their
-// sums meet in LDS in wave order.  [4096, 20000] bf16 190 us (2.6 TB/s: x and dy
-// cross three times); an element per load took 328.
+// sums meet in LDS in wave order.  [4096, 20000] bf16 190-198 us (2.5 TB/s: x and dy
+// cross three times), [4096, 16384] f32 305; an element per load took 328.
 template <int FT>
 __global__ __launch_bounds__(LN_LT) void k_ln_bwd_long(const void* __restrict__ dy, int64_t lddy,
                                                        const void* __restrict__ x, int64_t ldx, int cols,
