@@ -160,7 +160,7 @@ __device__ __forceinline__ Vec8 vec8(int v, int n)
 template <int FT, bool NT = false>
 __device__ __forceinline__ void store8_own(void* base, int64_t row, Vec8 q, const float v[8])
 {
-    if (q.lo == 0) {
+    if (__builtin_expect(q.lo == 0, 1)) {
         store8_any<FT, NT>(base, row + q.at, v);
     } else {
 #pragma unroll
