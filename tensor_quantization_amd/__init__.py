@@ -1013,7 +1013,8 @@ def tq_topk_distill(logits, top_idx, top_val, temperature=1.0, teacher_lse=None)
     (log-sum-exp of the teacher's logits / temperature) the rest of the
     vocabulary counts as one more outcome; without, the teacher's
     probabilities are normalised over its entries.  Returns (loss, stats,
-    rest_sum), the latter two for tq_topk_distill_backward."""
+    rest_sum), the latter two ([rows, 2] each, rest_sum only with
+    ``teacher_lse``) for tq_topk_distill_backward."""
     head, kept, rows, vocab, dev = _distill_args(logits, top_idx, top_val, teacher_lse)
     ws, nws = _distill_workspace(dev, rows, vocab, head[9])
     loss, stats = _f32(dev, rows), _f32(dev, rows, 2)

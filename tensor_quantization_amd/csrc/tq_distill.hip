@@ -134,7 +134,7 @@ __device__ __forceinline__ float rest_loss(float pr, float R, float S, float abo
     return S == 0.0f ? __builtin_inff() : pr * ((lg2(pr) - (lg2(R) - lg2(S))) * LN2 - above);
 }
 
-// The sum R relative to its largest term's logit m, and b's joined to it.
+// The sum of 2^((z - m) c) over some columns, m the largest z of them (or of more).
 struct Part {
     float m, sum;
 };
@@ -640,10 +640,9 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
 // 16-bit rows of up to 8192 stand eight to a CU, as the launch counts on, where
 // the registers are held to eight waves per SIMD (4096 rows of 8000 42.4 -> 38.8).
 template <int FT, int NT, int W>
-__global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_distill_held(const void* z, int64_t ldz, uint32_t rows, int V, Entries ent,
-                                                     float s, float c,
-                                                     const float* __restrict__ dloss, float* __restrict__ loss,
-                                                     void* dz, int64_t lddz)
+__global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_distill_held(
+    const void* z, int64_t ldz, uint32_t rows, int V, Entries ent, float s, float c, const float* __restrict__ dloss,
+    float* __restrict__ loss, void* dz, int64_t lddz)
 {
     constexpr int NW = NT / 64, ES = FT == F32 ? 4 : 2;
     __shared__ Marks<NT, NT * W / 4 + 1> k;
