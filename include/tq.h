@@ -682,6 +682,43 @@ tq_status tq_topk_distill_grad(const void* logits, int dtype, int64_t rows, int6
                                void* dlogits, int64_t d_row_stride, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* ===================================================================== */
+/* A gated block, adapters beside a projection, the policy loss            */
+/* ===================================================================== */
+/* Addresses, strides, sums and roundings as in the section above. */
+
+/* Both projections of a gated block on codes, the activation and the product in
+ * one kernel, from M = 1 (single tokens) to 65535 * 128:
+ *   g[m][f] = ((float)sum_k qx[m][k] * qw_gate[f][k] * sx[m]) * sw_gate[f] + bias_gate[f]
+ *   u[m][f] the same from qw_up, sw_up and bias_up
+ *   y[m][f] = act(g[m][f]) * u[m][f]
+ * in binary32, in that order, y rounded once to y_dtype.  qx [M, K], both weights
+ * [F, K]; each bias [F] (bias_dtype) may be NULL; act none makes the gate linear.
+ * preact, if not NULL, gets z = [g | u] ([M, 2 F], dense, y_dtype) for the way back.
+ * y and preact are dense and overlap no input and not each other.  F up to 2^27 -
+ * 16, K up to 131071, fewer than 2^23 tiles of 256 tokens and 128 features
+ * (TQ_ERR_UNSUPPORTED beyond).  Operands whose rows start at 16-byte addresses
+ * (bases and K) take the fastest kernels. */
+tq_status tq_w8a8_gated_linear(const int8_t* qx, const float* sx, const int8_t* qw_gate, const float* sw_gate,
+                               const int8_t* qw_up, const float* sw_up, int64_t M, int64_t F, int64_t K,
+                               const void* bias_gate, const void* bias_up, int bias_dtype, int act, void* y,
+                               void* preact, int y_dtype, void* stream);
+
+/* The gate by itself: y [M, F] = act(g) * u from z = [g | u] [M, 2 F] (both dense,
+ * in dtype; y overlaps no part of z).  F up to 2^31 - 16. */
+tq_status tq_gated_act(const void* z, int dtype, int64_t M, int64_t F, int act, void* y, void* stream);
+
+/* The way back through the gate: dz = [dy * u * act'(g) | dy * act(g)] ([M, 2 F])
+ * from dy [M, F] and z = [g | u] [M, 2 F] (all dense, in dtype), and dbias [2 F]
+ * (binary32, may be NULL) = the column sums of dz before its rounding, zeros when
+ * M is 0.  dz may be z itself.  Where act'(g) is 0 (relu at or below 0) the
+ * gate's gradient is 0, whatever dy and u hold; a NaN in g gives NaN.  F up to 2^31
+ * - 16.  `workspace` (needed for dbias): tq_gated_act_backward_workspace_bytes(M,
+ * F) bytes, 16-byte aligned (0 bytes, and null, for few rows). */
+size_t tq_gated_act_backward_workspace_bytes(int64_t M, int64_t F);
+tq_status tq_gated_act_backward(const void* dy, const void* z, int dtype, int64_t M, int64_t F, int act, void* dz,
+                                float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

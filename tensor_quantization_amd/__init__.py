@@ -110,6 +110,10 @@ _SIGS = {
                                  _I),
     "tq_topk_distill_grad": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _I, _I64, _P, _F, _P, _P, _P, _I64, _P, _SZ, _P],
                              _I),
+    "tq_w8a8_gated_linear": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I, _I, _P, _P, _I, _P], _I),
+    "tq_gated_act": ([_P, _I, _I64, _I64, _I, _P, _P], _I),
+    "tq_gated_act_backward_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_gated_act_backward": ([_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _SZ, _P], _I),
     "tq_stream_mix": ([_P, _P, _I64, _I, _I, _I, _I, _P], _I),
 }
 
@@ -1062,3 +1066,70 @@ def tq_topk_distill_grad(logits, top_idx, top_val, dloss=None, temperature=1.0, 
 
 def tq_topk_distill_workspace_bytes(rows, vocab, k):
     return int(_lib.tq_topk_distill_workspace_bytes(rows, vocab, k))
+
+
+# ------------------------------------------------------------- a gated block
+def _on(dev, name, *args):
+    """The call on the device's current stream, with that device as the current
+    one while it launches."""
+    if dev.index is None or dev.index == torch._C._cuda_getDevice():
+        _call(name, *args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args, _stream(dev))
+
+
+def tq_w8a8_gated_linear(qx, sx, qw_gate, sw_gate, qw_up, sw_up, bias_gate=None, bias_up=None, act="silu",
+                         out_dtype=torch.bfloat16, preact=False):
+    """y = act(x Wg^T + bg) * (x Wu^T + bu) from s8 activation codes qx [M, K]
+    (per-row scales sx) and the s8 codes of both weights [F, K] (per-channel
+    scales); with ``preact`` also z = [gate | up] [M, 2 F] before the activation,
+    for tq_gated_act_backward."""
+    qx, qg, qu = _codes(qx, "qx"), _codes(qw_gate, "qw_gate"), _codes(qw_up, "qw_up")
+    M, K = qx.shape
+    F = qg.shape[0]
+    dev = qx.device
+    if qg.shape[1] != K or qu.shape != qg.shape or qg.device != dev or qu.device != dev:
+        raise ValueError("the weights must be [F, K] codes of one shape, on qx's device")
+    sx, sg, su = _row_vector(sx, M, qx, "sx"), _row_vector(sw_gate, F, qx, "sw_gate"), _row_vector(sw_up, F, qx, "sw_up")
+    bg, bu, bdt = _params(qx, F, bias_gate, bias_up)
+    y = torch.empty(M, F, dtype=out_dtype, device=dev)
+    z = torch.empty(M, 2 * F, dtype=out_dtype, device=dev) if preact else None
+    _on(dev, "tq_w8a8_gated_linear", qx.data_ptr(), sx.data_ptr(), qg.data_ptr(), sg.data_ptr(), qu.data_ptr(),
+        su.data_ptr(), M, F, K, _ptr(bg), _ptr(bu), bdt, ACT[act], y.data_ptr(), _ptr(z), FTYPE[out_dtype])
+    return (y, z) if preact else y
+
+
+def _gate_z(z):
+    if z.dim() != 2 or z.shape[1] % 2:
+        raise ValueError("z must be [M, 2 F]")
+    return _dev_float(z, "z"), z.shape[0], z.shape[1] // 2
+
+
+def tq_gated_act(z, act="silu"):
+    """act(gate) * up of z = [gate | up] [M, 2 F], in z's type."""
+    z, M, F = _gate_z(z)
+    y = torch.empty(M, F, dtype=z.dtype, device=z.device)
+    _on(z.device, "tq_gated_act", z.data_ptr(), _ft(z), M, F, ACT[act], y.data_ptr())
+    return y
+
+
+def tq_gated_act_backward(dy, z, act="silu"):
+    """(dz, dbias) of the gate from dy [M, F] and z = [gate | up] [M, 2 F]: dz in
+    z's type and shape, dbias [2 F] its float32 column sums (before dz is
+    rounded)."""
+    z, M, F = _gate_z(z)
+    if dy.shape != (M, F) or dy.dtype != z.dtype or dy.device != z.device:
+        raise ValueError("dy must be [M, F] in z's type, on z's device")
+    dy = dy.contiguous()
+    dz = torch.empty_like(z)
+    dbias = _f32(z.device, 2 * F)
+    nws = _lib.tq_gated_act_backward_workspace_bytes(M, F)
+    ws = _workspace(z.device, nws)
+    _on(z.device, "tq_gated_act_backward", dy.data_ptr(), z.data_ptr(), _ft(z), M, F, ACT[act], dz.data_ptr(),
+        dbias.data_ptr(), _ptr(ws), nws)
+    return dz, dbias
+
+
+def tq_gated_act_backward_workspace_bytes(M, F):
+    return int(_lib.tq_gated_act_backward_workspace_bytes(M, F))

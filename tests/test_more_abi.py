@@ -1,0 +1,66 @@
+"""Host-side checks (no GPU) of the gated block's, the adapters' and the policy
+loss's calls: malformed arguments are refused before anything is enqueued, empty
+calls enqueue nothing, and the workspaces have the sizes their kernels fill."""
+import ctypes
+
+import pytest
+
+P = ctypes.c_void_p
+A, B, C = P(0x10000), P(0x20000), P(0x30000)     # fake device addresses, never dereferenced
+ODD2, ODD4, ODD8 = P(0x10001), P(0x10002), P(0x10004)
+
+
+@pytest.fixture(scope="module")
+def tq():
+    import tensor_quantization_amd as t
+    return t
+
+
+def cdiv(a, b):
+    return -(-a // b)
+
+
+def test_gated_refusals(tq):
+    L, INV, UNS, ALIGN = tq._lib, tq.TQ_ERR_INVALID, tq.TQ_ERR_UNSUPPORTED, tq.TQ_ERR_ALIGN
+    ok = dict(qx=A, sx=B, qg=A, sg=B, qu=A, su=B, M=4, F=8, K=16, bg=C, bu=C, bdt=2, act=2, y=B, z=None, ydt=2, st=None)
+
+    def call(**kw):
+        return L.tq_w8a8_gated_linear(*{**ok, **kw}.values())
+    for name in ("qx", "sx", "qg", "sg", "qu", "su", "y"):
+        assert call(**{name: None}) == INV, name
+    assert call(act=5) == INV and call(act=-1) == INV and call(ydt=3) == INV and call(bdt=3) == INV
+    assert call(M=-1) == INV and call(F=-1) == INV and call(K=-1) == INV
+    assert call(K=131072) == UNS and call(M=65535 * 128 + 1) == UNS and call(F=1 << 27) == UNS
+    assert call(M=65535 * 128, F=1 << 20) == UNS                  # too many tiles
+    for name in ("sx", "sg", "su"):
+        assert call(**{name: ODD4}) == ALIGN, name
+    assert call(bg=ODD2) == ALIGN and call(bu=ODD2) == ALIGN and call(y=ODD2) == ALIGN and call(z=ODD2) == ALIGN
+    assert call(y=ODD4, ydt=0) == ALIGN
+    assert call(M=0) == 0 and call(F=0) == 0
+    f = L.tq_gated_act
+    assert f(None, 2, 4, 8, 2, B, None) == INV and f(A, 2, 4, 8, 2, None, None) == INV
+    assert f(A, 3, 4, 8, 2, B, None) == INV and f(A, 2, 4, 8, 9, B, None) == INV and f(A, 2, -4, 8, 2, B, None) == INV
+    assert f(A, 2, 4, 1 << 31, 2, B, None) == UNS and f(ODD2, 2, 4, 8, 2, B, None) == ALIGN
+    assert f(A, 2, 0, 8, 2, B, None) == 0 and f(None, 2, 4, 0, 2, None, None) == 0
+    g = L.tq_gated_act_backward
+    n = tq.tq_gated_act_backward_workspace_bytes(100, 50)
+    assert n >= 100 * 4
+    assert g(A, None, 2, 100, 50, 1, B, C, A, n, None) == INV and g(None, A, 2, 100, 50, 1, B, C, A, n, None) == INV
+    assert g(A, A, 2, 100, 50, 7, B, C, A, n, None) == INV and g(A, A, 5, 100, 50, 1, B, C, A, n, None) == INV
+    assert g(A, A, 2, 100, 50, 1, None, C, A, n, None) == INV and g(A, A, 2, 100, 50, 1, B, C, None, n, None) == INV
+    assert g(A, A, 2, 100, 50, 1, B, C, A, n - 1, None) == INV
+    assert g(A, A, 2, 100, 50, 1, B, C, ODD8, n, None) == ALIGN and g(A, ODD2, 2, 100, 50, 1, B, C, A, n, None) == ALIGN
+    assert g(A, A, 2, 100, 50, 1, B, ODD4, A, n, None) == ALIGN
+    assert g(A, A, 2, 100, 1 << 31, 1, B, C, A, 1 << 62, None) == UNS
+    assert g(A, A, 2, 100, 0, 1, B, C, A, 0, None) == 0
+
+
+@pytest.mark.parametrize("F", [1, 7, 50, 512, 513, 11008, 1 << 23])
+@pytest.mark.parametrize("M", [1, 64, 65, 72, 73, 100, 1000, 8192, 8193, 1 << 20])
+def test_gate_backward_workspace(tq, M, F):
+    have = tq.tq_gated_act_backward_workspace_bytes(M, F)
+    if M <= 64:
+        assert have == 0                                # one chunk: its sums are dbias
+        return
+    chunk = 8 * cdiv(cdiv(M, max(1, 8192 // cdiv(F, 512))), 8)
+    assert have >= cdiv(M, chunk) * cdiv(2 * F, 4) * 16
