@@ -719,6 +719,30 @@ size_t tq_gated_act_backward_workspace_bytes(int64_t M, int64_t F);
 tq_status tq_gated_act_backward(const void* dy, const void* z, int dtype, int64_t M, int64_t F, int act, void* dz,
                                 float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The W8A8 product beside low-rank adapters of many requests.  Token m has the
+ * adapter c = adapter[m] (32-bit), or none where that lies outside [0, adapters):
+ *   h[m][r] = scale[c] * sum_k x[m][k] * a[c][r][k]                      (r < rank)
+ *   z[m][n] = ((float)sum_k qx[m][k] * qw[n][k] * sx[m]) * sw[n]
+ *             + sum_r h[m][r] * b[c][n][r] + bias[n]
+ *   y[m][n] = act(z[m][n]) + residual[m][n]
+ * x [M, K] (row stride x_row_stride), a [adapters, rank, K] and b [adapters, N,
+ * rank] have x_dtype; scale [adapters] (binary32) may be NULL: ones.  qx and sx are
+ * x's codes and their scales, and everything else is as in tq_w8a8_linear_epilogue,
+ * whose bits a token without an adapter gets.  Tokens may come in any order;
+ * what one adapter holds (infinities, NaN) does not reach another's tokens.  The
+ * products with a and b are summed in binary32, h is not rounded below 16 bits.
+ * rank from 1 to 256 (TQ_ERR_UNSUPPORTED beyond; adapters of lower rank are
+ * padded with zeros), M, N and K as in tq_w8a8_linear_epilogue.  `workspace`:
+ * tq_w8a8_linear_adapters_workspace_bytes(M, rank) bytes, 16-byte aligned, contents
+ * ignored (not needed with adapters = 0). */
+size_t tq_w8a8_linear_adapters_workspace_bytes(int64_t M, int64_t rank);
+tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stride, const int8_t* qx, const float* sx,
+                                  const int8_t* qw, const float* sw, int64_t M, int64_t N, int64_t K,
+                                  const int32_t* adapter, int64_t adapters, int64_t rank, const void* a, const void* b,
+                                  const float* scale, const void* bias, int bias_dtype, int act, const void* residual,
+                                  int64_t residual_row_stride, void* y, void* preact, int y_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -114,6 +114,9 @@ _SIGS = {
     "tq_gated_act": ([_P, _I, _I64, _I64, _I, _P, _P], _I),
     "tq_gated_act_backward_workspace_bytes": ([_I64, _I64], _SZ),
     "tq_gated_act_backward": ([_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _SZ, _P], _I),
+    "tq_w8a8_linear_adapters_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_w8a8_linear_adapters": ([_P, _I, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I, _I,
+                                 _P, _I64, _P, _P, _I, _P, _SZ, _P], _I),
     "tq_stream_mix": ([_P, _P, _I64, _I, _I, _I, _I, _P], _I),
 }
 
@@ -1133,3 +1136,52 @@ def tq_gated_act_backward(dy, z, act="silu"):
 
 def tq_gated_act_backward_workspace_bytes(M, F):
     return int(_lib.tq_gated_act_backward_workspace_bytes(M, F))
+
+
+# --------------------------------- the W8A8 product beside low-rank adapters
+def tq_w8a8_linear_adapters(x, qx, sx, qw, sw, adapter, a, b, scale=None, bias=None, act="none", residual=None,
+                            out_dtype=torch.bfloat16, preact=False):
+    """y = act(x W^T + scale[c] (x a[c]^T) b[c]^T + bias) + residual, where c =
+    adapter[m] (int32, one per token; outside [0, adapters), -1 say: none) and
+    the shared product runs on x's s8 codes qx [M, K] (per-row scales sx) and the
+    weight's qw [N, K] (per-channel scales sw).  a [adapters, rank, K] and b
+    [adapters, N, rank] have x's type; with ``preact`` also the value before the
+    activation."""
+    qx, qw = _codes(qx, "qx"), _codes(qw, "qw")
+    M, K = qx.shape
+    N = qw.shape[0]
+    dev = qx.device
+    if qw.shape[1] != K or qw.device != dev:
+        raise ValueError("qx and qw must share K and their device")
+    if x.shape != (M, K) or x.device != dev:
+        raise ValueError("x must be [M, K] as its codes, on their device")
+    sx, sw = _row_vector(sx, M, qx, "sx"), _row_vector(sw, N, qx, "sw")
+    if adapter.dtype != torch.int32 or adapter.shape != (M,) or adapter.device != dev:
+        raise ValueError("adapter must be int32 with one value per token, on x's device")
+    if a.dim() != 3 or a.shape[2] != K or b.shape != (a.shape[0], N, a.shape[1]):
+        raise ValueError("a must be [adapters, rank, K] and b [adapters, N, rank]")
+    if a.dtype != x.dtype or b.dtype != x.dtype or a.device != dev or b.device != dev:
+        raise ValueError("a and b must have x's type and device")
+    count, rank = a.shape[0], a.shape[1]
+    _, b_, bdt = _params(qx, N, None, bias)
+    ldr = N
+    if residual is not None:
+        if residual.shape != (M, N) or residual.dtype != out_dtype or residual.device != dev:
+            raise ValueError("residual must be [M, N] in the output's type, on x's device")
+        residual, _, _, ldr = _rows_of(residual, "residual")
+    xr, _, _, ldx = _rows_of(x, "x")
+    adapter, a, b = adapter.contiguous(), a.contiguous(), b.contiguous()
+    scale = None if scale is None else _row_vector(scale, count, qx, "scale")
+    y = torch.empty(M, N, dtype=out_dtype, device=dev)
+    z = torch.empty_like(y) if preact else None
+    nws = _lib.tq_w8a8_linear_adapters_workspace_bytes(M, rank)
+    ws = _workspace(dev, nws)
+    _on(dev, "tq_w8a8_linear_adapters", xr.data_ptr(), FTYPE[x.dtype], ldx, qx.data_ptr(), sx.data_ptr(),
+        qw.data_ptr(), sw.data_ptr(), M, N, K, adapter.data_ptr(), count, rank, a.data_ptr(), b.data_ptr(),
+        _ptr(scale), _ptr(b_), bdt, ACT[act], _ptr(residual), ldr, y.data_ptr(), _ptr(z), FTYPE[out_dtype], _ptr(ws),
+        nws)
+    return (y, z) if preact else y
+
+
+def tq_w8a8_linear_adapters_workspace_bytes(M, rank):
+    return int(_lib.tq_w8a8_linear_adapters_workspace_bytes(M, rank))

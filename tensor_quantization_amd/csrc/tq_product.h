@@ -167,15 +167,16 @@ __device__ __forceinline__ Raw8<YT> residual8(const Epi& e, const Cols8& c, int6
     return r;
 }
 
-// Finishes eight columns of one row from their sums.
-template <int YT>
+// Finishes eight columns of one row from their sums (SCALED: from the bits of
+// binary32 values that have been scaled already).
+template <int YT, bool SCALED = false>
 __device__ __forceinline__ void epilogue8(const Epi& e, const Cols8& c, int64_t row, float sx, const int acc[8],
                                           const Raw8<YT>& res)
 {
     const int64_t at = row * e.N + c.col;
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)acc[i] * sx * c.sw[i];
+    for (int i = 0; i < 8; ++i) v[i] = SCALED ? as_f((uint32_t)acc[i]) : (float)acc[i] * sx * c.sw[i];
     if (e.bias) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += c.b[i];
@@ -432,12 +433,22 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
     }
 }
 
+// What is done to a staged half of sums before it is finished: nothing, or (ADDS)
+// what turns them into scaled binary32 values and adds to these.
+struct NoDelta {
+    static constexpr bool ADDS = false;
+    template <int NM, int NN>
+    __device__ __forceinline__ void apply(const Epi&, int64_t, int64_t, int, int*) const
+    {
+    }
+};
+
 // Any part: bounds, and the value before the activation where it is asked for
 // (8192 x 11008 x 4096 with gelu_tanh and that value 366 us, 327 without: the 180 MB
 // more take 36 at a large copy's rate).
-template <int YT, int NM, int NN>
-__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, const v4i (&acc)[NM][NN],
-                                           int* stage)
+template <int YT, int NM, int NN, class D>
+__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, int64_t n0,
+                                           const v4i (&acc)[NM][NN], int* stage, const D& delta)
 {
     using S = Stage<NM, NN>;
     const int lane = threadIdx.x & 63;
@@ -448,6 +459,7 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
         const int64_t mh = m0 + 32 * h;
         if (mh >= e.M) return;           // uniform
         stage_half<NM, NN>(h, acc, stage);
+        delta.template apply<NM, NN>(e, m0, n0, h, stage);
         const int rows = cc.n == 0 ? 0 : e.M - mh < 32 ? (int)(e.M - mh) : 32;
 #pragma unroll 1
         for (int r = r0; r < rows; r += S::RPI) {
@@ -456,7 +468,7 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
             const v4i s0 = *reinterpret_cast<const v4i*>(&stage[r * S::PITCH + c]);
             const v4i s1 = *reinterpret_cast<const v4i*>(&stage[r * S::PITCH + c + 4]);
             const int s[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-            epilogue8<YT>(e, cc, mh + r, sx[32 * h + r], s, res);
+            epilogue8<YT, D::ADDS>(e, cc, mh + r, sx[32 * h + r], s, res);
         }
     }
 }
@@ -465,20 +477,20 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
 // of LDS, so that its stores are whole rows of its part and the epilogue's
 // code exists once per activation.  A lane keeps its eight columns for all
 // rows, so their scales and bias are read once.
-template <int YT, int NM, int NN, bool NTS = false>
+template <int YT, int NM, int NN, bool NTS = false, class D = NoDelta>
 __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0, const v4i (&acc)[NM][NN],
-                                               int* stage)
+                                            int* stage, const D& delta = D())
 {
     const Cols8 cc = cols8(e, n0 + 8 * ((threadIdx.x & 63) % Stage<NM, NN>::LPR));
     if (m0 >= e.M) return;               // uniform
     stage_scales<NM, NN>(e, m0, stage);
     const bool inside = m0 + 16 * NM <= e.M && n0 + 16 * NN <= e.N && e.N <= 1 << 22 && e.ldr <= 1 << 22;
-    if (inside && !e.z)
+    if (!D::ADDS && inside && !e.z)
         with_act(e.act, [&](auto a) {
             if (e.res) finish_inside<YT, NM, NN, decltype(a)::value, true, NTS>(e, cc, m0, n0, acc, stage);
             else finish_inside<YT, NM, NN, decltype(a)::value, false, NTS>(e, cc, m0, n0, acc, stage);
         });
-    else finish_any<YT, NM, NN>(e, cc, m0, acc, stage);
+    else finish_any<YT, NM, NN>(e, cc, m0, n0, acc, stage, delta);
 }
 
 // ------------------------------------------------------------ the tile kernels

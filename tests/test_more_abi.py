@@ -64,3 +64,28 @@ def test_gate_backward_workspace(tq, M, F):
         return
     chunk = 8 * cdiv(cdiv(M, max(1, 8192 // cdiv(F, 512))), 8)
     assert have >= cdiv(M, chunk) * cdiv(2 * F, 4) * 16
+
+
+def test_adapter_refusals(tq):
+    L, INV, UNS, ALIGN = tq._lib, tq.TQ_ERR_INVALID, tq.TQ_ERR_UNSUPPORTED, tq.TQ_ERR_ALIGN
+    n = tq.tq_w8a8_linear_adapters_workspace_bytes(4, 12)
+    assert n >= 4 * 12 * 4 and tq.tq_w8a8_linear_adapters_workspace_bytes(0, 12) == 0
+    ok = dict(x=A, xdt=2, ldx=16, qx=A, sx=B, qw=A, sw=B, M=4, N=8, K=16, ids=C, count=3, R=12, a=A, b=B, scale=C, bias=C,
+              bdt=2, act=1, res=C, ldr=8, y=B, z=None, ydt=2, ws=A, n=n, st=None)
+
+    def call(**kw):
+        return L.tq_w8a8_linear_adapters(*{**ok, **kw}.values())
+    for name in ("x", "qx", "sx", "qw", "sw", "ids", "a", "b", "y", "ws"):
+        assert call(**{name: None}) == INV, name
+    assert call(xdt=3) == INV and call(ydt=3) == INV and call(bdt=3) == INV and call(act=5) == INV
+    assert call(M=-1) == INV and call(count=-1) == INV and call(R=0) == INV
+    assert call(ldx=15) == INV and call(ldr=7) == INV and call(n=n - 1) == INV
+    big = 1 << 62
+    assert call(R=257, n=big) == UNS and call(K=131072, ldx=131072) == UNS and call(M=65535 * 128 + 1, n=big) == UNS
+    assert call(count=1 << 31) == UNS
+    for name in ("x", "a", "b", "bias", "res", "y", "z"):
+        assert call(**{name: ODD2}) == ALIGN, name
+    for name in ("sx", "sw", "ids", "scale"):
+        assert call(**{name: ODD4}) == ALIGN, name
+    assert call(ws=ODD8) == ALIGN
+    assert call(M=0) == 0 and call(N=0) == 0

@@ -9,7 +9,7 @@ from test_isa import CSRC, _asm, _bodies
 from test_llm_isa import matrix_hazards
 
 
-@pytest.mark.parametrize("source", ["tq_gated.hip"])
+@pytest.mark.parametrize("source", ["tq_gated.hip", "tq_adapters.hip"])
 def test_products_from_asm_wait(source, tmp_path):
     listing = _asm(os.path.join(CSRC, source), str(tmp_path))
     names = [n for n, body in _bodies(listing) if "k_epi_ring" in n and any(b.startswith("v_mfma_i32") for b in body)]
