@@ -21,7 +21,10 @@
  *   - what stands around a quantized layer: layer norm (forward, fused with
  *     the per-token quantizer, backward), the W8A8 product with bias,
  *     activation and residual in its epilogue and that epilogue's backward,
- *     and the distillation loss of a student against its teacher's top logits.
+ *     and the distillation loss of a student against its teacher's top logits,
+ *   - a gated block's two W8A8 projections in one kernel and its backward, the
+ *     W8A8 product beside low-rank adapters of many requests, and the clipped
+ *     policy loss on a token's log-probability, forward and backward.
  *
  * Sources (page titles and sections):
  *   [Q]  docs.rs baracuda_kernels::quantize -- module overview (dtype
@@ -742,6 +745,56 @@ tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stri
                                   const float* scale, const void* bias, int bias_dtype, int act, const void* residual,
                                   int64_t residual_row_stride, void* y, void* preact, int y_dtype, void* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/* A token's log-probability, and the clipped policy loss on it.  Logits [rows, vocab]
+ * (row stride row_stride), rows up to 2^31 - 1 and vocab up to 2^31 - 256; token
+ * [rows] (32- or 64-bit integers: idx_bits) is the column that was drawn.  A row
+ * whose token lies outside [0, vocab) (-1, say: a prompt's or padding) counts
+ * nowhere: log-probability, loss and gradient 0, whatever its logits hold, which are
+ * not read.  With s = 1 / temperature, y = token[row], q_j = softmax(s z)_j:
+ *   l = s z_y - log sum_i exp(s z_i)                                (logp [rows])
+ *   rho = exp(l - old_logp)      (old_logp NULL: the present policy's own, rho = 1)
+ *   loss = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)    (A = advantage)
+ *          + kl_coef (exp(d) - 1 - d),  d = ref_logp - l    (ref_logp NULL: without)
+ *   dloss/dl = (rho A <= clip(rho) A ? -rho A : 0) + kl_coef (1 - exp(d))
+ *   dlogits_j = dloss (dloss/dl) s (1[j = y] - q_j)
+ * advantage, old_logp and ref_logp are binary32 [rows]; gradients do not go through
+ * them.  clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, temperature > 0.  Logits of
+ * -inf are tokens that cannot be drawn; one that was drawn all the same has l =
+ * -inf, rho = 0, gradient 0, and with a KL term the loss +inf and a gradient that is not
+ * finite.  A row of nothing but -inf has l = -inf and gradient 0.
+ *
+ * tq_token_logp writes logp and, if not NULL, stats [rows, 2] = the row's largest
+ * logit and the sum of exp(s (z - it)) (-inf and 0 for a row that counts nowhere);
+ * tq_token_logp_backward turns dlogp [rows] (NULL: ones) into dlogits (logits' type,
+ * row stride d_row_stride).  tq_policy_loss writes loss, logp and stats (which may be
+ * NULL), and tq_policy_loss_backward takes the latter two back with dloss [rows] (NULL:
+ * ones); tq_policy_loss_grad does both in one call, for a program that knows dloss
+ * beforehand: where a workgroup can hold a row, the logits are read once.  dlogits
+ * may be the logits themselves (same address and stride).  `workspace`:
+ * tq_policy_loss_workspace_bytes(rows, vocab) bytes, 16-byte aligned, contents
+ * ignored. */
+size_t tq_policy_loss_workspace_bytes(int64_t rows, int64_t vocab);
+tq_status tq_token_logp(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                        const void* token, int idx_bits, float temperature, float* logp, float* stats, void* workspace,
+                        size_t workspace_bytes, void* stream);
+tq_status tq_token_logp_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                 const void* token, int idx_bits, float temperature, const float* stats,
+                                 const float* dlogp, void* dlogits, int64_t d_row_stride, void* stream);
+tq_status tq_policy_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                         const void* token, int idx_bits, const float* advantage, const float* old_logp,
+                         const float* ref_logp, float clip_low, float clip_high, float kl_coef, float temperature,
+                         float* loss, float* logp, float* stats, void* workspace, size_t workspace_bytes, void* stream);
+tq_status tq_policy_loss_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                  const void* token, int idx_bits, const float* advantage, const float* old_logp,
+                                  const float* ref_logp, float clip_low, float clip_high, float kl_coef,
+                                  float temperature, const float* logp, const float* stats, const float* dloss,
+                                  void* dlogits, int64_t d_row_stride, void* stream);
+tq_status tq_policy_loss_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                              const void* token, int idx_bits, const float* advantage, const float* old_logp,
+                              const float* ref_logp, float clip_low, float clip_high, float kl_coef, float temperature,
+                              const float* dloss, float* loss, float* logp, void* dlogits, int64_t d_row_stride,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

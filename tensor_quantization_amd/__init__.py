@@ -117,6 +117,14 @@ _SIGS = {
     "tq_w8a8_linear_adapters_workspace_bytes": ([_I64, _I64], _SZ),
     "tq_w8a8_linear_adapters": ([_P, _I, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I, _I,
                                  _P, _I64, _P, _P, _I, _P, _SZ, _P], _I),
+    "tq_policy_loss_workspace_bytes": ([_I64, _I64], _SZ),
+    "tq_token_logp": ([_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _SZ, _P], _I),
+    "tq_token_logp_backward": ([_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _I64, _P], _I),
+    "tq_policy_loss": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _P, _SZ, _P], _I),
+    "tq_policy_loss_backward": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _P, _I64,
+                                 _P], _I),
+    "tq_policy_loss_grad": ([_P, _I, _I64, _I64, _I64, _P, _I, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _P, _I64, _P,
+                             _SZ, _P], _I),
     "tq_stream_mix": ([_P, _P, _I64, _I, _I, _I, _I, _P], _I),
 }
 
@@ -1185,3 +1193,109 @@ def tq_w8a8_linear_adapters(x, qx, sx, qw, sw, adapter, a, b, scale=None, bias=N
 
 def tq_w8a8_linear_adapters_workspace_bytes(M, rank):
     return int(_lib.tq_w8a8_linear_adapters_workspace_bytes(M, rank))
+
+
+# ------------------------------------- token log-probability and policy loss
+def _logp_args(logits, token):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    z, _, _, ld = _rows_of(logits, "logits")
+    if token.dtype not in (torch.int32, torch.int64):
+        raise TypeError("token must be int32 or int64")
+    if token.shape != (rows,) or token.device != logits.device:
+        raise ValueError("token must have one value per row, on the logits' device")
+    token = token.contiguous()
+    head = (z.data_ptr(), FTYPE[z.dtype], rows, vocab, ld, token.data_ptr(), 32 if token.dtype == torch.int32 else 64)
+    return head, (z, token), rows, vocab, z.device
+
+
+def _policy_args(logits, rows, advantage, old_logp, ref_logp):
+    kept = [None if v is None else _row_vector(v, rows, logits, name)
+            for v, name in ((advantage, "advantage"), (old_logp, "old_logp"), (ref_logp, "ref_logp"))]
+    return kept, [_ptr(v) for v in kept]
+
+
+def _saved_stats(stats, rows, dev):
+    if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != dev:
+        raise ValueError("stats must be the forward call's [rows, 2]")
+    return stats.contiguous()
+
+
+def _logp_workspace(dev, rows, vocab):
+    nws = _lib.tq_policy_loss_workspace_bytes(rows, vocab)
+    return _workspace(dev, nws), nws
+
+
+def tq_token_logp(logits, token, temperature=1.0):
+    """(logp, stats): the log-probability of each row's token under logits [rows,
+    vocab] / temperature (0 where the token lies outside, -1 say), and what
+    tq_token_logp_backward needs ([rows, 2])."""
+    head, kept, rows, vocab, dev = _logp_args(logits, token)
+    ws, nws = _logp_workspace(dev, rows, vocab)
+    logp, stats = _f32(dev, rows), _f32(dev, rows, 2)
+    _on(dev, "tq_token_logp", *head, temperature, logp.data_ptr(), stats.data_ptr(), _ptr(ws), nws)
+    return logp, stats
+
+
+def tq_token_logp_backward(logits, token, stats, dlogp=None, temperature=1.0):
+    """dlogits of tq_token_logp from its inputs and statistics; ``dlogp`` [rows]
+    is the gradient of the log-probabilities (ones by default)."""
+    head, kept, rows, vocab, dev = _logp_args(logits, token)
+    stats = _saved_stats(stats, rows, dev)
+    dlogp = None if dlogp is None else _row_vector(dlogp, rows, logits, "dlogp")
+    dz = torch.empty_like(kept[0], memory_format=torch.contiguous_format)
+    _on(dev, "tq_token_logp_backward", *head, temperature, stats.data_ptr(), _ptr(dlogp), dz.data_ptr(), vocab)
+    return dz
+
+
+def tq_policy_loss(logits, token, advantage, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                   temperature=1.0):
+    """(loss, logp, stats) of every row: the clipped policy loss of the token
+    that was drawn, with ``kl_coef`` times the KL estimate exp(d) - 1 - d, d =
+    ref_logp - logp, where ``ref_logp`` is given; ``old_logp`` None stands for
+    the present policy's own.  logp and stats are for tq_policy_loss_backward."""
+    head, kept, rows, vocab, dev = _logp_args(logits, token)
+    vectors, ptrs = _policy_args(logits, rows, advantage, old_logp, ref_logp)
+    ws, nws = _logp_workspace(dev, rows, vocab)
+    loss, stats = _f32(dev, rows), _f32(dev, rows, 2)
+    logp = torch.empty_like(loss)
+    _on(dev, "tq_policy_loss", *head, *ptrs, clip_low, clip_high, kl_coef, temperature, loss.data_ptr(),
+        logp.data_ptr(), stats.data_ptr(), _ptr(ws), nws)
+    return loss, logp, stats
+
+
+def tq_policy_loss_backward(logits, token, advantage, logp, stats, dloss=None, old_logp=None, ref_logp=None,
+                            clip_low=0.2, clip_high=0.2, kl_coef=0.0, temperature=1.0):
+    """dlogits of tq_policy_loss from its inputs, logp and stats; ``dloss`` [rows]
+    is the gradient of the losses (ones by default)."""
+    head, kept, rows, vocab, dev = _logp_args(logits, token)
+    vectors, ptrs = _policy_args(logits, rows, advantage, old_logp, ref_logp)
+    logp, stats = _row_vector(logp, rows, logits, "logp"), _saved_stats(stats, rows, dev)
+    dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
+    dz = torch.empty_like(kept[0], memory_format=torch.contiguous_format)
+    _on(dev, "tq_policy_loss_backward", *head, *ptrs, clip_low, clip_high, kl_coef, temperature, logp.data_ptr(),
+        stats.data_ptr(), _ptr(dloss), dz.data_ptr(), vocab)
+    return dz
+
+
+def tq_policy_loss_grad(logits, token, advantage, dloss=None, old_logp=None, ref_logp=None, clip_low=0.2,
+                        clip_high=0.2, kl_coef=0.0, temperature=1.0, inplace=False):
+    """(loss, logp, dlogits) in one call, for a program that knows ``dloss`` (ones
+    by default) beforehand; ``inplace`` writes the gradient over the logits."""
+    head, kept, rows, vocab, dev = _logp_args(logits, token)
+    vectors, ptrs = _policy_args(logits, rows, advantage, old_logp, ref_logp)
+    dloss = None if dloss is None else _row_vector(dloss, rows, logits, "dloss")
+    if inplace and kept[0] is not logits:
+        raise ValueError("in place needs logits whose rows are contiguous")
+    ws, nws = _logp_workspace(dev, rows, vocab)
+    loss = _f32(dev, rows)
+    logp = torch.empty_like(loss)
+    dz = logits if inplace else torch.empty_like(kept[0], memory_format=torch.contiguous_format)
+    _on(dev, "tq_policy_loss_grad", *head, *ptrs, clip_low, clip_high, kl_coef, temperature, _ptr(dloss),
+        loss.data_ptr(), logp.data_ptr(), dz.data_ptr(), head[4] if inplace else vocab, _ptr(ws), nws)
+    return loss, logp, dz
+
+
+def tq_policy_loss_workspace_bytes(rows, vocab):
+    return int(_lib.tq_policy_loss_workspace_bytes(rows, vocab))
