@@ -5,13 +5,14 @@
 //   z[m][n] = ((float)sum_k qx[m][k] qw[n][k]) sx[m] sw[n] + sum_r h[m][r] b[c][n][r] + bias[n]
 //   y = act(z) + residual
 //
-// x and the adapters are of one type, their products summed in binary32; h stays
-// in binary32 between its kernel and the product's, which takes it in its
-// epilogue: as a scalar loop per output for a few tokens, on the matrix cores for
-// tiles.  There a 16-bit operand of h would lose what h holds beyond 8 or 11 bits,
-// so it goes in twice: h = hi + lo in the adapters' type, 16 or more bits in all
-// (f16, whose range is short, takes h relative to a power of two near the row's
-// largest value).
+// x and the adapters are of one type, their products summed in binary32.  h goes from
+// its kernel to the product's through the workspace, and the product adds its part in
+// the epilogue.  For a few tokens that is a scalar loop per output, and h is
+// binary32.  For tiles it is the matrix cores' work, and h comes in their operand order,
+// 16 tokens and a step of 32 ranks (binary32: 16) in one piece.  A 16-bit operand of h
+// would lose what h holds beyond 8 or 11 bits, so it goes in twice: h = hi + lo in the
+// adapters' type, 16 or more bits in all (f16, whose range is short, takes a token's
+// step relative to a power of two near its largest value).
 //
 // The tokens of one sixteen-row operand may have several adapters.  Each takes its
 // turn, the other tokens' h cleared, and only its own tokens take the result, so
@@ -29,8 +30,21 @@ struct Adapters {
     const void* a;                       // [count, R, K]
     const void* b;                       // [count, N, R]
     const float* scale;                  // [count], or null
-    float* h;                            // [M, ldh]
+    void* h;                             // for a few tokens binary32 [M, ldh], else in operand order
+    int* up;                             // f16 in operand order: a token's and step's exponent [M, steps]
     int count, R, ldh, dt;
+};
+
+// In operand order a piece of 1024 bytes holds, for lane l, E ranks from E (l / 16) on of
+// token l % 16; 16-bit types have two pieces, hi and lo.
+template <int AT>
+struct Low {
+    static constexpr int STEP = AT == F32 ? 16 : 32, E = STEP / 4, PIECES = AT == F32 ? 1 : 2;
+    static __device__ __forceinline__ int steps(const Adapters& ad) { return (ad.R + STEP - 1) / STEP; }
+    static __device__ __forceinline__ uint4* piece(const Adapters& ad, int64_t tile, int step)
+    {
+        return static_cast<uint4*>(ad.h) + (tile * steps(ad) + step) * (64 * PIECES);
+    }
 };
 
 __device__ __forceinline__ int adapter_of(const Adapters& ad, int64_t row, int64_t M)
@@ -41,13 +55,19 @@ __device__ __forceinline__ int adapter_of(const Adapters& ad, int64_t row, int64
 
 constexpr int AD_R = 256;                // largest rank
 
+// Sixteen bytes of elements.
+template <int AT>
+__device__ __forceinline__ uint4 whole_chunk(const void* p, int64_t at)
+{
+    return ld16_any(static_cast<const char*>(p) + at * (AT == F32 ? 4 : 2));
+}
+
 // Elements r .. of a vector of n (16 bytes of them), zeros past its end.
 template <int AT>
 __device__ __forceinline__ uint4 chunk_of(const void* p, int64_t at, int r, int n)
 {
     constexpr int E = AT == F32 ? 4 : 8;
-    if (r + E <= n) return AT == F32 ? ld16_any(static_cast<const float*>(p) + at + r)
-                                     : ld16_any(static_cast<const uint16_t*>(p) + at + r);
+    if (r + E <= n) return whole_chunk<AT>(p, at + r);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < E - 1; ++i)
@@ -77,97 +97,212 @@ __device__ __forceinline__ v4f add_low(uint4 w, uint4 x, v4f d)
     }
 }
 
-// ------------------------------------------------------------- h, a few tokens
-// k_low_few: a wave per token and rank.
 template <int AT>
-__global__ __launch_bounds__(256) void k_low_few(const void* __restrict__ x, int64_t ldx, int K, Adapters ad)
+__device__ __forceinline__ v4f add_low(v4i w, v4i x, v4f d)
 {
-    constexpr int U = 4;
-    const int lane = threadIdx.x & 63, r = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t m = blockIdx.y;
-    const int c = adapter_of(ad, m, m + 1);
-    if (r >= ad.R || c < 0) return;
-    const int64_t xr = m * ldx, ar = ((int64_t)c * ad.R + r) * K;
-    float s = 0.0f;
-    if (K < 8) {
-        if (lane < K) s = load1<AT>(x, xr + lane) * load1<AT>(ad.a, ar + lane);
-    } else {
-        const int nvec = (K + 7) / 8;
-        for (int v0 = lane; v0 < nvec; v0 += 64 * U) {
-            Raw8<AT> p[U], q[U];
-            Vec8 at[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                at[u] = vec8(v0 + 64 * u, K);
-                p[u] = load8_any<AT>(x, xr + at[u].at);
-                q[u] = load8_any<AT>(ad.a, ar + at[u].at);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float f[8], g[8];
-                widen8<AT>(p[u], f);
-                widen8<AT>(q[u], g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s = i >= at[u].lo ? __builtin_fmaf(f[i], g[i], s) : s;
-            }
-        }
-    }
-    s = wave_sum(s);
-    if (lane == 0) ad.h[m * ad.ldh + r] = ad.scale ? s * ad.scale[c] : s;
+    return add_low<AT>(__builtin_bit_cast(uint4, w), __builtin_bit_cast(uint4, x), d);
 }
 
-// ------------------------------------------------------------ h, many tokens
-// k_low_many: a workgroup per 16 tokens, on the matrix cores; its waves take the K
-// axis in turn, two steps' 128 bytes of every row at a time, and their sums meet in LDS.
-template <int AT, int RT, int NWV>
+// ------------------------------------------------------------------------- h
+// Writes E ranks of token m, from rank E g of the step on, in operand order; the four
+// threads of a token's step stand side by side.
+template <int AT>
+__device__ __forceinline__ void put_low(const Adapters& ad, int64_t m, int step, int g, float v[Low<AT>::E])
+{
+    uint4* to = Low<AT>::piece(ad, m / 16, step) + 16 * g + m % 16;
+    if constexpr (AT == F32) {
+        *to = make_uint4(as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
+    } else {
+        if constexpr (AT == F16) {
+            float most = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = __builtin_fmaxf(most, __builtin_fabsf(v[k]));
+            most = __builtin_fmaxf(most, as_f(dpp<DPP_XOR1>(as_u(most))));
+            most = __builtin_fmaxf(most, as_f(dpp<DPP_XOR2>(as_u(most))));
+            const int up = most > 0.0f && most < __builtin_inff() ? __builtin_amdgcn_frexp_expf(most) : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __builtin_amdgcn_ldexpf(v[k], -up);
+            if (g == 0) ad.up[m * Low<AT>::steps(ad) + step] = up;
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            hi[k] = narrow2<AT>(v[2 * k], v[2 * k + 1]);
+            Raw8<AT> back = {};
+            back.w[0].x = hi[k];
+            float wide[8];
+            widen8<AT>(back, wide);
+            // an infinite or NaN hi is all there is
+            lo[k] = narrow2<AT>(__builtin_fabsf(wide[0]) < __builtin_inff() ? v[2 * k] - wide[0] : 0.0f,
+                                __builtin_fabsf(wide[1]) < __builtin_inff() ? v[2 * k + 1] - wide[1] : 0.0f);
+        }
+        to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        to[64] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
+// A wave's share of the sum of x a over vectors v0, v0 + step, ... of K elements.
+template <int AT>
+__device__ __forceinline__ float low_dot(const void* x, int64_t xr, const void* a, int64_t ar, int K, int v0, int step)
+{
+    constexpr int U = AT == F32 ? 4 : 8;
+    float s = 0.0f;
+    if (K < 8) {
+        if (v0 < K) s = load1<AT>(x, xr + v0) * load1<AT>(a, ar + v0);
+        return s;
+    }
+    const int nvec = (K + 7) / 8;
+    for (; v0 < nvec; v0 += step * U) {
+        Raw8<AT> p[U], q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = vec8(v0 + step * u, K).at;
+            p[u] = load8_any<AT>(x, xr + at);
+            q[u] = load8_any<AT>(a, ar + at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int lo = vec8(v0 + step * u, K).lo;
+            float f[8], g[8];
+            widen8<AT>(p[u], f);
+            widen8<AT>(q[u], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = i >= lo ? __builtin_fmaf(f[i], g[i], s) : s;
+        }
+    }
+    return s;
+}
+
+// k_low_few: h of a few tokens in binary32; two waves per token and rank.  Bound by
+// the latency of its few loads: 1 x 4096, rank 16 3.5 us, 48 x 11008 6.
+template <int AT>
+__global__ __launch_bounds__(512) void k_low_few(const void* __restrict__ x, int64_t ldx, int K, Adapters ad)
+{
+    __shared__ float half[4];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = blockIdx.x * 4 + (w & 3);
+    const int64_t m = blockIdx.y;
+    const int c = adapter_of(ad, m, m + 1);
+    if (c < 0) return;                   // uniform
+    float s = 0.0f;
+    if (r < ad.R)
+        s = wave_sum(low_dot<AT>(x, m * ldx, ad.a, ((int64_t)c * ad.R + r) * K, K, 64 * (w >> 2) + lane, 128));
+    if (w >= 4 && lane == 0) half[w - 4] = s;
+    __syncthreads();
+    if (w < 4 && lane == 0 && r < ad.R)
+        static_cast<float*>(ad.h)[m * ad.ldh + r] = (s + half[w]) * (ad.scale ? ad.scale[c] : 1.0f);
+}
+
+// k_low_tokens: the same in operand order, a workgroup per token, whose sixteen waves
+// take the ranks in turn.
+template <int AT>
+__global__ __launch_bounds__(1024) void k_low_tokens(const void* __restrict__ x, int64_t ldx, int K, Adapters ad)
+{
+    __shared__ float h[AD_R];
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int64_t m = blockIdx.x;
+    const int c = adapter_of(ad, m, m + 1);
+    if (c < 0) return;                   // uniform
+    const float f = ad.scale ? ad.scale[c] : 1.0f;
+    for (int r = w; r < ad.R; r += 16) {
+        const float s = wave_sum(low_dot<AT>(x, m * ldx, ad.a, ((int64_t)c * ad.R + r) * K, K, lane, 64));
+        if (lane == 0) h[r] = s * f;
+    }
+    __syncthreads();
+    constexpr int E = Low<AT>::E;
+    if (t < 4 * Low<AT>::steps(ad)) {
+        float v[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = E * t + k < ad.R ? h[E * t + k] : 0.0f;
+        put_low<AT>(ad, m, t / 4, t & 3, v);
+    }
+}
+
+// k_low_many: many tokens, on the matrix cores.  A workgroup takes 16 of them; its waves
+// take the K axis in turn, 256 bytes of every row at a time (Quad), and their sums meet
+// in LDS.  Workgroups of neighbouring tokens go to one XCD, whose L2 then holds their
+// adapters alone.  Without operand order (ORDER) h is binary32, for the few-token product
+// of a small output.
+template <int AT, int RT, int NWV, bool ORDER>
 __global__ __launch_bounds__(64 * NWV) void k_low_many(const void* __restrict__ x, int64_t ldx, int64_t M, int K,
                                                        Adapters ad)
 {
-    constexpr int STEP = AT == F32 ? 16 : 32, E = STEP / 4, U = 4;    // elements per step and per lane; steps at a time
+    constexpr int ES = AT == F32 ? 4 : 2, STEP = Low<AT>::STEP, E = Low<AT>::E;
+    constexpr int STEPS = 16 * RT > STEP ? 16 * RT / STEP : 1;               // steps of the ranks at a time
     __shared__ float sums[NWV][16][16 * RT + 4];
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l16 = lane & 15, g4 = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const int64_t row = m0 + l16 < M ? m0 + l16 : M - 1;
+    const int64_t T = gridDim.x, xcd = blockIdx.x % 8, left = T % 8;
+    const int64_t m0 = 16 * ((xcd < left ? xcd * (T / 8 + 1) : left + xcd * (T / 8)) + blockIdx.x / 8);
+    const int xlast = M - 1 - m0 < 15 ? (int)(M - 1 - m0) : 15, groups = (int)((int64_t)K * ES / 256);
+    const char* xrows = static_cast<const char*>(x) + m0 * ldx * ES;
     const int id = adapter_of(ad, m0 + l16, M);
-    const int steps = (K + STEP - 1) / STEP;
     for (int r0 = 0; r0 < ad.R; r0 += 16 * RT) {
-        int64_t todo = __ballot(id >= 0) & 0xffff;
+        int todo = (int)(__ballot(id >= 0) & 0xffff);
         while (todo) {                   // uniform
-            const int c = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-            todo &= ~__ballot(id == c);
+            const int c = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+            todo &= ~(int)__ballot(id == c);
+            const float f = ad.scale ? ad.scale[c] : 1.0f;
             v4f acc[RT];
+            const char* arows[RT];
+            int alast[RT];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) acc[j] = v4f{};
-            for (int s0 = w * U; s0 < steps; s0 += NWV * U) {
-                uint4 xv[U], av[U][RT];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int k = (s0 + u) * STEP + g4 * E;
-                    xv[u] = chunk_of<AT>(x, row * ldx, k, K);
-#pragma unroll
-                    for (int j = 0; j < RT; ++j) {
-                        const int r = r0 + 16 * j + l16;
-                        av[u][j] = chunk_of<AT>(ad.a, ((int64_t)c * ad.R + (r < ad.R ? r : ad.R - 1)) * K, k, K);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int j = 0; j < RT; ++j) acc[j] = add_low<AT>(av[u][j], xv[u], acc[j]);
+            for (int j = 0; j < RT; ++j) {
+                const int r = r0 + 16 * j < ad.R ? r0 + 16 * j : ad.R - 1;
+                acc[j] = v4f{};
+                arows[j] = static_cast<const char*>(ad.a) + ((int64_t)c * ad.R + r) * K * ES;
+                alast[j] = ad.R - 1 - r < 15 ? ad.R - 1 - r : 15;
             }
+            const auto xa = quad_at(xlast, (uint64_t)(ldx * ES));
+            for (int g = w; g < groups; g += NWV) {
+                Quad xv, av[RT];
+                quad_load(xv, xrows + g * 256, xa);
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+                    quad_load(av[j], arows[j] + g * 256, quad_at(alast[j], (uint32_t)(K * ES)));
+                __builtin_amdgcn_sched_barrier(0);       // every load is on its way
+                change_places(xv);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) {
+                    change_places(av[j]);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) acc[j] = add_low<AT>(av[j].r[s], xv.r[s], acc[j]);
+                }
+            }
+            if (groups % NWV == w)
+                for (int k = groups * (256 / ES); k < K; k += STEP) {        // the rest of K
+                    const uint4 xv = chunk_of<AT>(xrows, (int64_t)(l16 < xlast ? l16 : xlast) * ldx, k + g4 * E, K);
+#pragma unroll
+                    for (int j = 0; j < RT; ++j)
+                        acc[j] = add_low<AT>(chunk_of<AT>(arows[j], (int64_t)(l16 < alast[j] ? l16 : alast[j]) * K,
+                                                          k + g4 * E, K), xv, acc[j]);
+                }
             // lane l holds ranks 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
             for (int j = 0; j < RT; ++j) *reinterpret_cast<v4f*>(&sums[w][l16][16 * j + 4 * g4]) = acc[j];
             __syncthreads();
-            const float f = ad.scale ? ad.scale[c] : 1.0f;
-            for (int o = t; o < 256 * RT; o += 64 * NWV) {
-                const int m = o / (16 * RT), r = o % (16 * RT);
-                if (adapter_of(ad, m0 + m, M) != c || r0 + r >= ad.R) continue;
+            auto value = [&](int m, int r) {
                 float v = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NWV; ++i) v += sums[i][m][r];
-                ad.h[(m0 + m) * ad.ldh + r0 + r] = v * f;
+                return v * f;
+            };
+            if constexpr (ORDER) {
+                const int m = t / (4 * STEPS), g = t % (4 * STEPS);
+                if (m < 16 && adapter_of(ad, m0 + m, M) == c && r0 + g / 4 * STEP < ad.R) {
+                    float v[E];
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        const int r = E * g + k;
+                        v[k] = r < 16 * RT && r0 + r < ad.R ? value(m, r) : 0.0f;
+                    }
+                    put_low<AT>(ad, m0 + m, r0 / STEP + g / 4, g & 3, v);
+                }
+            } else {
+                for (int o = t; o < 256 * RT; o += 64 * NWV) {
+                    const int m = o / (16 * RT), r = o % (16 * RT);
+                    if (adapter_of(ad, m0 + m, M) == c && r0 + r < ad.R)
+                        static_cast<float*>(ad.h)[(m0 + m) * ad.ldh + r0 + r] = value(m, r);
+                }
             }
             __syncthreads();
         }
@@ -180,7 +315,7 @@ __global__ __launch_bounds__(64 * NWV) void k_low_many(const void* __restrict__ 
 template <int AT>
 __device__ __forceinline__ float low_output(const Adapters& ad, int64_t m, int c, int64_t n, int64_t N)
 {
-    const float* h = ad.h + m * ad.ldh;
+    const float* h = static_cast<const float*>(ad.h) + m * ad.ldh;
     const int64_t at = ((int64_t)c * N + n) * ad.R;
     float s = 0.0f;
 #pragma unroll 2
@@ -221,20 +356,13 @@ __global__ __launch_bounds__(64 * NWV) void k_adapt_few(const int8_t* __restrict
         osw = e.sw[on];
         ob = load1_rt(e.bias, e.bias_dt, on, 0.0f);
     }
-    const int8_t* pw[CT];
-    const int8_t* px[MT];
+    Rows16 weights[CT], tokens[MT];
 #pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int64_t n = n0 + 16 * j + l16;
-        pw[j] = qw + (n < e.N ? n : e.N - 1) * K;
-    }
+    for (int j = 0; j < CT; ++j) weights[j] = rows16_of(qw, e.N, n0 + 16 * j, K);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + l16;
-        px[i] = qx + (m < e.M ? m : e.M - 1) * K;
-    }
+    for (int i = 0; i < MT; ++i) tokens[i] = rows16_of(qx, e.M, m0 + 16 * i, K);
     v4i acc[MT][CT];
-    few_product<MT, CT, NWV, U>(pw, px, K, acc);
+    few_product<MT, CT, NWV, U>(weights, tokens, K, acc);
     // lane l holds columns 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -256,8 +384,9 @@ __global__ __launch_bounds__(64 * NWV) void k_adapt_few(const int8_t* __restrict
         int s = 0;
 #pragma unroll
         for (int v = 0; v < NWV; ++v) s += sums[v][m][t % COLS];
-        float v = (float)s * osx[i] * osw + low[i];
+        float v = (float)s * osx[i] * osw;
         if (e.bias) v += ob;
+        v += low[i];
         const int64_t at = (m0 + m) * e.N + on;
         if (e.z) store1<YT>(e.z, at, v);
         with_act(e.act, [&](auto a) { v = act1<decltype(a)::value>(v); });
@@ -267,171 +396,273 @@ __global__ __launch_bounds__(64 * NWV) void k_adapt_few(const int8_t* __restrict
 }
 
 // --------------------------------------------------- the product, many tokens
-// A staged half of a wave's sums, 32 tokens of 16 NN columns: scaled where it lies,
-// and their adapters' parts added, an adapter and a step of ranks at a time.
-struct AdaptDelta {
-    static constexpr bool ADDS = true;
-    Adapters ad;
+// A wave finishes its part 32 tokens at a time, in its own part of LDS: the scaled sums
+// and the bias go there, the matrix cores' adapter parts are added to them, an adapter
+// and a step of ranks at a time, and from there the values leave in whole rows.  A step's
+// h is loaded while the tokens before it leave; b's rows, whose loads cost the address
+// unit a lane per clock, stay in registers, up to HELD steps of them, while the adapter
+// does.
+template <int NM>
+struct Ids {
+    int of[(NM + 3) / 4];                // lane l: the adapter of token 64 i + l of a wave's part
+};
 
-    // `at` is the lane's first value of a tile of 16 tokens and 16 columns, `tile` apart to the next 16 tokens.
-    template <int AT, int NN>
-    __device__ __forceinline__ void add(const Epi& e, const int (&id)[2], int64_t row0, int64_t n0, float* at,
-                                        int tile) const
+template <int YT, int AT, int NM, int NN>
+struct AdaptPart {
+    using S = Stage<NM, NN>;
+    static constexpr int STEP = Low<AT>::STEP, E = Low<AT>::E, PIECES = Low<AT>::PIECES;
+    static constexpr int HELD = NN >= 4 && AT != F32 && YT != F32 ? 2 : 1;   // steps of b that fit in registers
+    static constexpr int IDS = S::INTS, SW = IDS + 16 * NM, BIAS = SW + 16 * NN, INTS = BIAS + 16 * NN;   // in ints
+
+    const Epi& e;
+    const Adapters& ad;
+    const int64_t m0, n0;
+    int* const stage;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+    // the present step: of which 32 tokens, whose, from which rank on; the tokens still to be looked at, and their adapters
+    int half = 0, c = 0, r0 = 0, id[2] = {};
+    uint32_t todo = 0;
+    bool have = false;
+    int whose = -1, from = -1;           // b: this adapter's HELD steps from this rank on
+    uint4 b[HELD][NN], h[2][PIECES];
+    int up[2];
+
+    __device__ __forceinline__ uint32_t tokens(bool first, bool second) const
     {
-        constexpr int STEP = AT == F32 ? 16 : 32, E = STEP / 4;
-        const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
-        // f16: h relative to a power of two near its row's largest value
-        int up[2] = {0, 0};
-        if constexpr (AT == F16) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float most = 0.0f;
-                if (id[t] >= 0)
-                    for (int r = g4; r < ad.R; r += 4)
-                        most = __builtin_fmaxf(most, __builtin_fabsf(ad.h[(row0 + 16 * t) * ad.ldh + r]));
-                most = __builtin_fmaxf(most, lane_get(most, 16));
-                most = __builtin_fmaxf(most, lane_get(most, 32));
-                up[t] = most > 0.0f && most < __builtin_inff() ? __builtin_amdgcn_frexp_expf(most) : 0;
+        return (uint32_t)(__ballot(first) & 0xffff) | (uint32_t)(__ballot(second) & 0xffff) << 16;
+    }
+    __device__ __forceinline__ void enter()
+    {
+        id[0] = stage[IDS + 32 * half + l16];
+        id[1] = stage[IDS + 32 * half + 16 + l16];
+        todo = tokens(id[0] >= 0, id[1] >= 0);
+    }
+    // The next adapter (uniform).
+    __device__ __forceinline__ void pop()
+    {
+        while (!todo) {
+            if (++half >= NM / 2) {
+                have = false;
+                return;
             }
+            enter();
         }
-        uint32_t todo = (uint32_t)(__ballot(id[0] >= 0) & 0xffff) | (uint32_t)(__ballot(id[1] >= 0) & 0xffff) << 16;
-        while (todo) {                   // uniform
-            const int lead = __builtin_ctz(todo);
-            const int c = lead < 16 ? __builtin_amdgcn_readlane(id[0], lead)
-                                    : __builtin_amdgcn_readlane(id[1], lead - 16);
-            todo &= ~((uint32_t)(__ballot(id[0] == c) & 0xffff) | (uint32_t)(__ballot(id[1] == c) & 0xffff) << 16);
-#pragma unroll 1
-            for (int r0 = 0; r0 < ad.R; r0 += STEP) {
-                const int r = r0 + E * g4;
-                uint4 b[NN];
+        const int lead = __builtin_ctz(todo);
+        c = lead < 16 ? __builtin_amdgcn_readlane(id[0], lead) : __builtin_amdgcn_readlane(id[1], lead - 16);
+        todo &= ~tokens(id[0] == c, id[1] == c);
+        r0 = 0;
+        have = true;
+    }
+    __device__ __forceinline__ void fetch()
+    {
+        if (!have) return;
+        const int pair = r0 / (HELD * STEP) * (HELD * STEP);
+        if (whose != c || from != pair) {        // uniform
+            whose = c;
+            from = pair;
 #pragma unroll
-                for (int j = 0; j < NN; ++j) {
-                    const int64_t n = n0 + 16 * j + l16;
-                    b[j] = chunk_of<AT>(ad.b, ((int64_t)c * e.N + (n < e.N ? n : e.N - 1)) * ad.R, r, ad.R);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const bool mine = id[t] == c;
-                    float h[E];
-#pragma unroll
-                    for (int i = 0; i < E; i += 4) {
-                        float4 v = make_float4(0, 0, 0, 0);
-                        if (mine && r + i < ad.R)
-                            v = *reinterpret_cast<const float4*>(ad.h + (row0 + 16 * t) * ad.ldh + r + i);
-                        h[i] = v.x;
-                        h[i + 1] = r + i + 1 < ad.R ? v.y : 0.0f;
-                        h[i + 2] = r + i + 2 < ad.R ? v.z : 0.0f;
-                        h[i + 3] = r + i + 3 < ad.R ? v.w : 0.0f;
-                    }
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (AT == F32) {
-                            hi[i] = as_u(h[i]);
-                        } else {
-                            float p = h[2 * i], q = h[2 * i + 1];
-                            if constexpr (AT == F16) {
-                                p = __builtin_amdgcn_ldexpf(p, -up[t]);
-                                q = __builtin_amdgcn_ldexpf(q, -up[t]);
-                            }
-                            hi[i] = narrow2<AT>(p, q);
-                            Raw8<AT> back = {};
-                            back.w[0].x = hi[i];
-                            float wide[8];
-                            widen8<AT>(back, wide);
-                            // an infinite or NaN hi is all there is
-                            lo[i] = narrow2<AT>(__builtin_fabsf(wide[0]) < __builtin_inff() ? p - wide[0] : 0.0f,
-                                                __builtin_fabsf(wide[1]) < __builtin_inff() ? q - wide[1] : 0.0f);
-                        }
-                    }
+            for (int s = 0; s < HELD; ++s) {
+                const int r = pair + STEP * s + E * g4;
+                if (pair + STEP * s < ad.R)
 #pragma unroll
                     for (int j = 0; j < NN; ++j) {
-                        v4f d = add_low<AT>(b[j], make_uint4(hi[0], hi[1], hi[2], hi[3]), v4f{});
-                        if constexpr (AT != F32) d = add_low<AT>(b[j], make_uint4(lo[0], lo[1], lo[2], lo[3]), d);
-                        v4f* z = reinterpret_cast<v4f*>(at + t * tile + 16 * j);
-                        if constexpr (AT == F16) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_ldexpf(d[i], up[t]);
-                        }
-                        if (mine) *z += d;
+                        const int64_t n = n0 + 16 * j + l16, at = ((int64_t)c * e.N + (n < e.N ? n : e.N - 1)) * ad.R;
+                        // without a branch; only a rank that is no multiple of a chunk ends inside one
+                        if (ad.R % E == 0) b[s][j] = whole_chunk<AT>(ad.b, at + (r < ad.R ? r : 0));    // uniform
+                        else b[s][j] = chunk_of<AT>(ad.b, at, r, ad.R);
                     }
-                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int64_t row = m0 + 32 * half + 16 * t, tile = (row < e.M ? row : e.M - 1) / 16;
+            const uint4* p = Low<AT>::piece(ad, tile, r0 / STEP) + lane;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) h[t][i] = p[64 * i];
+            if constexpr (AT == F16) {
+                const int64_t m = row + l16 < e.M ? row + l16 : e.M - 1;
+                up[t] = ad.up[m * Low<AT>::steps(ad) + r0 / STEP];
             }
         }
     }
-
-    template <int NM, int NN>
-    __device__ __forceinline__ void apply(const Epi& e, int64_t m0, int64_t n0, int half, int* stage) const
+    __device__ __forceinline__ void add_step(uint4 (&w)[NN])
     {
-        using S = Stage<NM, NN>;
-        const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
-        const int64_t row0 = m0 + 32 * half + l16;
-        const int id[2] = {adapter_of(ad, row0, e.M), adapter_of(ad, row0 + 16, e.M)};
-        int* at = stage + l16 * S::PITCH + 4 * g4;
-        const float* sx = reinterpret_cast<const float*>(stage + 32 * S::PITCH) + 32 * half + l16;
+        if (r0 + E * g4 >= ad.R)
 #pragma unroll
-        for (int j = 0; j < NN; ++j) {
-            const int64_t n = n0 + 16 * j + 4 * g4;
-            float sw[4];
+            for (int j = 0; j < NN; ++j) w[j] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sw[i] = n + i < e.N ? e.sw[n + i] : 0.0f;
+        for (int t = 0; t < 2; ++t) {
+            const bool mine = stage[IDS + 32 * half + 16 * t + l16] == c;
+            uint4 x[PIECES];
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+                x[i] = make_uint4(mine ? h[t][i].x : 0, mine ? h[t][i].y : 0, mine ? h[t][i].z : 0, mine ? h[t][i].w : 0);
+#pragma unroll
+            for (int j = 0; j < NN; ++j) {
+                v4f d = v4f{};
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) d = add_low<AT>(w[j], x[i], d);
+                if constexpr (AT == F16) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) d[k] = __builtin_amdgcn_ldexpf(d[k], up[t]);
+                }
+                v4f* z = reinterpret_cast<v4f*>(&stage[(16 * t + l16) * S::PITCH + 16 * j + 4 * g4]);
+                if (mine) *z += d;
+            }
+            __builtin_amdgcn_sched_barrier(0);   // sixteen tokens at a time, in few registers
+        }
+    }
+    // Adds the present step, and asks for the next.
+    __device__ __forceinline__ void add()
+    {
+        if (r0 / STEP % HELD == 0) add_step(b[0]);       // uniform
+        else add_step(b[HELD - 1]);
+        r0 += STEP;
+        if (r0 >= ad.R) pop();
+        fetch();
+    }
+
+    // Eight columns of a row on their way out.
+    template <bool NTS>
+    __device__ __forceinline__ void leave(const Cols8& cc, int64_t row, const int* from) const
+    {
+        Raw8<YT> res = {};
+        if (YT != F32 && e.res) res = residual8<YT>(e, cc, row);
+        const v4f s0 = *reinterpret_cast<const v4f*>(from), s1 = *reinterpret_cast<const v4f*>(from + 4);
+        float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
+        const int64_t at = row * e.N + cc.col;
+        if (e.z) store8_first<YT>(e.z, at, cc.n, v);
+        act8(e.act, v);
+        if (e.res) {
+            if constexpr (YT == F32) res = residual8<YT>(e, cc, row);    // its registers are taken until here
+            float w[8];
+            widen8<YT>(res, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += w[i];
+        }
+        if (cc.n == 8) store8_any<YT, NTS>(e.y, at, v);
+        else store8_first<YT>(e.y, at, cc.n, v);
+    }
+
+    template <bool NTS>
+    __device__ __forceinline__ void finish(const v4i (&acc)[NM][NN], const Ids<NM>& ids)
+    {
+        if (m0 >= e.M) return;           // uniform
+#pragma unroll
+        for (int i = 0; i < NM; i += 4)
+            if (16 * i + lane < 16 * NM) stage[IDS + 16 * i + lane] = ids.of[i / 4];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        enter();
+        pop();
+        fetch();
+        stage_scales<NM, NN>(e, m0, stage);
+        if (lane < 16 * NN) {
+            const int64_t n = n0 + lane < e.N ? n0 + lane : e.N - 1;
+            stage[SW + lane] = (int)as_u(e.sw[n]);
+            stage[BIAS + lane] = (int)as_u(load1_rt(e.bias, e.bias_dt, n, 0.0f));
+        }
+        const float* sx = reinterpret_cast<const float*>(stage + 32 * S::PITCH);
+        Cols8 cc = {};
+        cc.col = n0 + 8 * (lane % S::LPR);
+        cc.n = e.N - cc.col >= 8 ? 8 : e.N - cc.col > 0 ? (int)(e.N - cc.col) : 0;
+#pragma unroll
+        for (int p = 0; p < NM / 2; ++p) {
+            const int64_t mh = m0 + 32 * p;
+            if (mh >= e.M) return;       // uniform
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const v4i s = *reinterpret_cast<const v4i*>(at + 16 * t * S::PITCH + 16 * j);
-                const float f = sx[16 * t];
-                v4i z;
+                const float f = sx[32 * p + 16 * t + l16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = (int)as_u((float)s[i] * f * sw[i]);
-                *reinterpret_cast<v4i*>(at + 16 * t * S::PITCH + 16 * j) = z;
+                for (int j = 0; j < NN; ++j) {
+                    const v4f sw = *reinterpret_cast<const v4f*>(stage + SW + 16 * j + 4 * g4);
+                    v4f z;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) z[k] = (float)acc[2 * p + t][j][k] * f * sw[k];
+                    if (e.bias) {
+                        const v4f bias = *reinterpret_cast<const v4f*>(stage + BIAS + 16 * j + 4 * g4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) z[k] += bias[k];
+                    }
+                    *reinterpret_cast<v4f*>(&stage[(16 * t + l16) * S::PITCH + 16 * j + 4 * g4]) = z;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+            while (have && half == p) add();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const int rows = cc.n == 0 ? 0 : e.M - mh < 32 ? (int)(e.M - mh) : 32;
+#pragma unroll 1
+            for (int r = lane / S::LPR; r < rows; r += S::RPI)
+                leave<NTS>(cc, mh + r, stage + r * S::PITCH + 8 * (lane % S::LPR));
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        float* zf = reinterpret_cast<float*>(at);
-        if (ad.dt == F32) add<F32, NN>(e, id, row0, n0, zf, 16 * S::PITCH);
-        else if (ad.dt == BF16) add<BF16, NN>(e, id, row0, n0, zf, 16 * S::PITCH);
-        else add<F16, NN>(e, id, row0, n0, zf, 16 * S::PITCH);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 };
 
 template <int YT>
 struct AdaptTile : Epi {
     static constexpr bool GATED = false;
-    AdaptDelta delta;
+    Adapters ad;
     static __device__ __forceinline__ const int8_t* second_weight(const int8_t* first) { return first; }
     template <int TILE, int WM, int WN>
     static constexpr int staging()
     {
-        return 4 * WM * WN * Stage<TILE / WM / 16, TILE / WN / 16>::INTS;
+        return 4 * WM * WN * AdaptPart<YT, F32, TILE / WM / 16, TILE / WN / 16>::INTS;
+    }
+    template <int TILE, int WM, int WN>
+    static __device__ __forceinline__ Ids<TILE / WM / 16> early(const AdaptTile& e, int64_t m0)
+    {
+        Ids<TILE / WM / 16> ids;
+        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < (TILE / WM / 16 + 3) / 4; ++i)
+            ids.of[i] = adapter_of(e.ad, m0 + TILE / WM * (w / WN) + 64 * i + (threadIdx.x & 63), e.M);
+        return ids;
     }
     template <int TILE, int WM, int WN>
     static __device__ __forceinline__ void finish(const AdaptTile& e, int64_t m0, int64_t n0,
-                                                  const v4i (&acc)[TILE / WM / 16][TILE / WN / 16], uint8_t* lds)
+                                                  const v4i (&acc)[TILE / WM / 16][TILE / WN / 16], uint8_t* lds,
+                                                  const Ids<TILE / WM / 16>& ids)
     {
         constexpr int NM = TILE / WM / 16, NN = TILE / WN / 16;
         const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        finish_part<YT, NM, NN, TILE == 256>(e, m0 + TILE / WM * (w / WN), n0 + TILE / WN * (w % WN), acc,
-                                             reinterpret_cast<int*>(lds) + w * Stage<NM, NN>::INTS, e.delta);
+        const int64_t m = m0 + TILE / WM * (w / WN), n = n0 + TILE / WN * (w % WN);
+        int* stage = reinterpret_cast<int*>(lds) + w * AdaptPart<YT, F32, NM, NN>::INTS;
+        constexpr bool NTS = TILE == 256;
+        if (e.ad.dt == F32) AdaptPart<YT, F32, NM, NN>{e, e.ad, m, n, stage}.template finish<NTS>(acc, ids);
+        else if (e.ad.dt == BF16) AdaptPart<YT, BF16, NM, NN>{e, e.ad, m, n, stage}.template finish<NTS>(acc, ids);
+        else AdaptPart<YT, F16, NM, NN>{e, e.ad, m, n, stage}.template finish<NTS>(acc, ids);
     }
 };
 
 // ---------------------------------------------------------------- launches
-// A wave per token and rank reads an adapter's rows anew for every token; the matrix
-// cores take sixteen tokens at once, but in M / 16 workgroups only.
-constexpr int64_t LOW_FEW = 128;
+// Up to LOW_FEW tokens times ranks every token reads its adapter's rows for itself, which
+// does not mind whose they are; beyond, the matrix cores.
+constexpr int64_t LOW_FEW = 8192;
 
 template <int AT>
-static void low_launch(const void* x, int64_t ldx, int64_t M, int64_t K, const Adapters& ad, hipStream_t st)
+static void low_launch(const void* x, int64_t ldx, int64_t M, int64_t K, bool few, const Adapters& ad, hipStream_t st)
 {
-    if (M <= LOW_FEW) {
-        hipLaunchKernelGGL((k_low_few<AT>), dim3((unsigned)cdiv(ad.R, 4), (unsigned)M), dim3(256), 0, st, x, ldx, (int)K,
-                           ad);
+    if (M * ad.R <= LOW_FEW) {
+        if (few)
+            hipLaunchKernelGGL((k_low_few<AT>), dim3((unsigned)cdiv(ad.R, 4), (unsigned)M), dim3(512), 0, st, x, ldx,
+                               (int)K, ad);
+        else hipLaunchKernelGGL((k_low_tokens<AT>), dim3((unsigned)M), dim3(1024), 0, st, x, ldx, (int)K, ad);
         return;
     }
     const dim3 grid((unsigned)cdiv(M, 16));
-    if (ad.R <= 16) hipLaunchKernelGGL((k_low_many<AT, 1, 16>), grid, dim3(1024), 0, st, x, ldx, M, (int)K, ad);
-    else if (ad.R <= 32) hipLaunchKernelGGL((k_low_many<AT, 2, 16>), grid, dim3(1024), 0, st, x, ldx, M, (int)K, ad);
-    else hipLaunchKernelGGL((k_low_many<AT, 4, 8>), grid, dim3(512), 0, st, x, ldx, M, (int)K, ad);
+#define TQ_LOW(RT, NWV)                                                                                             \
+    do {                                                                                                            \
+        if (few)                                                                                                    \
+            hipLaunchKernelGGL((k_low_many<AT, RT, NWV, false>), grid, dim3(64 * NWV), 0, st, x, ldx, M, (int)K, ad);   \
+        else                                                                                                        \
+            hipLaunchKernelGGL((k_low_many<AT, RT, NWV, true>), grid, dim3(64 * NWV), 0, st, x, ldx, M, (int)K, ad);    \
+    } while (0)
+    if (ad.R <= 16) TQ_LOW(1, 16);
+    else if (ad.R <= 32) TQ_LOW(2, 8);
+    else TQ_LOW(4, 8);
+#undef TQ_LOW
 }
 
 // The kernel of a product, by the rule of the product without adapters
@@ -447,12 +678,13 @@ static void adapt_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Ep
         hipLaunchKernelGGL((k_adapt_few<YT, MT, CT, NWV, U>), grid, dim3(64 * NWV), 0, st, qx, qw, K, e, ad);   \
         return;                                                                                                 \
     } while (0)
-    if (e.M <= 16) TQ_FEW(1, 1, 8, 4);
-    if ((e.M <= 32 && (e.N <= 6144 || !rows16)) || (rows16 && cdiv(e.M, 32) * cdiv(e.N, 16) <= 256))
-        TQ_FEW(2, 1, 8, 2);
-    if (rows16 && cdiv(e.M, 32) * cdiv(e.N, 32) <= 256) TQ_FEW(2, 2, 8, 2);
+    if (few_tokens(e.M, e.N)) {
+        if (e.M <= 16) TQ_FEW(1, 1, 8, 2);
+        if (few_columns(e.M, e.N)) TQ_FEW(2, 1, 8, 1);
+        TQ_FEW(2, 2, 8, 1);
+    }
 #undef TQ_FEW
-    const AdaptTile<YT> tile = {e, {ad}};
+    const AdaptTile<YT> tile = {e, ad};
     if (rows16) {
 #define TQ_RING(TILE, RING, WM, WN, WGS)                                                                        \
     do {                                                                                                        \
@@ -476,15 +708,22 @@ static void adapt_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Ep
         hipLaunchKernelGGL((k_epi_tile<AdaptTile<YT>, TILE, WM, WN, D, WGS>), dim3((unsigned)(nt * mt)),        \
                            dim3(64 * WM * WN), 0, st, qx, qw, K, nt, mt, slab, tile);                           \
     } while (0)
-    if (cdiv(e.M, 256) * cdiv(e.N, 256) > 160) TQ_TILE(256, 2, 4, 2, 1);
-    else if (cdiv(e.M, 64) * cdiv(e.N, 64) > 512) TQ_TILE(128, 2, 4, 2, 2);
+    if constexpr (YT != F32)             // with binary32 outputs the 256 tile's registers do not suffice
+        if (cdiv(e.M, 256) * cdiv(e.N, 256) > 160) {
+            TQ_TILE(256, 2, 4, 2, 1);
+            return;
+        }
+    if (cdiv(e.M, 64) * cdiv(e.N, 64) > 512) TQ_TILE(128, 2, 4, 2, 2);
     else TQ_TILE(64, 2, 2, 4, 2);
 #undef TQ_TILE
 }
 
 static bool natural(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(ftype_size(dt) - 1)) == 0; }
 static bool valid_act(int a) { return a >= TQ_ACT_NONE && a <= TQ_ACT_GELU_TANH; }
+// Bytes of h: whole tiles of 16 tokens and steps of 32 ranks in 4 bytes each, which also
+// holds binary32 rows of a multiple of 8 ranks, and an exponent per token and step behind.
 inline int64_t low_ld(int64_t rank) { return cdiv(rank, 8) * 8; }
+inline size_t low_bytes(int64_t M, int64_t rank) { return (size_t)(cdiv(M, 16) * 16) * (size_t)(cdiv(rank, 32) * 32) * 4; }
 
 }  // namespace tq
 
@@ -494,7 +733,7 @@ extern "C" {
 
 size_t tq_w8a8_linear_adapters_workspace_bytes(int64_t M, int64_t rank)
 {
-    return M > 0 && rank > 0 ? (size_t)M * (size_t)low_ld(rank) * sizeof(float) : 0;
+    return M > 0 && rank > 0 ? low_bytes(M, rank) + (size_t)M * (size_t)cdiv(rank, 32) * sizeof(int) : 0;
 }
 
 tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stride, const int8_t* qx, const float* sx,
@@ -523,10 +762,11 @@ tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stri
     if (!workspace || workspace_bytes < tq_w8a8_linear_adapters_workspace_bytes(M, rank)) return TQ_ERR_INVALID;
     if (!aligned16(workspace)) return TQ_ERR_ALIGN;
     const Epi e = {sx, sw, bias, bias_dtype, act, residual, residual_row_stride, y, preact, M, N};
-    const Adapters ad = {adapter, a, b, scale, static_cast<float*>(workspace), (int)adapters, (int)rank,
-                         (int)low_ld(rank), x_dtype};
+    const Adapters ad = {adapter, a, b, scale, workspace, reinterpret_cast<int*>(static_cast<char*>(workspace) +
+                         low_bytes(M, rank)), (int)adapters, (int)rank, (int)low_ld(rank), x_dtype};
     hipStream_t st = as_stream(stream);
-    TQ_LLM_FT_SWITCH(x_dtype, low_launch<FTV>(x, x_row_stride, M, K, ad, st));
+    const bool few = few_tokens(M, N);
+    TQ_LLM_FT_SWITCH(x_dtype, low_launch<FTV>(x, x_row_stride, M, K, few, ad, st));
     TQ_LLM_FT_SWITCH(y_dtype, adapt_launch<FTV>(qx, qw, K, e, ad, st));
     return launch_status();
 }

@@ -14,15 +14,10 @@ namespace tq {
 // ------------------------------------------------------------- a few tokens
 // k_epi_few: a few tokens, bound by the weights, which are read once; or an
 // output of few elements.  A workgroup of NWV waves owns 16 CT output columns of
-// 16 MT tokens; the waves take the K axis in turn, 128 codes at a time, so that a wave's two loads use whole 128-byte
-// lines; the sums meet in LDS, one thread per output.  The weights are the
-// matrix core's first operand (16 columns), the tokens its second (16 tokens;
-// rows past the end repeat the last), U blocks of both in flight per wave.  What an
-// output's epilogue needs is loaded before the weights are.  Kernel times: 1 x
-// 11008 x 4096 10.2 us (4.4 TB/s of weights), 16 x 4096 x 11008 12.2 (3.7): with
-// 256 workgroups each CU has one slice of 16 columns, whose first loads and
-// last sums nothing covers.  Refilling each of the U slots as it is used instead
-// of all at once: 13.3 -> 12.2 us.
+// 16 MT tokens (few_product); the waves' sums meet in LDS, one thread per output.  What
+// an output's epilogue needs is loaded before the weights are.  With 256 workgroups
+// each CU has one slice of 16 columns, whose first loads and last sums nothing covers:
+// 16 x 4096 x 11008 10.6 us (4.3 TB/s of weights).
 template <int YT, int MT, int CT, int NWV, int U>
 __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__ qx, const int8_t* __restrict__ qw,
                                                       int64_t K, Epi e)
@@ -51,20 +46,13 @@ __global__ __launch_bounds__(64 * NWV) void k_epi_few(const int8_t* __restrict__
         ob = load1_rt(e.bias, e.bias_dt, on, 0.0f);
     }
 
-    const int8_t* pw[CT];
-    const int8_t* px[MT];
+    Rows16 weights[CT], tokens[MT];
 #pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int64_t n = n0 + 16 * j + l16;
-        pw[j] = qw + (n < e.N ? n : e.N - 1) * K;
-    }
+    for (int j = 0; j < CT; ++j) weights[j] = rows16_of(qw, e.N, n0 + 16 * j, K);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + l16;
-        px[i] = qx + (m < e.M ? m : e.M - 1) * K;
-    }
+    for (int i = 0; i < MT; ++i) tokens[i] = rows16_of(qx, e.M, m0 + 16 * i, K);
     v4i acc[MT][CT];
-    few_product<MT, CT, NWV, U>(pw, px, K, acc);
+    few_product<MT, CT, NWV, U>(weights, tokens, K, acc);
     // lane l holds columns 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -125,8 +113,13 @@ struct EpiTile : Epi {
         return 4 * WM * WN * Stage<TILE / WM / 16, TILE / WN / 16>::INTS;
     }
     template <int TILE, int WM, int WN>
+    static __device__ __forceinline__ int early(const Epi&, int64_t)
+    {
+        return 0;
+    }
+    template <int TILE, int WM, int WN>
     static __device__ __forceinline__ void finish(const Epi& e, int64_t m0, int64_t n0,
-                                                  const v4i (&acc)[TILE / WM / 16][TILE / WN / 16], uint8_t* lds)
+                                                  const v4i (&acc)[TILE / WM / 16][TILE / WN / 16], uint8_t* lds, int)
     {
         constexpr int NM = TILE / WM / 16, NN = TILE / WN / 16;
         const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -246,24 +239,23 @@ inline int64_t epi_chunk(int64_t M, int64_t N)
     return cdiv(cdiv(M, chunks), 16) * 16;
 }
 
-// The kernel of a product, by its shape.  Measured (us, K = 4096 unless given;
-// few tokens / 64 / 128 / 256 tile):
-//   24 x 4096      8.3 / 11.9 / 18 / 46      32 x 11008    19.2 / 11.9 / 21 / 47
-//   64 x 11008      30 / 12.0 / 21 / 49      512 x 4096       - / 16.6 / 19.5 / -
-//   640 x 4096       - / 24.5 / 20.0 / -     2048 x 4096      - / - / 35 / 51
-//   4096 x 4096      - / - / 87 / 60
-// The few-token kernel reads the tokens again for every 16 columns, which costs
-// more the more columns there are.  A tile kernel takes a time of its own per
-// round of resident workgroups (two 64 x 64 tiles or, up to 256 of them, one
-// 128 x 128 tile per CU), so the smallest tile that needs one round is taken,
-// and the largest once it fills the chip.  128 x 128 tiles beyond one round run
-// two to a CU on shorter rings.  Where the output is so small that tiles leave
-// most CUs idle, its 32 x 16 or 32 x 32 pieces, each with the K axis split over
-// eight waves, do not (tiles / 32 x 16 / 32 x 32):
-//   220 x 507 x 10256   27 / 13.4 / 17.1     40 x 1024 x 8192     17.8 / 12.9 / 16.6
-//   64 x 4096 x 4096  11.1 / 13.3 / 9.9      1260 x 140 x 10688   23.4 / 26 / 17.2
-//   128 x 4096 x 4096 11.2 / 24 / 16.9       220 x 507 x 10250    34 / 42 / 55
-// (the last with rows at odd addresses, whose loads cost these kernels more).
+// The kernel of a product, by its shape.  Measured (us, K = 4096; 64 / 128 / 256 tile):
+//   512 x 4096     16.6 / 19.5 / -     640 x 4096     24.5 / 20.0 / -
+//   2048 x 4096       - / 35 / 51      4096 x 4096       - / 87 / 60
+// A tile kernel takes a time of its own per round of resident workgroups (two 64 x 64
+// tiles or, up to 256 of them, one 128 x 128 tile per CU), so the smallest tile that
+// needs one round is taken, and the largest once it fills the chip.  128 x 128 tiles
+// beyond one round run two to a CU on shorter rings.  Where the output is so small that
+// tiles leave most CUs idle, its 32 x 16 or 32 x 32 pieces, each with the K axis split
+// over eight waves, do not (few_tokens; us, 32 x 16 / 32 x 32 / 64 tile):
+//   24 x 4096 x 4096    8.5 /  8.4 / 11.7     220 x 507 x 10256   10.2 / 12.2 / 27.2
+//   24 x 11008 x 4096  13.4 / 14.6 / 12.7     40 x 1024 x 8192     8.2 /  8.7 / 18.1
+//   48 x 11008 x 4096  20.5 / 18.9 / 12.7     1260 x 140 x 10688  23.3 / 16.4 / 23.3
+//   64 x 4096 x 4096   10.5 /  8.3 / 11.3     48 x 4096 x 11008      - / 13.8 / 25.8
+//   128 x 4096 x 4096  15.5 / 12.5 / 11.2     512 x 512 x 90       8.4 /    - /  8.3
+// and with rows at odd addresses
+//   24 x 11008 x 4090  26.4 / 27.0 / 23.4     48 x 4096 x 4095       - / 15.5 / 19.6
+//   220 x 507 x 10250  13.6 / 17.2 / 34.2     243 x 1000 x 9000      - / 12.6 / 26.1
 // Operands of other alignments (k_epi_tile, us; 64 / 128 / 256 tile):
 //   243 x 2546 x 9000    26.7 / 51 / -      777 x 4096 x 4095     57 / 35 / 81
 //   2564 x 614 x 2708    20.5 / 21.8 / -    2048 x 4096 x 4098    87 / 58 / 75
@@ -279,10 +271,11 @@ static void product_launch(const int8_t* qx, const int8_t* qw, int64_t K, const 
         hipLaunchKernelGGL((k_epi_few<YT, MT, CT, NWV, U>), grid, dim3(64 * NWV), 0, st, qx, qw, K, e);     \
         return;                                                                                             \
     } while (0)
-    if (e.M <= 16) TQ_FEW(1, 1, 8, 4);
-    if ((e.M <= 32 && (e.N <= 6144 || !rows16)) || (rows16 && cdiv(e.M, 32) * cdiv(e.N, 16) <= 256))
-        TQ_FEW(2, 1, 8, 2);
-    if (rows16 && cdiv(e.M, 32) * cdiv(e.N, 32) <= 256) TQ_FEW(2, 2, 8, 2);
+    if (few_tokens(e.M, e.N)) {
+        if (e.M <= 16) TQ_FEW(1, 1, 8, 2);
+        if (few_columns(e.M, e.N)) TQ_FEW(2, 1, 8, 1);
+        TQ_FEW(2, 2, 8, 1);
+    }
 #undef TQ_FEW
     if (rows16) {
 #define TQ_RING(TILE, RING, WM, WN, WGS)                                                                     \

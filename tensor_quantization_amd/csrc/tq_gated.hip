@@ -52,18 +52,12 @@ __global__ __launch_bounds__(64 * NWV) void k_gate_few(const int8_t* __restrict_
             ob[j] = load1_rt(e.bias[j], e.bias_dt, on, 0.0f);
         }
 
-    const int8_t* pw[2];
-    const int8_t* px[MT];
-    const int64_t n = n0 + l16 < e.N ? n0 + l16 : e.N - 1;
+    const Rows16 weights[2] = {rows16_of(wg, e.N, n0, K), rows16_of(wu, e.N, n0, K)};
+    Rows16 tokens[MT];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) pw[j] = (j ? wu : wg) + n * K;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + l16;
-        px[i] = qx + (m < e.M ? m : e.M - 1) * K;
-    }
+    for (int i = 0; i < MT; ++i) tokens[i] = rows16_of(qx, e.M, m0 + 16 * i, K);
     v4i acc[MT][2];
-    few_product<MT, 2, NWV, U>(pw, px, K, acc);
+    few_product<MT, 2, NWV, U>(weights, tokens, K, acc);
     // lane l holds features 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -205,8 +199,13 @@ struct GateTile : Gate {
         return GateStage<YT, TILE>::BYTES;
     }
     template <int TILE, int WM, int WN>
+    static __device__ __forceinline__ int early(const Gate&, int64_t)
+    {
+        return 0;
+    }
+    template <int TILE, int WM, int WN>
     static __device__ __forceinline__ void finish(const Gate& e, int64_t m0, int64_t n0,
-                                                  const v4i (&acc)[TILE / WM / 16][TILE / WN / 16], uint8_t* lds)
+                                                  const v4i (&acc)[TILE / WM / 16][TILE / WN / 16], uint8_t* lds, int)
     {
         finish_gate<YT, TILE, WM, WN>(e, m0, n0, acc, lds);
     }
@@ -425,7 +424,11 @@ inline int64_t gate_chunk(int64_t M, int64_t F)
 }
 
 // The kernel of a gated product, by its shape: as for the product with one weight of
-// 2 F rows (product_launch), whose rounds and rates it shares.
+// 2 F rows (product_launch), whose rounds and rates it shares.  Few tokens / 64 tile, us:
+//   24 x 4096 x 4096    9.4 / 11.7     48 x 4096 x 4096   14.7 / 11.7
+//   24 x 4096 x 11008  17.7 / 24.2     48 x 4096 x 11008  31.9 / 25.8
+//   24 x 11008 x 4096  24.2 / 19.2     96 x 1024 x 4096    9.0 / 11.4
+//   24 x 4096 x 4095   16.6 / 21.6     220 x 507 x 10250  17.3 / 33.6
 template <int YT>
 static void gate_launch(const int8_t* qx, const int8_t* wg, const int8_t* wu, int64_t K, const Gate& e, hipStream_t st)
 {
@@ -437,8 +440,10 @@ static void gate_launch(const int8_t* qx, const int8_t* wg, const int8_t* wu, in
         hipLaunchKernelGGL((k_gate_few<YT, MT, NWV, U>), grid, dim3(64 * NWV), 0, st, qx, wg, wu, K, e);        \
         return;                                                                                             \
     } while (0)
-    if (e.M <= 16) TQ_FEW(1, 8, 2);
-    if ((e.M <= 32 && (N <= 6144 || !rows16)) || (rows16 && cdiv(e.M, 32) * cdiv(N, 32) <= 256)) TQ_FEW(2, 8, 2);
+    if (few_tokens(e.M, N)) {
+        if (e.M <= 16) TQ_FEW(1, 8, 1);
+        TQ_FEW(2, 8, 1);
+    }
 #undef TQ_FEW
     if (rows16) {
 #define TQ_RING(TILE, RING, WM, WN, WGS)                                                                     \

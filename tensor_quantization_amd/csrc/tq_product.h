@@ -167,16 +167,15 @@ __device__ __forceinline__ Raw8<YT> residual8(const Epi& e, const Cols8& c, int6
     return r;
 }
 
-// Finishes eight columns of one row from their sums (SCALED: from the bits of
-// binary32 values that have been scaled already).
-template <int YT, bool SCALED = false>
+// Finishes eight columns of one row from their sums.
+template <int YT>
 __device__ __forceinline__ void epilogue8(const Epi& e, const Cols8& c, int64_t row, float sx, const int acc[8],
                                           const Raw8<YT>& res)
 {
     const int64_t at = row * e.N + c.col;
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = SCALED ? as_f((uint32_t)acc[i]) : (float)acc[i] * sx * c.sw[i];
+    for (int i = 0; i < 8; ++i) v[i] = (float)acc[i] * sx * c.sw[i];
     if (e.bias) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += c.b[i];
@@ -211,64 +210,153 @@ __device__ __forceinline__ v4i codes16(const int8_t* row, int64_t k, int64_t K)
     }
     return r;
 }
+// ------------------------------------------------------------- operand loads
+// A matrix operand wants row l % 16 in lane l, so lanes side by side read rows apart, and
+// the address unit takes such a load one lane per clock: 64 clocks for 1 KB, which
+// bounds a CU to 16 bytes per clock wherever operands come straight from memory (48 x
+// 4096 x 11008 codes took 21.8 us for it, a few tokens' weights 10 of their 12).  So four
+// lanes side by side read 64 bytes of one row at a time, four rows in turn, and change
+// places afterwards: 256 bytes of sixteen rows, in four operands of 64.  Lane l's j-th
+// then holds bytes 64 (l / 16) + 16 j of row l % 16: the same order of K for every
+// operand so loaded.
+struct Quad {
+    v4i r[4];
+};
+
+// x and y of the lanes l ^ 1 (XOR1) or l ^ 2 trade places: where that bit of l is 0, y
+// becomes the neighbour's x, where it is 1, x the neighbour's y.  (The same as one
+// selecting instruction per value, from asm, which the compiler does not find, was
+// slower: 48 x 4096 x 11008 15.7 us against 13.3.)
+template <int CTRL>
+__device__ __forceinline__ void trade(v4i& x, v4i& y, bool bit)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int u = x[i], v = y[i];
+        const int of_u = (int)dpp<CTRL>((uint32_t)u), of_v = (int)dpp<CTRL>((uint32_t)v);
+        x[i] = bit ? of_v : u;
+        y[i] = bit ? v : of_u;
+    }
+}
+
+// Lane 4 a + b's r[u] goes to lane 4 a + u's r[b].  Every lane takes part.
+__device__ __forceinline__ void change_places(Quad& q)
+{
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    trade<DPP_XOR1>(q.r[0], q.r[1], odd);
+    trade<DPP_XOR1>(q.r[2], q.r[3], odd);
+    trade<DPP_XOR2>(q.r[0], q.r[2], high);
+    trade<DPP_XOR2>(q.r[1], q.r[3], high);
+}
+
+// Where a lane's four loads of sixteen rows begin, relative to the first of them:
+// rows past `last` are the last again.
+template <class Off>
+struct QuadAt {
+    Off at[4];
+};
+template <class Off>
+__device__ __forceinline__ QuadAt<Off> quad_at(int last, Off row_bytes)
+{
+    const int l = threadIdx.x & 63, first = (l & 15) & ~3;
+    QuadAt<Off> q;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        q.at[u] = (Off)(first + u < last ? first + u : last) * row_bytes + (Off)(64 * (l >> 4) + 16 * (l & 3));
+    return q;
+}
+template <class Off>
+__device__ __forceinline__ void quad_load(Quad& q, const void* rows, const QuadAt<Off>& a)
+{
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q.r[u] = codes16_whole(static_cast<const int8_t*>(rows) + a.at[u]);
+}
+
 // ------------------------------------------------------------- a few tokens
+// Whether the few-token kernels take a product: they read the tokens again for every 16
+// columns, which costs more the more columns there are, but give work to every CU
+// where an output has few 32 x 32 pieces.
+inline bool few_tokens(int64_t M, int64_t N)
+{
+    return M <= 16 || (M <= 32 && N <= 6144) || cdiv(M, 32) * cdiv(N, 32) <= 256;
+}
+// And, beyond 16 tokens, whether in 32 x 16 pieces rather than 32 x 32.
+inline bool few_columns(int64_t M, int64_t N) { return (M <= 32 && N <= 6144) || cdiv(M, 32) * cdiv(N, 16) <= 256; }
+
+// Sixteen rows of an operand: the first (uniform) and the last of them that is there.
+struct Rows16 {
+    const int8_t* first;
+    int last;
+};
+// Rows from `from` on of a matrix of n rows of K codes; past its end the last one.
+__device__ __forceinline__ Rows16 rows16_of(const int8_t* m, int64_t n, int64_t from, int64_t K)
+{
+    const int64_t f = from < n ? from : n - 1;
+    return Rows16{m + f * K, n - 1 - f < 15 ? (int)(n - 1 - f) : 15};
+}
+
 // The sums of 16 CT weight rows with 16 MT tokens by a workgroup of NWV waves,
-// which take the K axis in turn, 128 codes at a time, so that a wave's two
-// loads use whole 128-byte lines: acc holds this wave's share.  The weights are
-// the matrix core's first operand, the tokens its second; lane l's rows of them
-// start at pw[j] and px[i] (those of row l % 16 of each 16).  U blocks of both
-// are in flight per wave, each slot refilled as it is used.
+// which take the K axis in turn, 256 codes at a time: acc holds this wave's share.
+// The weights are the matrix core's first operand, the tokens its second.  U groups of
+// both are in flight per wave, each slot refilled as it is used.
 template <int MT, int CT, int NWV, int U>
-__device__ __forceinline__ void few_product(const int8_t* const (&pw)[CT], const int8_t* const (&px)[MT], int64_t K,
+__device__ __forceinline__ void few_product(const Rows16 (&weights)[CT], const Rows16 (&tokens)[MT], int64_t K,
                                             v4i (&acc)[MT][CT])
 {
-    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), g4 = (t & 63) >> 4;
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6), l16 = t & 15, g4 = (t & 63) >> 4;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < CT; ++j) acc[i][j] = v4i{};
-    // this wave's whole blocks are w, w + NWV, ...: U of them under way, each slot refilled as it is used
-    const int nkb = (int)((K + 127) / 128), whole = (int)(K / 128);
-    v4i a[U][2][CT], b[U][2][MT];
-    auto fetch = [&](int u, int kb) {
+    QuadAt<uint32_t> wa[CT], xa[MT];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int k = kb * 128 + 64 * s + 16 * g4;
+    for (int j = 0; j < CT; ++j) wa[j] = quad_at(weights[j].last, (uint32_t)K);
 #pragma unroll
-            for (int j = 0; j < CT; ++j) a[u][s][j] = codes16_whole(pw[j] + k);
+    for (int i = 0; i < MT; ++i) xa[i] = quad_at(tokens[i].last, (uint32_t)K);
+    // this wave's whole groups are w, w + NWV, ...
+    const int groups = (int)(K / 256);
+    Quad a[U][CT], b[U][MT];
+    auto fetch = [&](int u, int g) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) b[u][s][i] = codes16_whole(px[i] + k);
-        }
+        for (int j = 0; j < CT; ++j) quad_load(a[u][j], weights[j].first + g * 256, wa[j]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) quad_load(b[u][i], tokens[i].first + g * 256, xa[i]);
     };
-    auto products = [&](const v4i (&x)[CT], const v4i (&y)[MT]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (w + u * NWV < groups) fetch(u, w + u * NWV);
+    for (int g = w; g < groups; g += U * NWV)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (g + u * NWV >= groups) break;
+#pragma unroll
+            for (int j = 0; j < CT; ++j) change_places(a[u][j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) change_places(b[u][i]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][j].r[s], b[u][i].r[s], acc[i][j], 0, 0, 0);
+            if (g + (u + U) * NWV < groups) fetch(u, g + (u + U) * NWV);
+        }
+    if (groups % NWV != w) return;
+    for (int64_t k = (int64_t)groups * 256 + 16 * g4; k - 16 * g4 < K; k += 64) {    // the rest of K
+        v4i x[CT], y[MT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+            x[j] = codes16(weights[j].first + (int64_t)(l16 < weights[j].last ? l16 : weights[j].last) * K, k, K);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            y[i] = codes16(tokens[i].first + (int64_t)(l16 < tokens[i].last ? l16 : tokens[i].last) * K, k, K);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < CT; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[j], y[i], acc[i][j], 0, 0, 0);
-    };
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (w + u * NWV < whole) fetch(u, w + u * NWV);
-    for (int kb = w; kb < whole; kb += U * NWV)
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (kb + u * NWV >= whole) break;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) products(a[u][s], b[u][s]);
-            if (kb + (u + U) * NWV < whole) fetch(u, kb + (u + U) * NWV);
-        }
-    if (whole < nkb && whole % NWV == w)     // the rest of K
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int64_t k = (int64_t)whole * 128 + 64 * s + 16 * g4;
-            v4i x[CT], y[MT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) x[j] = codes16(pw[j], k, K);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) y[i] = codes16(px[i], k, K);
-            products(x, y);
-        }
+    }
 }
 
 // -------------------------------------------------------------- many tokens
@@ -433,22 +521,12 @@ __device__ __forceinline__ void finish_inside(const Epi& e, const Cols8& cc, int
     }
 }
 
-// What is done to a staged half of sums before it is finished: nothing, or (ADDS)
-// what turns them into scaled binary32 values and adds to these.
-struct NoDelta {
-    static constexpr bool ADDS = false;
-    template <int NM, int NN>
-    __device__ __forceinline__ void apply(const Epi&, int64_t, int64_t, int, int*) const
-    {
-    }
-};
-
 // Any part: bounds, and the value before the activation where it is asked for
 // (8192 x 11008 x 4096 with gelu_tanh and that value 366 us, 327 without: the 180 MB
 // more take 36 at a large copy's rate).
-template <int YT, int NM, int NN, class D>
-__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, int64_t n0,
-                                           const v4i (&acc)[NM][NN], int* stage, const D& delta)
+template <int YT, int NM, int NN>
+__device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_t m0, const v4i (&acc)[NM][NN],
+                                           int* stage)
 {
     using S = Stage<NM, NN>;
     const int lane = threadIdx.x & 63;
@@ -459,7 +537,6 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
         const int64_t mh = m0 + 32 * h;
         if (mh >= e.M) return;           // uniform
         stage_half<NM, NN>(h, acc, stage);
-        delta.template apply<NM, NN>(e, m0, n0, h, stage);
         const int rows = cc.n == 0 ? 0 : e.M - mh < 32 ? (int)(e.M - mh) : 32;
 #pragma unroll 1
         for (int r = r0; r < rows; r += S::RPI) {
@@ -468,7 +545,7 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
             const v4i s0 = *reinterpret_cast<const v4i*>(&stage[r * S::PITCH + c]);
             const v4i s1 = *reinterpret_cast<const v4i*>(&stage[r * S::PITCH + c + 4]);
             const int s[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-            epilogue8<YT, D::ADDS>(e, cc, mh + r, sx[32 * h + r], s, res);
+            epilogue8<YT>(e, cc, mh + r, sx[32 * h + r], s, res);
         }
     }
 }
@@ -477,27 +554,27 @@ __device__ __forceinline__ void finish_any(const Epi& e, const Cols8& cc, int64_
 // of LDS, so that its stores are whole rows of its part and the epilogue's
 // code exists once per activation.  A lane keeps its eight columns for all
 // rows, so their scales and bias are read once.
-template <int YT, int NM, int NN, bool NTS = false, class D = NoDelta>
+template <int YT, int NM, int NN, bool NTS = false>
 __device__ __forceinline__ void finish_part(const Epi& e, int64_t m0, int64_t n0, const v4i (&acc)[NM][NN],
-                                            int* stage, const D& delta = D())
+                                            int* stage)
 {
     const Cols8 cc = cols8(e, n0 + 8 * ((threadIdx.x & 63) % Stage<NM, NN>::LPR));
     if (m0 >= e.M) return;               // uniform
     stage_scales<NM, NN>(e, m0, stage);
     const bool inside = m0 + 16 * NM <= e.M && n0 + 16 * NN <= e.N && e.N <= 1 << 22 && e.ldr <= 1 << 22;
-    if (!D::ADDS && inside && !e.z)
+    if (inside && !e.z)
         with_act(e.act, [&](auto a) {
             if (e.res) finish_inside<YT, NM, NN, decltype(a)::value, true, NTS>(e, cc, m0, n0, acc, stage);
             else finish_inside<YT, NM, NN, decltype(a)::value, false, NTS>(e, cc, m0, n0, acc, stage);
         });
-    else finish_any<YT, NM, NN>(e, cc, m0, n0, acc, stage, delta);
+    else finish_any<YT, NM, NN>(e, cc, m0, acc, stage);
 }
 
 // ------------------------------------------------------------ the tile kernels
 // An epilogue E gives M and N (rows of a weight), GATED (two weights, the second
 // from second_weight, sixteen rows of either in turn: a tile is TILE / 2 columns
-// wide), staging() bytes of LDS and finish(), which takes a wave's sums and the
-// tile's place.
+// wide), staging() bytes of LDS and finish(), which takes a wave's sums, the tile's
+// place and what early() read before the first block.
 //
 // k_epi_ring: operands whose rows start at 16-byte addresses.  A TILE x TILE tile
 // per workgroup of WM x WN waves, a wave a TILE / WM x TILE /
@@ -606,6 +683,7 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    const auto early = E::template early<TILE, WM, WN>(e, m0);
     const int units = 2 * nkb;
     int sa = 0, sb = 1;                  // slots of the present block's units
     for (int u = 0; u < (units < RING ? units : RING); ++u) load_unit(u, u);
@@ -661,7 +739,7 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_ring(co
         for (int j = 0; j < NN; ++j) asm volatile("" : "+a"(acc[i][j]));
     __builtin_amdgcn_s_waitcnt(0x0070);
     asm volatile("s_barrier" ::: "memory");   // the ring gives way to the staged sums
-    E::template finish<TILE, WM, WN>(e, m0, n0, acc, ring);
+    E::template finish<TILE, WM, WN>(e, m0, n0, acc, ring, early);
 }
 
 // k_epi_tile: operands of any alignment and K.  Direct loads to LDS take 16-byte addresses only, so the codes pass through
@@ -741,6 +819,7 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_tile(co
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[j], av[i], acc[i][j], 0, 0, 0);
         }
     };
+    const auto early = E::template early<TILE, WM, WN>(e, m0);
     const int whole = (int)(K / ET);
     if (whole > 0) {
 #pragma unroll
@@ -768,7 +847,7 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_epi_tile(co
         __syncthreads();
     }
     // the operands give way to the staged sums
-    E::template finish<TILE, WM, WN>(e, m0, n0, acc, lds.out);
+    E::template finish<TILE, WM, WN>(e, m0, n0, acc, lds.out, early);
 }
 
 }  // namespace tq
