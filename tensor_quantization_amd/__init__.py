@@ -1157,21 +1157,25 @@ def tq_w8a8_linear_adapters(x, qx, sx, qw, sw, adapter, a, b, scale=None, bias=N
     activation."""
     qx, qw = _codes(qx, "qx"), _codes(qw, "qw")
     M, K = qx.shape
-    N = qw.shape[0]
-    dev = qx.device
-    if qw.shape[1] != K or qw.device != dev:
+    N, kw = qw.shape
+    dev, dt = qx.device, x.dtype
+    if kw != K or qw.device != dev:
         raise ValueError("qx and qw must share K and their device")
-    if x.shape != (M, K) or x.device != dev:
+    if x.shape != qx.shape or x.device != dev:
         raise ValueError("x must be [M, K] as its codes, on their device")
     sx, sw = _row_vector(sx, M, qx, "sx"), _row_vector(sw, N, qx, "sw")
-    if adapter.dtype != torch.int32 or adapter.shape != (M,) or adapter.device != dev:
+    if adapter.dtype is not torch.int32 or adapter.numel() != M or adapter.dim() != 1 or adapter.device != dev:
         raise ValueError("adapter must be int32 with one value per token, on x's device")
-    if a.dim() != 3 or a.shape[2] != K or b.shape != (a.shape[0], N, a.shape[1]):
+    if a.dim() != 3:
         raise ValueError("a must be [adapters, rank, K] and b [adapters, N, rank]")
-    if a.dtype != x.dtype or b.dtype != x.dtype or a.device != dev or b.device != dev:
+    count, rank, ka = a.shape
+    if ka != K or b.shape != (count, N, rank):
+        raise ValueError("a must be [adapters, rank, K] and b [adapters, N, rank]")
+    if a.dtype is not dt or b.dtype is not dt or a.device != dev or b.device != dev:
         raise ValueError("a and b must have x's type and device")
-    count, rank = a.shape[0], a.shape[1]
-    _, b_, bdt = _params(qx, N, None, bias)
+    b_, bdt = None, 0
+    if bias is not None:
+        _, b_, bdt = _params(qx, N, None, bias)
     ldr = N
     if residual is not None:
         if residual.shape != (M, N) or residual.dtype != out_dtype or residual.device != dev:
@@ -1179,15 +1183,15 @@ def tq_w8a8_linear_adapters(x, qx, sx, qw, sw, adapter, a, b, scale=None, bias=N
         residual, _, _, ldr = _rows_of(residual, "residual")
     xr, _, _, ldx = _rows_of(x, "x")
     adapter, a, b = adapter.contiguous(), a.contiguous(), b.contiguous()
-    scale = None if scale is None else _row_vector(scale, count, qx, "scale")
+    if scale is not None:
+        scale = _row_vector(scale, count, qx, "scale")
     y = torch.empty(M, N, dtype=out_dtype, device=dev)
     z = torch.empty_like(y) if preact else None
     nws = _lib.tq_w8a8_linear_adapters_workspace_bytes(M, rank)
     ws = _workspace(dev, nws)
-    _on(dev, "tq_w8a8_linear_adapters", xr.data_ptr(), FTYPE[x.dtype], ldx, qx.data_ptr(), sx.data_ptr(),
-        qw.data_ptr(), sw.data_ptr(), M, N, K, adapter.data_ptr(), count, rank, a.data_ptr(), b.data_ptr(),
-        _ptr(scale), _ptr(b_), bdt, ACT[act], _ptr(residual), ldr, y.data_ptr(), _ptr(z), FTYPE[out_dtype], _ptr(ws),
-        nws)
+    _on(dev, "tq_w8a8_linear_adapters", xr.data_ptr(), FTYPE[dt], ldx, qx.data_ptr(), sx.data_ptr(), qw.data_ptr(),
+        sw.data_ptr(), M, N, K, adapter.data_ptr(), count, rank, a.data_ptr(), b.data_ptr(), _ptr(scale), _ptr(b_), bdt,
+        ACT[act], _ptr(residual), ldr, y.data_ptr(), _ptr(z), FTYPE[out_dtype], _ptr(ws), nws)
     return (y, z) if preact else y
 
 
@@ -1197,23 +1201,29 @@ def tq_w8a8_linear_adapters_workspace_bytes(M, rank):
 
 # ------------------------------------- token log-probability and policy loss
 def _logp_args(logits, token):
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [rows, vocab]")
-    rows, vocab = logits.shape
+    rows, vocab = shape
     z, _, _, ld = _rows_of(logits, "logits")
-    if token.dtype not in (torch.int32, torch.int64):
+    dt, dev = token.dtype, logits.device
+    if dt is not torch.int64 and dt is not torch.int32:
         raise TypeError("token must be int32 or int64")
-    if token.shape != (rows,) or token.device != logits.device:
+    if token.shape != (rows,) or token.device != dev:
         raise ValueError("token must have one value per row, on the logits' device")
     token = token.contiguous()
-    head = (z.data_ptr(), FTYPE[z.dtype], rows, vocab, ld, token.data_ptr(), 32 if token.dtype == torch.int32 else 64)
-    return head, (z, token), rows, vocab, z.device
+    head = (z.data_ptr(), FTYPE[z.dtype], rows, vocab, ld, token.data_ptr(), 32 if dt is torch.int32 else 64)
+    return head, (z, token), rows, vocab, dev
 
 
 def _policy_args(logits, rows, advantage, old_logp, ref_logp):
-    kept = [None if v is None else _row_vector(v, rows, logits, name)
-            for v, name in ((advantage, "advantage"), (old_logp, "old_logp"), (ref_logp, "ref_logp"))]
-    return kept, [_ptr(v) for v in kept]
+    """The vectors, and their addresses."""
+    advantage = _row_vector(advantage, rows, logits, "advantage")
+    if old_logp is not None:
+        old_logp = _row_vector(old_logp, rows, logits, "old_logp")
+    if ref_logp is not None:
+        ref_logp = _row_vector(ref_logp, rows, logits, "ref_logp")
+    return (advantage, old_logp, ref_logp), (advantage.data_ptr(), _ptr(old_logp), _ptr(ref_logp))
 
 
 def _saved_stats(stats, rows, dev):

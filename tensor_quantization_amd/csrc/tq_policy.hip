@@ -471,8 +471,10 @@ inline Split logp_split(int64_t rows, int64_t V)
     return q;
 }
 
-// From LP_ROWS rows on a workgroup takes a whole row forwards: one launch.
-constexpr int64_t LP_ROWS = 256;
+// Whether a workgroup takes a whole row forwards, in one launch: from LP_ROWS rows on,
+// and where a row is short enough that a launch costs more than its reading.
+constexpr int64_t LP_ROWS = 256, LP_SHORT = 8192;
+inline bool whole_rows(int64_t rows, int64_t V) { return rows >= LP_ROWS || V <= LP_SHORT; }
 
 // Most workgroups per launch: a grid holds fewer than 2^32 threads.  Further rows
 // are further launches.
@@ -523,7 +525,7 @@ static void parts_launch(const Logp& all, float* ws, hipStream_t st)
 template <int FT>
 static void forward_launch(const Logp& all, float* ws, float* loss, float* logp, float* stats, hipStream_t st)
 {
-    if (all.rows >= LP_ROWS) {
+    if (whole_rows(all.rows, all.V)) {
         for (int64_t r = 0; r < all.rows; r += LP_LAUNCH / 4) {
             const Logp d = rows_from(all, FT, r, LP_LAUNCH / 4);
 #define TQ_ROWS(NT)                                                                                                  \
@@ -623,7 +625,9 @@ static tq_status policy_check(const float* advantage, const float* old_logp, con
 
 static tq_status workspace_check(const void* ws, size_t have, int64_t rows, int64_t vocab)
 {
-    if (!ws || have < tq_policy_loss_workspace_bytes(rows, vocab)) return TQ_ERR_INVALID;
+    const size_t need = tq_policy_loss_workspace_bytes(rows, vocab);
+    if (need == 0) return TQ_OK;
+    if (!ws || have < need) return TQ_ERR_INVALID;
     return aligned16(ws) ? TQ_OK : TQ_ERR_ALIGN;
 }
 
@@ -635,7 +639,7 @@ extern "C" {
 
 size_t tq_policy_loss_workspace_bytes(int64_t rows, int64_t vocab)
 {
-    if (rows <= 0 || vocab <= 0) return 0;
+    if (rows <= 0 || vocab <= 0 || (vocab <= LP_SHORT && vocab >= 8)) return 0;  // whole rows, forwards and held
     return (logp_part_floats(rows, vocab) + (size_t)rows) * sizeof(float);
 }
 

@@ -93,16 +93,17 @@ def test_adapter_refusals(tq):
 
 def test_policy_refusals(tq):
     L, INV, UNS, ALIGN = tq._lib, tq.TQ_ERR_INVALID, tq.TQ_ERR_UNSUPPORTED, tq.TQ_ERR_ALIGN
-    n = tq.tq_policy_loss_workspace_bytes(4, 100)
-    ok = dict(z=A, dt=2, rows=4, V=100, ld=100, tok=A, bits=64, adv=C, old=None, ref=None, lo=0.2, hi=0.2, beta=0.0, T=1.0,
-              dloss=None, loss=C, logp=C, dz=B, ldd=100, ws=A, n=n, st=None)
+    V = 10000
+    n = tq.tq_policy_loss_workspace_bytes(4, V)
+    ok = dict(z=A, dt=2, rows=4, V=V, ld=V, tok=A, bits=64, adv=C, old=None, ref=None, lo=0.2, hi=0.2, beta=0.0, T=1.0,
+              dloss=None, loss=C, logp=C, dz=B, ldd=V, ws=A, n=n, st=None)
 
     def call(**kw):
         return L.tq_policy_loss_grad(*{**ok, **kw}.values())
     for name in ("z", "tok", "adv", "loss", "logp", "dz", "ws"):
         assert call(**{name: None}) == INV, name
     assert call(dt=3) == INV and call(bits=16) == INV and call(rows=-1) == INV and call(V=0) == INV
-    assert call(ld=99) == INV and call(ldd=99) == INV and call(n=n - 1) == INV
+    assert call(ld=V - 1) == INV and call(ldd=V - 1) == INV and call(n=n - 1) == INV
     for t in (0.0, -1.0, float("nan"), float("inf")):
         assert call(T=t) == INV
     for kw in ({"lo": -0.1}, {"lo": 1.1}, {"hi": -0.1}, {"beta": -1.0}, {"beta": float("inf")}, {"lo": float("nan")}):
@@ -114,20 +115,23 @@ def test_policy_refusals(tq):
         assert call(**{name: ODD4}) == ALIGN, name
     assert call(ws=ODD8) == ALIGN and call(rows=0) == 0
     f = L.tq_token_logp
-    assert f(A, 2, 4, 100, 100, A, 64, 1.0, None, None, A, n, None) == INV               # no output
-    assert f(A, 2, 4, 100, 100, A, 64, 1.0, C, ODD4, A, n, None) == ALIGN
-    assert f(A, 2, 4, 100, 100, A, 64, 1.0, C, None, A, n - 1, None) == INV
+    assert f(A, 2, 4, V, V, A, 64, 1.0, None, None, A, n, None) == INV               # no output
+    assert f(A, 2, 4, V, V, A, 64, 1.0, C, ODD4, A, n, None) == ALIGN
+    assert f(A, 2, 4, V, V, A, 64, 1.0, C, None, A, n - 1, None) == INV
     b = L.tq_token_logp_backward
-    assert b(A, 2, 4, 100, 100, A, 64, 1.0, None, None, B, 100, None) == INV             # no stats
-    assert b(A, 2, 4, 100, 100, A, 64, 1.0, C, None, B, 99, None) == INV
+    assert b(A, 2, 4, V, V, A, 64, 1.0, None, None, B, V, None) == INV             # no stats
+    assert b(A, 2, 4, V, V, A, 64, 1.0, C, None, B, V - 1, None) == INV
     g = L.tq_policy_loss_backward
-    assert g(A, 2, 4, 100, 100, A, 64, C, None, None, 0.2, 0.2, 0.0, 1.0, None, C, None, B, 100, None) == INV   # no logp
-    assert g(A, 2, 4, 100, 100, A, 64, C, None, None, 0.2, 0.2, 0.0, 1.0, C, None, None, B, 100, None) == INV   # no stats
+    assert g(A, 2, 4, V, V, A, 64, C, None, None, 0.2, 0.2, 0.0, 1.0, None, C, None, B, V, None) == INV   # no logp
+    assert g(A, 2, 4, V, V, A, 64, C, None, None, 0.2, 0.2, 0.0, 1.0, C, None, None, B, V, None) == INV   # no stats
 
 
 @pytest.mark.parametrize("V", [1, 7, 4096, 4097, 8192, 8193, 32000, 131001, 131072, 1 << 20])
 @pytest.mark.parametrize("rows", [1, 9, 127, 128, 511, 512, 2047, 2048, 5000])
 def test_policy_workspace(tq, rows, V):
+    if 8 <= V <= 8192:
+        assert tq.tq_policy_loss_workspace_bytes(rows, V) == 0      # a workgroup per row, forwards and in one call
+        return
     most = 8192 if rows * cdiv(V, 8192) >= 2048 else 4096
     parts = cdiv(V, 8 * cdiv(cdiv(V, cdiv(V, most)), 8))
     assert tq.tq_policy_loss_workspace_bytes(rows, V) >= rows * (8 * parts + 4)   # a part's pair, the token's logit
