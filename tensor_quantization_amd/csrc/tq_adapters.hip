@@ -641,6 +641,17 @@ struct AdaptTile : Epi {
 // does not mind whose they are; beyond, the matrix cores.
 constexpr int64_t LOW_FEW = 8192;
 
+// Whether the few-token kernel takes the product: by the product's rule, and for so few
+// tokens times ranks also with two pieces of 32 x 32 per CU, since a tile takes the
+// adapters of its tokens in turn.  Few tokens / tiles, us, rank 16, each token with an
+// adapter of its own | all with one:
+//   100 x 4096 x 11008   36 / 66 | 33 / 35     128 x 4096 x 4096   21 / 45 | 19.5 / 18
+//   64 x 11008 x 4096    30 / 51 | 26 / 19     200 x 4096 x 4096   35 / 47 | 32.5 / 18
+inline bool adapt_few(int64_t M, int64_t N, int64_t rank)
+{
+    return few_tokens(M, N) || (M * rank <= LOW_FEW && cdiv(M, 32) * cdiv(N, 32) <= 512);
+}
+
 template <int AT>
 static void low_launch(const void* x, int64_t ldx, int64_t M, int64_t K, bool few, const Adapters& ad, hipStream_t st)
 {
@@ -678,7 +689,7 @@ static void adapt_launch(const int8_t* qx, const int8_t* qw, int64_t K, const Ep
         hipLaunchKernelGGL((k_adapt_few<YT, MT, CT, NWV, U>), grid, dim3(64 * NWV), 0, st, qx, qw, K, e, ad);   \
         return;                                                                                                 \
     } while (0)
-    if (few_tokens(e.M, e.N)) {
+    if (adapt_few(e.M, e.N, ad.R)) {
         if (e.M <= 16) TQ_FEW(1, 1, 8, 2);
         if (few_columns(e.M, e.N)) TQ_FEW(2, 1, 8, 1);
         TQ_FEW(2, 2, 8, 1);
@@ -765,7 +776,7 @@ tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stri
     const Adapters ad = {adapter, a, b, scale, workspace, reinterpret_cast<int*>(static_cast<char*>(workspace) +
                          low_bytes(M, rank)), (int)adapters, (int)rank, (int)low_ld(rank), x_dtype};
     hipStream_t st = as_stream(stream);
-    const bool few = few_tokens(M, N);
+    const bool few = adapt_few(M, N, rank);
     TQ_LLM_FT_SWITCH(x_dtype, low_launch<FTV>(x, x_row_stride, M, K, few, ad, st));
     TQ_LLM_FT_SWITCH(y_dtype, adapt_launch<FTV>(qx, qw, K, e, ad, st));
     return launch_status();

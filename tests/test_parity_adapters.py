@@ -116,8 +116,18 @@ def test_tiles(tq, M, N, K, R, ft, out, sort):
     check(tq, M, N, K, R, 5, ft, out, act="none" if sort else "gelu_tanh", sort=sort)
 
 
+# either side of the rules of the few-token kernel, adapters in any order
+@pytest.mark.parametrize("M,N,K,R", [(90, 4300, 272, 16), (128, 4096, 144, 64), (130, 3270, 208, 63), (128, 4097, 144, 64),
+                                     (32, 6145, 135, 9), (33, 8192, 129, 8), (33, 8193, 144, 8)])
+@pytest.mark.parametrize("ft", ["bf16", "f32"])
+def test_few_token_rules(tq, M, N, K, R, ft):
+    note("adapters rules", M, N, K, R, ft)
+    check(tq, M, N, K, R, 90, ft)
+
+
 # codes whose rows start anywhere: every tile of that kernel
-@pytest.mark.parametrize("M,N,K", [(100, 130, 127), (100, 130, 513), (1500, 1600, 389), (2900, 4110, 131)])
+@pytest.mark.parametrize("M,N,K", [(100, 130, 127), (100, 130, 513), (530, 540, 259), (1500, 1600, 389),
+                                   (2900, 4110, 131)])
 @pytest.mark.parametrize("ft", ["bf16", "f32"])
 def test_any_alignment(tq, M, N, K, ft):
     note("adapters any alignment", M, N, K, ft)
@@ -126,24 +136,25 @@ def test_any_alignment(tq, M, N, K, ft):
 
 @pytest.mark.parametrize("parts", [(False, False, False), (True, False, True), (False, True, False)])
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
-@pytest.mark.parametrize("M", [6, 150])
-def test_parts(tq, parts, act, M):
-    check(tq, M, 264, 384, 16, 3, "bf16", act=act, parts=parts)
+@pytest.mark.parametrize("M,N", [(6, 264), (150, 264), (600, 568)])
+def test_parts(tq, parts, act, M, N):
+    check(tq, M, N, 384, 16, 3, "bf16", act=act, parts=parts)
 
 
 @pytest.mark.parametrize("M", [3, 40, 200, 600])
 def test_ids_outside_are_none(tq, M):
     """Every value that is no adapter, and batches where nobody has one."""
     ids = torch.tensor([-1, 3, 2, -2 ** 31, 0, 2 ** 31 - 1, 1, 4])[torch.arange(M) % 8].int()
-    check(tq, M, 200, 256, 16, 3, "bf16", adapter=ids)
-    check(tq, M, 200, 256, 16, 3, "f16", adapter=torch.full((M,), -1, dtype=torch.int32))
+    N = 200 if M < 600 else 520
+    check(tq, M, N, 256, 16, 3, "bf16", adapter=ids)
+    check(tq, M, N, 256, 16, 3, "f16", adapter=torch.full((M,), -1, dtype=torch.int32))
 
 
 @pytest.mark.parametrize("M", [1, 12, 40, 130, 300, 700])
 @pytest.mark.parametrize("ft", ["bf16", "f16", "f32"])
 def test_other_adapters_do_not_reach_a_token(tq, M, ft):
     """Infinities and NaN in adapters, their scales and their tokens stay with them."""
-    N, K, R, count = 300, 272, 16, 6
+    N, K, R, count = 300 if M < 700 else 900, 272, 16, 6
     ops = [t.cuda() for t in operands(M, N, K, R, count, M, ft, "f32")]
     want = tq.tq_w8a8_linear_adapters(*ops[:8], scale=ops[8], out_dtype=torch.float32)
     bad = [t.clone() for t in ops]
@@ -162,11 +173,11 @@ def test_other_adapters_do_not_reach_a_token(tq, M, ft):
     assert torch.equal(got[two][:, ~col], want[two][:, ~col]) and not bool(torch.isfinite(got[two][:, col]).any())
 
 
-@pytest.mark.parametrize("M", [4, 200])
+@pytest.mark.parametrize("M", [4, 200, 600])
 @pytest.mark.parametrize("ft,size", [("f16", 1e-7), ("f16", 300.0), ("bf16", 1e30), ("bf16", 1e-25), ("f32", 1e25)])
 def test_low_values_far_from_one(tq, M, ft, size):
     """h beyond f16's range on either side, and near the ends of binary32's."""
-    N, K, R, count = 130, 256, 16, 3
+    N, K, R, count = 130 if M < 600 else 500, 256, 16, 3
     g = torch.Generator().manual_seed(M)
     x = torch.randn((M, K), generator=g).to(ref.TORCH[ft])
     a = (torch.randn((count, R, K), generator=g) * (size if ft != "f16" else min(size, 300.0))).to(ref.TORCH[ft])
@@ -181,8 +192,8 @@ def test_low_values_far_from_one(tq, M, ft, size):
 
 
 def test_strides_and_odd_addresses(tq):
-    for M in (5, 70, 300):
-        N, K, R, count = 136, 272, 13, 4
+    for M in (5, 70, 300, 600):
+        N, K, R, count = 136 if M < 600 else 520, 272, 13, 4
         ops = [t.cuda() for t in operands(M, N, K, R, count, 8, "bf16", "bf16")]
         want = tq.tq_w8a8_linear_adapters(*ops[:8], scale=ops[8], bias=ops[9], residual=ops[10])
 
@@ -200,7 +211,7 @@ def test_strides_and_odd_addresses(tq):
 
 @pytest.mark.parametrize("M,R", [(1, 16), (40, 9), (300, 33), (700, 64)])
 def test_keeps_inside_its_workspace(tq, M, R):
-    N, K, count, G = 200, 272, 3, 4096
+    N, K, count, G = 200 if M < 700 else 520, 272, 3, 4096
     ops = [t.cuda() for t in operands(M, N, K, R, count, 9, "bf16", "bf16")]
     want = tq.tq_w8a8_linear_adapters(*ops[:8], scale=ops[8])
     n = tq.tq_w8a8_linear_adapters_workspace_bytes(M, R)
