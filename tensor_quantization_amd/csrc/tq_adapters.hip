@@ -637,9 +637,15 @@ struct AdaptTile : Epi {
 };
 
 // ---------------------------------------------------------------- launches
-// Up to LOW_FEW tokens times ranks every token reads its adapter's rows for itself, which
-// does not mind whose they are; beyond, the matrix cores.
+// Up to LOW_FEW tokens times ranks, or twice as many where the tokens' tiles of 16 are too
+// few for the chip, every token reads its adapter's rows for itself, which does not mind whose
+// they are; beyond, the matrix cores, which take the adapters of a tile in turn.  The call
+// with 128 columns, tokens of eight adapters in turn | in runs, by token / by tile, us:
+//   48 x 11008, rank 16  16 / 70 | 16 / 38      512 x 4096, rank 16  20 / 33 | 20 / 16
+//   128 x 4096, rank 64  20 / 76 | 20 / 18     1024 x 4096, rank 16  32 / 41 | 32 / 16
+//   200 x 4096, rank 64  26 / 74 | 26 / 26      512 x 4096, rank 64  52 / 74 | 52 / 19
 constexpr int64_t LOW_FEW = 8192;
+inline bool low_by_token(int64_t M, int64_t rank) { return M * rank <= (M <= 256 ? 2 : 1) * LOW_FEW; }
 
 // Whether the few-token kernel takes the product: by the product's rule, and for so few
 // tokens times ranks also with two pieces of 32 x 32 per CU, since a tile takes the
@@ -655,7 +661,7 @@ inline bool adapt_few(int64_t M, int64_t N, int64_t rank)
 template <int AT>
 static void low_launch(const void* x, int64_t ldx, int64_t M, int64_t K, bool few, const Adapters& ad, hipStream_t st)
 {
-    if (M * ad.R <= LOW_FEW) {
+    if (low_by_token(M, ad.R)) {
         if (few)
             hipLaunchKernelGGL((k_low_few<AT>), dim3((unsigned)cdiv(ad.R, 4), (unsigned)M), dim3(512), 0, st, x, ldx,
                                (int)K, ad);

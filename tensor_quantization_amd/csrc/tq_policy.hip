@@ -472,9 +472,14 @@ inline Split logp_split(int64_t rows, int64_t V)
 }
 
 // Whether a workgroup takes a whole row forwards, in one launch: from LP_ROWS rows on,
-// and where a row is short enough that a launch costs more than its reading.
-constexpr int64_t LP_ROWS = 256, LP_SHORT = 8192;
-inline bool whole_rows(int64_t rows, int64_t V) { return rows >= LP_ROWS || V <= LP_SHORT; }
+// and where a row is so short (LP_BYTES) that the second launch costs more than its
+// reading by one CU.  Whole rows / parts and their join, one call after another, us, bf16:
+//   64 x 32000   11.5 / 14.6     64 x 131072   13.3 / 14.6 (kernels 12 / 6.9 + 3.0)
+//   256 x 32000  11.5 / 14.5     256 x 131072  15.5 / 17.7
+//   2048 x 32000 30.5 / 33.2     512 x 131072  30.2 / 30.0
+constexpr int64_t LP_ROWS = 256, LP_BYTES = 131072;
+inline bool whole_rows(int64_t rows, int64_t V, int FT) { return rows >= LP_ROWS || V * ftype_size(FT) <= LP_BYTES; }
+constexpr int64_t LP_NO_WORKSPACE = 8192;    // whole rows forwards and held in one call, in every type
 
 // Most workgroups per launch: a grid holds fewer than 2^32 threads.  Further rows
 // are further launches.
@@ -525,7 +530,7 @@ static void parts_launch(const Logp& all, float* ws, hipStream_t st)
 template <int FT>
 static void forward_launch(const Logp& all, float* ws, float* loss, float* logp, float* stats, hipStream_t st)
 {
-    if (whole_rows(all.rows, all.V)) {
+    if (whole_rows(all.rows, all.V, FT)) {
         for (int64_t r = 0; r < all.rows; r += LP_LAUNCH / 4) {
             const Logp d = rows_from(all, FT, r, LP_LAUNCH / 4);
 #define TQ_ROWS(NT)                                                                                                  \
@@ -639,7 +644,7 @@ extern "C" {
 
 size_t tq_policy_loss_workspace_bytes(int64_t rows, int64_t vocab)
 {
-    if (rows <= 0 || vocab <= 0 || (vocab <= LP_SHORT && vocab >= 8)) return 0;  // whole rows, forwards and held
+    if (rows <= 0 || vocab <= 0 || (vocab <= LP_NO_WORKSPACE && vocab >= 8)) return 0;
     return (logp_part_floats(rows, vocab) + (size_t)rows) * sizeof(float);
 }
 

@@ -118,7 +118,8 @@ def test_tiles(tq, M, N, K, R, ft, out, sort):
 
 # either side of the rules of the few-token kernel, adapters in any order
 @pytest.mark.parametrize("M,N,K,R", [(90, 4300, 272, 16), (128, 4096, 144, 64), (130, 3270, 208, 63), (128, 4097, 144, 64),
-                                     (32, 6145, 135, 9), (33, 8192, 129, 8), (33, 8193, 144, 8)])
+                                     (32, 6145, 135, 9), (33, 8192, 129, 8), (33, 8193, 144, 8),
+                                     (200, 4096, 144, 64), (256, 1000, 135, 64), (257, 1000, 144, 64)])
 @pytest.mark.parametrize("ft", ["bf16", "f32"])
 def test_few_token_rules(tq, M, N, K, R, ft):
     note("adapters rules", M, N, K, R, ft)
