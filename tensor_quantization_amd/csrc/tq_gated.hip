@@ -24,7 +24,7 @@ struct Gate {
 // k_gate_few: a workgroup of NWV waves owns 16 features of 16 MT tokens, the 16
 // rows of either weight side by side (few_product), so that the thread that
 // finishes an output finds both sums in LDS.  Bound by the weights, which are read
-// once.
+// once: 1 x 11008 x 4096 17.2 us (90 MB of codes, 5.2 TB/s).
 template <int YT, int MT, int NWV, int U>
 __global__ __launch_bounds__(64 * NWV) void k_gate_few(const int8_t* __restrict__ qx, const int8_t* __restrict__ wg,
                                                        const int8_t* __restrict__ wu, int64_t K, Gate e)
@@ -87,7 +87,14 @@ __global__ __launch_bounds__(64 * NWV) void k_gate_few(const int8_t* __restrict_
 // A tile's outputs are finished in registers, where a lane holds both sums of four
 // consecutive features of a row, and pass through LDS, so that stores are whole
 // lines: half as many values to stage as there are sums, and the whole tile's at
-// once (rows 16 features apart beyond theirs, which meets all banks).
+// once (rows 16 features apart beyond theirs, which meets all banks).  For that a tile's
+// weight rows are 16 of the gate and 16 of the other in turn (tile_row), and nothing
+// else differs from the plain product with 2 F columns: 8192 x 11008 x 4096 bf16 590-610
+// us (2 x 8192 x 22016 x 4096 operations at 2420-2500 TOP/s; matrix cores busy 61%,
+// 722 MB read for 124 MB of codes, most of it from the last cache), 777 x 4096 x 4096
+// f16 35 us: 448 tiles of 128 in one round of two to a CU, a seventh of which hold no
+// token.  Any alignment with z kept: 1021 x 2501 x 5003 f32 83 us, 320 tiles for 256
+// CUs and the loads of k_epi_tile.
 template <int YT, int TILE>
 struct GateStage {
     static constexpr int ES = YT == F32 ? 4 : 2, PITCH = (TILE / 2 + 16) * ES, BYTES = TILE * PITCH;
@@ -265,7 +272,8 @@ __device__ __forceinline__ void act_slope8(int act, const float g[8], float a[8]
     }
 }
 
-// k_gate_act: a thread per eight features of a row (F >= 8), or per feature.
+// k_gate_act: a thread per eight features of a row (F >= 8), or per feature.  Bound by
+// HBM: [8192, 2 x 11008] bf16 92.5 us (541 MB, 5.85 TB/s).
 template <int FT>
 __global__ __launch_bounds__(256) void k_gate_act(const void* __restrict__ z, uint32_t M, int64_t F, uint32_t per,
                                                   int act, void* __restrict__ y)
@@ -299,7 +307,8 @@ __global__ __launch_bounds__(256) void k_gate_act(const void* __restrict__ z, ui
 // chunk, the gate's F and then the other's.  dz may be z: an element's output
 // depends on its own row's pair and dy alone and is stored by the lane that owns
 // them after their load; what a moved-back vector or a chunk's last rows read
-// besides may be new already, and is not used.
+// besides may be new already, and is not used.  Bound by HBM: [8192, 2 x 11008] bf16
+// 168.6 us (902 MB, 5.35 TB/s) and 10.4 us for the sums of the chunks' partials.
 template <int FT>
 __global__ __launch_bounds__(256) void k_gate_bwd(const void* dy, const void* z, int64_t M, int64_t F, int64_t chunk,
                                                   int act, void* dz, float* __restrict__ part, int64_t ldp)
@@ -412,8 +421,9 @@ __global__ __launch_bounds__(256) void k_gate_bwd_thin(const void* dy, const voi
 
 // ---------------------------------------------------------------- launches
 // Rows per chunk of the backward pass: whole rounds of the four waves' two rows,
-// in about GATE_GROUPS workgroups over the slabs of 512 features; up to GATE_ONE rows
-// are one chunk, whose sums are dbias itself: one launch.
+// in about GATE_GROUPS workgroups over the slabs of 512 features ([8192, 2 x 11008]:
+// 4096 178.0 us, 8192 179.5, 16384 179.6); up to GATE_ONE rows are one chunk, whose sums
+// are dbias itself: one launch.
 constexpr int64_t GATE_GROUPS = 8192;
 constexpr int64_t GATE_ONE = 64;
 inline int64_t gate_chunk(int64_t M, int64_t F)

@@ -151,7 +151,7 @@ __device__ __forceinline__ void row_out(const Policy& p, int64_t row, int tok, f
     }
 }
 
-// k_logp_rows: a workgroup per row.
+// k_logp_rows: a workgroup per row.  512 x 32000 binary32 13.3 us (65.5 MB, 4.9 TB/s).
 template <int FT, int NT>
 __global__ __launch_bounds__(NT) void k_logp_rows(const void* __restrict__ z, int64_t ldz, int V, Tokens tok, Policy p,
                                                   float s, float c, float* __restrict__ loss, float* __restrict__ logp,
@@ -172,7 +172,8 @@ __global__ __launch_bounds__(NT) void k_logp_rows(const void* __restrict__ z, in
 // k_logp_parts: a workgroup per row and part of it (`len` columns), whose sum it
 // leaves, and the logit at the row's token where that lies in it (for whoever writes
 // the loss when the gradient may have overwritten the logits).  k_logp_join: a wave
-// per row joins its parts.
+// per row joins its parts.  64 x 131072 bf16 6.9 and 3.0 us, 9 x 131001 f16 3.8: some 2-3
+// us of each are a launch's beginning and end, which so few rows do not cover.
 template <int FT>
 __global__ __launch_bounds__(256) void k_logp_parts(const void* __restrict__ z, int64_t ldz, int V, int parts, int len,
                                                     Tokens tok, float c, Sum* __restrict__ part,
@@ -224,7 +225,7 @@ __device__ __forceinline__ Grad grad_of(float slope, float g, float s, float S)
 
 // k_logp_grad: a workgroup per row and part of it.  FROM_PARTS: the row's sum from
 // its parts, and the row's first workgroup writes loss and log-probability; otherwise
-// from the saved ones.
+// from the saved ones.  512 x 32000 binary32 21.2 us (131 MB, 6.2 TB/s).
 template <int FT, bool FROM_PARTS>
 __global__ __launch_bounds__(256) void k_logp_grad(const void* z, int64_t ldz, int V, int parts, int len, Tokens tok,
                                                    Policy p, float s, float c, const Sum* __restrict__ part,
@@ -304,7 +305,9 @@ __global__ __launch_bounds__(256) void k_logp_grad(const void* z, int64_t ldz, i
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's gradient is
 // computed its registers take the next row's vector, so that the reads go on under the
 // gradient's arithmetic and stores.  Rows whose token counts nowhere are not read.
-// Loads and stores are non-temporal: a row is not met again.
+// Loads and stores are non-temporal: a row is not met again.  4096 x 131072 bf16 410 us
+// (2148 MB, 5.2 TB/s, a large copy 5.0; a pass for the sums and one for the gradient
+// would read 1074 MB more).
 template <int FT, int NT, int W>
 __global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_policy_held(
     const void* z, int64_t ldz, uint32_t rows, int V, Tokens tok, Policy p, float s, float c,
