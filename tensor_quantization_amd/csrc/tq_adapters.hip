@@ -175,7 +175,9 @@ __device__ __forceinline__ float low_dot(const void* x, int64_t xr, const void* 
 }
 
 // k_low_few: h of a few tokens in binary32; two waves per token and rank.  Bound by
-// the latency of its few loads: 1 x 4096, rank 16 3.9 us, 48 x 11008 7.1.
+// the latency of its few loads: 1 x 4096, rank 16 3.9 us, 48 x 11008 7.1.  Four waves per
+// token and rank: no faster for few of them, the call of 128 x 4096 x 4096, rank 64, 45 us
+// instead of 35.
 template <int AT>
 __global__ __launch_bounds__(512) void k_low_few(const void* __restrict__ x, int64_t ldx, int K, Adapters ad)
 {
