@@ -90,10 +90,10 @@ __global__ __launch_bounds__(64 * NWV) void k_gate_few(const int8_t* __restrict_
 // once (rows 16 features apart beyond theirs, which meets all banks).  For that a tile's
 // weight rows are 16 of the gate and 16 of the other in turn (tile_row), and nothing
 // else differs from the plain product with 2 F columns: 8192 x 11008 x 4096 bf16 590-621
-// us (2 x 8192 x 22016 x 4096 operations at 2420-2500 TOP/s; matrix cores busy 61%,
-// 722 MB read for 124 MB of codes, most of it from the last cache), 777 x 4096 x 4096
+// us (2 x 8192 x 22016 x 4096 operations at 2380-2500 TOP/s; matrix cores busy 61%,
+// 1444 MB read past the L2s for 124 MB of codes), 777 x 4096 x 4096
 // f16 35 us: 448 tiles of 128 in one round of two to a CU, a seventh of which hold no
-// token.  Any alignment with z kept: 1021 x 2501 x 5003 f32 83 us, 320 tiles for 256
+// token.  Any alignment with z kept: 1021 x 2501 x 5003 f32 80 us, 320 tiles for 256
 // CUs and the loads of k_epi_tile.
 template <int YT, int TILE>
 struct GateStage {
