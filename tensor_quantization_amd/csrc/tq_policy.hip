@@ -298,9 +298,12 @@ __global__ __launch_bounds__(256) void k_logp_grad(const void* z, int64_t ldz, i
 // its first vector instead of the row's, as 2^(z c - mc) with one rounding, mc being
 // m c rounded; whatever meets these sums knows that rounding: the waves are joined by
 // 2^(mc - mc'), the gradient's exponentials take the same mc, and the loss, which needs
-// log2 S relative to m itself, takes m c - mc out again.  Such sums lose nothing unless
-// they overflow or come out below 1/2 (no logit near the row's largest where a wave
-// looks first); then the row is summed again around its own maximum.
+// log2 S relative to m itself, takes m c - mc out again.  A factor 2^(mc - mc') below
+// 2^-126 comes out as 0, which a wave's sum survives only while it is small: one of 2^96
+// or more counts as infinite.  Then the sums lose nothing (a share of 2^-30, one in 2^26 of
+// the row's at most, over sixteen waves) unless they overflow or come out below 1/2 (no logit
+// near the row's largest where a wave looks first); in both cases the row is summed again
+// around its own maximum.
 //
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's gradient is
 // computed its registers take the next row's vector, so that the reads go on under the
@@ -398,7 +401,7 @@ __global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_policy_held
         __syncthreads();                     // the row before is done with `red`
         if (lane == 0) {
             red[0][wave] = m;
-            red[1][wave] = S;
+            red[1][wave] = S < 0x1p96f ? S : __builtin_inff();    // 0 times it is NaN, which is not near
         }
         __syncthreads();
         m = wave_max(lane < NW ? red[0][lane] : -__builtin_inff());
