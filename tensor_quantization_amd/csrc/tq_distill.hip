@@ -620,11 +620,14 @@ __global__ __launch_bounds__(256) void k_distill_grad(const void* z, int64_t ldz
 // rounding, where mc is m c rounded.  That rounding grows with |m| and differs
 // from wave to wave, so whatever meets these sums knows it: the waves are joined
 // by 2^(mc - mc'), the gradient's exponentials take the same mc, and the loss,
-// which needs log2 S relative to m itself, subtracts m c - mc.  Such sums lose
-// nothing unless they overflow (a logit more than 69 / s above m), m c does, or
-// the complement's comes out below its largest term's 1 (no logit above -inf where
-// a wave looks first); then the complement and the entries are each summed again
-// around their own maximum, the products taken after the difference.
+// which needs log2 S relative to m itself, subtracts m c - mc.  A factor
+// 2^(mc - mc') below 2^-126 comes out as 0, which a wave's sum survives only while
+// it is small: one of 2^96 or more counts as infinite.  Then such sums lose nothing
+// (a share of 2^-30, one in 2^26 of the row's at most, over sixteen waves) unless they
+// overflow (a logit more than 66 / s above a wave's m), m c does, or the complement's
+// comes out below its largest term's 1 (no logit above -inf where a wave looks first);
+// then the complement and the entries are each summed again around their own maximum,
+// the products taken after the difference.
 //
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's
 // gradient is computed its registers take the next row's vector, so that the
@@ -758,7 +761,7 @@ __global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_distill_hel
         tsum = wave_sum(tsum);
         if ((t & 63) == 0) {
             red[1][wave] = m;
-            red[2][wave] = S;
+            red[2][wave] = S < 0x1p96f ? S : __builtin_inff();   // 0 times it is NaN, which is not near
             red[3][wave] = R;
             red[4][wave] = tsum;
         }
