@@ -53,17 +53,20 @@ struct Policy {
     float lo, hi, beta;
 };
 
-// The loss of a row's log-probability l, and its slope dL/dl.
+// The loss of a row's log-probability l, and its slope dL/dl.  Where l is -inf, what
+// the other policies say of the token does not matter (but a NaN stays): rho = 0, and d =
+// +inf.
 __device__ __forceinline__ float policy_loss(const Policy& p, int64_t row, float l, float* slope)
 {
-    const float A = p.adv[row];
-    const float rho = p.old ? ex2((l - p.old[row]) * LOG2E) : 1.0f;
+    constexpr float INF = __builtin_inff();
+    const float A = p.adv[row], old = p.old ? p.old[row] : l;
+    const float rho = l == -INF && old == old ? 0.0f : ex2((l - old) * LOG2E);
     const float held = __builtin_fminf(__builtin_fmaxf(rho, 1.0f - p.lo), 1.0f + p.hi);
     const float u = rho * A, v = held * A;
     float loss = u <= v || u != u ? -u : -v, g = u <= v || u != u ? -u : 0.0f;
     if (p.ref) {
-        const float d = p.ref[row] - l, x = expm1f(d);
-        loss += p.beta * (x == __builtin_inff() ? x : x - d);    // a token that cannot be drawn: infinitely far
+        const float ref = p.ref[row], d = l == -INF && ref == ref ? INF : ref - l, x = expm1f(d);
+        loss += p.beta * (x == INF ? x : x - d);
         g -= p.beta * x;
     }
     *slope = g;
