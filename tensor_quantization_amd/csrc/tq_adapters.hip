@@ -381,7 +381,7 @@ __global__ __launch_bounds__(64 * NWV) void k_adapt_few(const int8_t* __restrict
     for (int i = 0; i < PER; ++i) {
         const int64_t m = m0 + t / COLS + i * STEP;
         const int c = mine[i] ? adapter_of(ad, m, e.M) : -1;
-        low[i] = 0.0f;
+        low[i] = -0.0f;                  // added to any value, -0 among them, it changes nothing
         if (c >= 0) low[i] = ad.dt == F32 ? low_output<F32>(ad, m, c, on, e.N)
                              : ad.dt == BF16 ? low_output<BF16>(ad, m, c, on, e.N) : low_output<F16>(ad, m, c, on, e.N);
     }
