@@ -117,10 +117,13 @@ __device__ __forceinline__ void put_low(const Adapters& ad, int64_t m, int step,
         if constexpr (AT == F16) {
             float most = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) most = __builtin_fmaxf(most, __builtin_fabsf(v[k]));
+            for (int k = 0; k < 8; ++k) {        // an infinity needs no room; what is beside it does
+                const float size = __builtin_fabsf(v[k]);
+                most = size < __builtin_inff() ? __builtin_fmaxf(most, size) : most;
+            }
             most = __builtin_fmaxf(most, as_f(dpp<DPP_XOR1>(as_u(most))));
             most = __builtin_fmaxf(most, as_f(dpp<DPP_XOR2>(as_u(most))));
-            const int up = most > 0.0f && most < __builtin_inff() ? __builtin_amdgcn_frexp_expf(most) : 0;
+            const int up = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = __builtin_amdgcn_ldexpf(v[k], -up);
             if (g == 0) ad.up[m * Low<AT>::steps(ad) + step] = up;

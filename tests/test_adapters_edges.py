@@ -1,5 +1,8 @@
 """GPU parity of the W8A8 product beside adapters at the edges of binary32: zeros
-keep their sign for a token without an adapter."""
+keep their sign for a token without an adapter, and an infinite h leaves the others
+their size."""
+import math
+
 import pytest
 import torch
 
@@ -7,6 +10,7 @@ import llm_util as ref
 from test_parity_adapters import operands
 
 pytestmark = pytest.mark.gpu
+INF = math.inf
 
 
 @pytest.fixture(scope="module")
@@ -36,3 +40,28 @@ def test_zeros_keep_their_sign_without_an_adapter(tq, M, out):
         wy, wz = tq.tq_w8a8_linear_epilogue(*dev[1:5], bias=bias, act="none", out_dtype=ref.TORCH[out], preact=True)
         assert bool((wy[0] == 0).all()) and bool(torch.signbit(wy[0]).any())
         assert torch.equal(bits(y[none]), bits(wy[none])) and torch.equal(bits(z[none]), bits(wz[none]))
+
+
+def few_and_tiles(M):
+    return (136 if M < 600 else 1040), 272, 40, 4
+
+
+@pytest.mark.parametrize("M", [3, 40, 300, 700])
+@pytest.mark.parametrize("ft", ["bf16", "f16", "f32"])
+def test_a_large_h_beside_an_infinite_one(tq, M, ft):
+    """A rank of a is infinite, another one's h is finite but beyond f16's range and
+    against it: the infinity stands."""
+    N, K, R, count = few_and_tiles(M)
+    ops = list(operands(M, N, K, R, count, M, ft, "f32"))
+    ops[0], ops[5] = 1 + ops[0].abs(), torch.arange(M, dtype=torch.int32) % count
+    a, b = ops[6], ops[7]
+    a[1] = a[1].abs() + 1
+    a[1, 3] = 300.0                                      # h = 300 K times x of at least 1: above 81600
+    a[1, 2, 11] = INF
+    b[1] = b[1].abs() + 0.25
+    b[1, :, 3] *= -1
+    dev = [t.cuda() for t in ops]
+    y = tq.tq_w8a8_linear_adapters(*dev[:8], scale=dev[8], out_dtype=torch.float32)
+    mine = dev[5] == 1
+    assert bool((y[mine] == INF).all()), y[mine]
+    assert bool(torch.isfinite(y[~mine]).all())
