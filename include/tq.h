@@ -732,8 +732,9 @@ tq_status tq_gated_act_backward(const void* dy, const void* z, int dtype, int64_
  * rank] have x_dtype; scale [adapters] (binary32) may be NULL: ones.  qx and sx are
  * x's codes and their scales, and everything else is as in tq_w8a8_linear_epilogue,
  * whose bits a token without an adapter gets.  Tokens may come in any order;
- * what one adapter holds (infinities, NaN) does not reach another's tokens.  The
- * products with a and b are summed in binary32, h is not rounded below 16 bits.
+ * what one adapter holds (infinities, NaN) does not reach another's tokens, and an
+ * infinite b gives its own an infinity where h, as it is held, is not 0, and NaN where it
+ * is.  The products with a and b are summed in binary32, h is not rounded below 16 bits.
  * rank from 1 to 256 (TQ_ERR_UNSUPPORTED beyond; adapters of lower rank are
  * padded with zeros), M, N and K as in tq_w8a8_linear_epilogue.  `workspace`:
  * tq_w8a8_linear_adapters_workspace_bytes(M, rank) bytes, 16-byte aligned, contents

@@ -16,8 +16,10 @@
 //
 // The tokens of one sixteen-row operand may have several adapters.  Each takes its
 // turn, the other tokens' h cleared, and only its own tokens take the result, so
-// that what another adapter holds (infinities, NaN) does not reach them.  (An infinity in
-// a token's own b is an infinity or NaN in its outputs: the lower operand may be 0.)
+// that what another adapter holds (infinities, NaN) does not reach them.  An infinity in
+// a token's own b makes NaN where it meets hi and lo apart, one of which may be 0 or of the
+// other sign; outputs that are NaN are therefore looked at once more on their way out
+// (which costs the call 0.2 to 1.5%; b looked through as it is loaded, 2 to 6%).
 #include "tq_product.h"
 
 namespace tq {
@@ -45,6 +47,15 @@ struct Low {
     static __device__ __forceinline__ uint4* piece(const Adapters& ad, int64_t tile, int step)
     {
         return static_cast<uint4*>(ad.h) + (tile * steps(ad) + step) * (64 * PIECES);
+    }
+    // h of token m and rank r.
+    static __device__ __forceinline__ float value(const Adapters& ad, int64_t m, int r)
+    {
+        const uint4* p = piece(ad, m / 16, r / STEP) + 16 * (r % STEP / E) + m % 16;
+        float h = load1<AT>(p, r % E);
+        if constexpr (PIECES > 1) h += load1<AT>(p + 64, r % E);
+        if constexpr (AT == F16) h = __builtin_amdgcn_ldexpf(h, ad.up[m * steps(ad) + r / STEP]);
+        return h;
     }
 };
 
@@ -536,13 +547,43 @@ struct AdaptPart {
         fetch();
     }
 
+    // Eight columns of a row, some of them NaN: a sum over the ranks that is infinite with h
+    // in one piece stands.
+    __device__ __forceinline__ void infinite_sums(int row, int col, int n, int* at) const
+    {
+        constexpr float INF = __builtin_inff();
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, ++col, ++at) {
+            if (as_f((uint32_t)*at) == as_f((uint32_t)*at)) continue;
+            float s = 0.0f;
+#pragma unroll 1
+            for (int r = 0; r < ad.R && s == s; ++r) {
+                // from the start each time: a held address costs the common path its registers
+                const int m = afresh(row), c = adapter_of(ad, m, e.M);
+                if (c >= 0) s += Low<AT>::value(ad, m, r) * load1<AT>(ad.b, ((int64_t)c * e.N + afresh(col)) * ad.R + r);
+            }
+            if (__builtin_fabsf(s) == INF && __builtin_fabsf(e.sx[row] * e.sw[col]) < INF)
+                *at = (int)as_u(s + load1_rt(e.bias, e.bias_dt, col, 0.0f));
+        }
+    }
+
     // Eight columns of a row on their way out.
     template <bool NTS>
-    __device__ __forceinline__ void leave(const Cols8& cc, int64_t row, const int* from) const
+    __device__ __forceinline__ void leave(const Cols8& cc, int64_t row, int* from) const
     {
         Raw8<YT> res = {};
         if (YT != F32 && e.res) res = residual8<YT>(e, cc, row);
-        const v4f s0 = *reinterpret_cast<const v4f*>(from), s1 = *reinterpret_cast<const v4f*>(from + 4);
+        v4f s0 = *reinterpret_cast<const v4f*>(from), s1 = *reinterpret_cast<const v4f*>(from + 4);
+        if constexpr (PIECES > 1) {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nan |= __builtin_isunordered(s0[i], s1[i]);
+            if (__builtin_expect(nan, 0)) {
+                infinite_sums((int)row, (int)cc.col, cc.n, from);
+                s0 = *reinterpret_cast<const v4f*>(from);
+                s1 = *reinterpret_cast<const v4f*>(from + 4);
+            }
+        }
         float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
         const int64_t at = row * e.N + cc.col;
         if (e.z) store8_first<YT>(e.z, at, cc.n, v);
