@@ -764,7 +764,8 @@ tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stri
  * -inf are tokens that cannot be drawn; one that was drawn all the same has l =
  * -inf, rho = 0, gradient 0, and with a KL term the loss +inf and a gradient that is not
  * finite, whatever old_logp and ref_logp say of it (-inf too; a NaN there stays).  A row
- * of nothing but -inf has l = -inf and gradient 0.
+ * of nothing but -inf has l = -inf and gradient 0.  With advantage 0 the clipped term is 0
+ * also where rho overflows.
  *
  * tq_token_logp writes logp and, if not NULL, stats [rows, 2] = the row's largest
  * logit and the sum of exp(s (z - it)) (-inf and 0 for a row that counts nowhere);

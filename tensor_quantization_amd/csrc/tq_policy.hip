@@ -62,7 +62,7 @@ __device__ __forceinline__ float policy_loss(const Policy& p, int64_t row, float
     const float A = p.adv[row], old = p.old ? p.old[row] : l;
     const float rho = l == -INF && old == old ? 0.0f : ex2((l - old) * LOG2E);
     const float held = __builtin_fminf(__builtin_fmaxf(rho, 1.0f - p.lo), 1.0f + p.hi);
-    const float u = rho * A, v = held * A;
+    const float u = A == 0.0f && rho == INF ? A : rho * A, v = held * A;     // no advantage, however far rho overflows
     float loss = u <= v || u != u ? -u : -v, g = u <= v || u != u ? -u : 0.0f;
     if (p.ref) {
         const float ref = p.ref[row], d = l == -INF && ref == ref ? INF : ref - l, x = expm1f(d);
