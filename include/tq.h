@@ -760,8 +760,8 @@ tq_status tq_w8a8_linear_adapters(const void* x, int x_dtype, int64_t x_row_stri
  *   dloss/dl = (rho A <= clip(rho) A ? -rho A : 0) + kl_coef (1 - exp(d))
  *   dlogits_j = dloss (dloss/dl) s (1[j = y] - q_j)
  * advantage, old_logp and ref_logp are binary32 [rows]; gradients do not go through
- * them.  clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, temperature > 0.  Logits of
- * -inf are tokens that cannot be drawn; one that was drawn all the same has l =
+ * them.  clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, temperature from 1e-38 (whose
+ * inverse binary32 still holds) to 3e38.  Logits of -inf are tokens that cannot be drawn; one that was drawn all the same has l =
  * -inf, rho = 0, gradient 0, and with a KL term the loss +inf and a gradient that is not
  * finite, whatever old_logp and ref_logp say of it (-inf too; a NaN there stays).  A row
  * of nothing but -inf has l = -inf and gradient 0.  With advantage 0 the clipped term is 0

@@ -614,7 +614,7 @@ static tq_status logp_check(const void* logits, int dt, int64_t rows, int64_t vo
 {
     *work = false;
     if (!valid_ftype(dt) || (idx_bits != 32 && idx_bits != 64) || rows < 0 || vocab < 0) return TQ_ERR_INVALID;
-    if (!(temperature > 0.0f) || temperature > 3.0e38f) return TQ_ERR_INVALID;
+    if (!(temperature >= 1e-38f) || temperature > 3.0e38f) return TQ_ERR_INVALID;    // s and c are finite
     if (rows == 0) return TQ_OK;
     if (vocab == 0 || !logits || ldz < vocab || !token) return TQ_ERR_INVALID;
     if (vocab > 0x7fffff00 || rows > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
