@@ -657,7 +657,8 @@ tq_status tq_linear_epilogue_backward(const void* dy, const void* preact, int dt
  * drawn (gradient 0; the loss is +inf where the teacher gives them mass); a row
  * of nothing but -inf has gradient 0 and, if it has entries, loss +inf.
  * Entries that repeat a column count each, and its gradient takes their sum.
- * loss [rows]; no reduction and no factor T^2 are applied.  temperature > 0.
+ * loss [rows]; no reduction and no factor T^2 are applied.  temperature from 1e-38
+ * (whose inverse binary32 still holds) to 3e38.
  *
  * tq_topk_distill writes the loss and what the backward pass needs: stats
  * [rows, 2] = the row's largest logit and the sum of exp(s (z - it)), rest_sum

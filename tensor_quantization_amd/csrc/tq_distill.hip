@@ -1041,7 +1041,7 @@ static tq_status distill_check(const void* logits, int dt, int64_t rows, int64_t
     *work = false;
     if (!valid_ftype(dt) || !valid_ftype(val_dt) || (idx_bits != 32 && idx_bits != 64)) return TQ_ERR_INVALID;
     if (rows < 0 || vocab < 0 || K < 1) return TQ_ERR_INVALID;
-    if (!(temperature > 0.0f) || temperature > 3.0e38f) return TQ_ERR_INVALID;
+    if (!(temperature >= 1e-38f) || temperature > 3.0e38f) return TQ_ERR_INVALID;    // s and c are finite
     if (rows == 0) return TQ_OK;
     if (vocab == 0 || !logits || ldz < vocab || !idx || !val) return TQ_ERR_INVALID;
     if (K > DT_K || vocab > 0x7fffff00 || rows > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
