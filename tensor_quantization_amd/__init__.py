@@ -1154,7 +1154,8 @@ def tq_w8a8_linear_adapters(x, qx, sx, qw, sw, adapter, a, b, scale=None, bias=N
     the shared product runs on x's s8 codes qx [M, K] (per-row scales sx) and the
     weight's qw [N, K] (per-channel scales sw).  a [adapters, rank, K] and b
     [adapters, N, rank] have x's type; with ``preact`` also the value before the
-    activation."""
+    activation.  Beyond some hundred tokens those of one adapter should stand
+    together: neighbours' different adapters are taken one after another."""
     qx, qw = _codes(qx, "qx"), _codes(qw, "qw")
     M, K = qx.shape
     N, kw = qw.shape

@@ -242,7 +242,9 @@ __global__ __launch_bounds__(1024) void k_low_tokens(const void* __restrict__ x,
 // of a small output.  4096 x 4096, rank 64, f16 23 us, bound by what one workgroup per CU
 // has in flight: 650 KB of x and a pass through every CU at 12 bytes per clock, 43 MB of
 // them from HBM.  Sixteen waves for 64 ranks cost 14 us more, two groups in flight per
-// wave 7 (their registers spill); K split over workgroups was no faster.
+// wave 7 (their registers spill); K split over workgroups was no faster.  Every further
+// adapter among the 16 tokens is another pass over K: with 48 adapters in turn 152 us, and
+// the product beside them, whose 32 tokens take theirs in turn too, 451 instead of 80.
 template <int AT, int RT, int NWV, bool ORDER>
 __global__ __launch_bounds__(64 * NWV) void k_low_many(const void* __restrict__ x, int64_t ldx, int64_t M, int K,
                                                        Adapters ad)
@@ -699,6 +701,7 @@ struct AdaptTile : Epi {
 //   48 x 11008, rank 16  16 / 70 | 16 / 38      512 x 4096, rank 16  20 / 33 | 20 / 16
 //   128 x 4096, rank 64  20 / 76 | 20 / 18     1024 x 4096, rank 16  32 / 41 | 32 / 16
 //   200 x 4096, rank 64  26 / 74 | 26 / 26      512 x 4096, rank 64  52 / 74 | 52 / 19
+// (the last goes by tile, for batches whose tokens of one adapter stand together).
 constexpr int64_t LOW_FEW = 8192;
 inline bool low_by_token(int64_t M, int64_t rank) { return M * rank <= (M <= 256 ? 2 : 1) * LOW_FEW; }
 
@@ -708,6 +711,8 @@ inline bool low_by_token(int64_t M, int64_t rank) { return M * rank <= (M <= 256
 // adapter of its own | all with one:
 //   100 x 4096 x 11008   36 / 66 | 33 / 35     128 x 4096 x 4096   21 / 45 | 19.5 / 18
 //   64 x 11008 x 4096    30 / 51 | 26 / 19     200 x 4096 x 4096   35 / 47 | 32.5 / 18
+// (the last two go to the tiles: what tokens with an adapter each lose there, tokens that
+// share one gain).
 inline bool adapt_few(int64_t M, int64_t N, int64_t rank)
 {
     return few_tokens(M, N) || (M * rank <= LOW_FEW && cdiv(M, 32) * cdiv(N, 32) <= 512);

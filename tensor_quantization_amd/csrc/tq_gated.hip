@@ -91,8 +91,8 @@ __global__ __launch_bounds__(64 * NWV) void k_gate_few(const int8_t* __restrict_
 // weight rows are 16 of the gate and 16 of the other in turn (tile_row), and nothing
 // else differs from the plain product with 2 F columns: 8192 x 11008 x 4096 bf16 590-621
 // us (2 x 8192 x 22016 x 4096 operations at 2380-2500 TOP/s; matrix cores busy 61%,
-// 1444 MB read past the L2s for 124 MB of codes), 777 x 4096 x 4096
-// f16 35 us: 448 tiles of 128 in one round of two to a CU, a seventh of which hold no
+// 1444 MB read past the L2s for 124 MB of codes), 694 with z kept (361 MB more to
+// write, 72 us at a large copy's rate), 777 x 4096 x 4096 f16 36 us: 448 tiles of 128 in one round of two to a CU, a seventh of which hold no
 // token.  Any alignment with z kept: 1021 x 2501 x 5003 f32 80 us, 320 tiles for 256
 // CUs and the loads of k_epi_tile.
 template <int YT, int TILE>
@@ -273,7 +273,7 @@ __device__ __forceinline__ void act_slope8(int act, const float g[8], float a[8]
 }
 
 // k_gate_act: a thread per eight features of a row (F >= 8), or per feature.  Bound by
-// HBM: [8192, 2 x 11008] bf16 92.5 us (541 MB, 5.85 TB/s).
+// HBM: [8192, 2 x 11008] bf16 93.1 us (541 MB, 5.8 TB/s).
 template <int FT>
 __global__ __launch_bounds__(256) void k_gate_act(const void* __restrict__ z, uint32_t M, int64_t F, uint32_t per,
                                                   int act, void* __restrict__ y)

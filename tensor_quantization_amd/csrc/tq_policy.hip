@@ -310,7 +310,8 @@ __global__ __launch_bounds__(256) void k_logp_grad(const void* z, int64_t ldz, i
 //
 // A workgroup walks the rows blockIdx + k gridDim: as soon as a vector's gradient is
 // computed its registers take the next row's vector, so that the reads go on under the
-// gradient's arithmetic and stores.  Rows whose token counts nowhere are not read.
+// gradient's arithmetic and stores.  Of a row whose token counts nowhere one address is
+// read, and not used.
 // Loads and stores are non-temporal: a row is not met again.  4096 x 131072 bf16 410 us
 // (2148 MB, 5.2 TB/s, a large copy 5.0; a pass for the sums and one for the gradient
 // would read 1074 MB more).
@@ -342,7 +343,7 @@ __global__ __launch_bounds__(NT, FT != F32 && W == 4 ? 8 : 1) void k_policy_held
         const int ynext = more ? token_of(tok, row + step, V) : -1;
         // vector w of the next row
         auto ahead = [&](int w) { raw[w] = load8_off<FT, true>(next, at_of(afresh(afresh(t) + w * NT), ynext >= 0)); };
-        if (y < 0) {                     // uniform: nothing was read of this row
+        if (y < 0) {                     // uniform: nothing of this row is used
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 ahead(w);
@@ -482,10 +483,16 @@ inline Split logp_split(int64_t rows, int64_t V)
 
 // Whether a workgroup takes a whole row forwards, in one launch: from LP_ROWS rows on,
 // and where a row is so short (LP_BYTES) that the second launch costs more than its
-// reading by one CU.  Whole rows / parts and their join, one call after another, us, bf16:
-//   64 x 32000   11.5 / 14.6     64 x 131072   13.3 / 14.6 (kernels 12 / 6.9 + 3.0)
-//   256 x 32000  11.5 / 14.5     256 x 131072  15.5 / 17.7
-//   2048 x 32000 30.5 / 33.2     512 x 131072  30.2 / 30.0
+// reading by one CU.  Longer rows go by what the GPU takes in a replayed graph, where no host
+// stands between the launches.  Whole rows / parts and their join, us, bf16, called one after
+// another and, where two pairs are given, replayed:
+//   64 x 32000   11.5 / 14.6     16 x 131072   12.0 / 14.0, 11.4 / 6.1
+//   256 x 32000  11.5 / 14.5     64 x 131072   12.8 / 13.7, 12.7 / 9.1
+//   2048 x 32000 30.5 / 33.2     128 x 131072  13.2 / 13.9, 12.9 / 12.0
+//   64 x 66000   10.8 / 13.9, 8.0 / 7.5     192 x 131072  13.6 / 15.0, 13.4 / 14.6
+//   64 x 100000  11.0 / 14.2, 10.6 / 8.4    255 x 131072  14.5 / 17.4, 14.5 / 17.4
+//                                           512 x 131072  30.2 / 30.0
+// (between some 150 and LP_ROWS long rows whole ones would be faster by up to a sixth).
 constexpr int64_t LP_ROWS = 256, LP_BYTES = 131072;
 inline bool whole_rows(int64_t rows, int64_t V, int FT) { return rows >= LP_ROWS || V * ftype_size(FT) <= LP_BYTES; }
 constexpr int64_t LP_NO_WORKSPACE = 8192;    // whole rows forwards and held in one call, in every type
