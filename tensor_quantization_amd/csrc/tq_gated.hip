@@ -92,9 +92,9 @@ __global__ __launch_bounds__(64 * NWV) void k_gate_few(const int8_t* __restrict_
 // else differs from the plain product with 2 F columns: 8192 x 11008 x 4096 bf16 590-621
 // us (2 x 8192 x 22016 x 4096 operations at 2380-2500 TOP/s; matrix cores busy 61%,
 // 1444 MB read past the L2s for 124 MB of codes), 694 with z kept (361 MB more to
-// write, 72 us at a large copy's rate), 777 x 4096 x 4096 f16 36 us: 448 tiles of 128 in one round of two to a CU, a seventh of which hold no
-// token.  Any alignment with z kept: 1021 x 2501 x 5003 f32 80 us, 320 tiles for 256
-// CUs and the loads of k_epi_tile.
+// write, 72 us at a large copy's rate), 777 x 4096 x 4096 f16 36 us: 448 tiles of 128
+// in one round of two to a CU, a seventh of which hold no token.  Any alignment with z
+// kept: 1021 x 2501 x 5003 f32 80 us, 320 tiles for 256 CUs and the loads of k_epi_tile.
 template <int YT, int TILE>
 struct GateStage {
     static constexpr int ES = YT == F32 ? 4 : 2, PITCH = (TILE / 2 + 16) * ES, BYTES = TILE * PITCH;
